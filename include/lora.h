@@ -60,6 +60,9 @@ extern "C" {
 #define LORA_F32 0
 #define LORA_BF16 1
 
+/* 4-bit weights (MXFP4): a form of lora_moe_experts' weights, not of a pool */
+#define LORA_MX4 2
+
 /* rows per work item of the plan (one 16-row matrix-core tile) */
 #define LORA_PLAN_ROWS 16
 
@@ -386,9 +389,130 @@ int lora_linear_noalloc(const lora_pool* pool, const void* x, const void* W, con
                         void* stream);
 
 /*
+ * MXFP4 rows (OCP Microscaling Formats 1.0): 32 consecutive values of a row
+ * share a scale 2^(b - 127), b one byte (255: not a number), and each is an
+ * E2M1 code: 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a sign. A matrix of
+ * `rows` x K is held as
+ *   codes   dev bytes [rows][lora_mx4_row_bytes(K)], two codes a byte, the
+ *           earlier value in the low four bits; a row is whole blocks of 32
+ *           (16 bytes), the codes past K being 0
+ *   scales  dev bytes [lora_mx4_scale_bytes(rows, K)], the scale bytes in the
+ *           order in which the products read them: tiles of 64 rows x 8
+ *           blocks, 512 bytes each, row groups first; in a tile, row r and
+ *           block b at 4 (2 (16 (b % 4) + r % 16) + b / 4) + r / 16; zero
+ *           past the matrix
+ * and `batch` matrices follow one another. Codes start on 16-byte, scales on
+ * 8-byte boundaries. lora_mx4_row_bytes and lora_mx4_scale_bytes return 0
+ * for sizes below 1; rows is at most LORA_MX4_MAX_ROWS, batch 65535.
+ *
+ * lora_mx4_quantize takes, per block, b - 127 = floor(log2(max |v|)) - 2 (not
+ * below -127) and rounds v / 2^(b - 127) to the nearest code, ties to the
+ * even mantissa, at most 6: the conversion of the format's specification. A
+ * block that holds an infinity or a NaN gets b = 255 and zero codes.
+ *   src   dev [batch][rows][K], LORA_F32 or LORA_BF16
+ * lora_mx4_dequantize writes the values back in fp32 or bf16 (exact, except
+ * where a scale under 2^-125 or over 2^125 leaves the type's range);
+ * lora_mx4_pack_scales lays out scale bytes in row order, dev
+ * [batch][rows][ceil(K / 32)], as a checkpoint holds them (the codes of such
+ * a checkpoint are already in this form).
+ * All three are asynchronous on `stream`. Errors: LORA_EINVAL (sizes, null
+ * or misaligned pointers, unknown dtype), LORA_EHIP. With rows or batch 0
+ * they return LORA_OK and launch nothing.
+ */
+#define LORA_MX4_MAX_ROWS 4194240
+size_t lora_mx4_row_bytes(int K);
+size_t lora_mx4_scale_bytes(int rows, int K);
+int lora_mx4_quantize(int dtype, const void* src, int batch, int rows, int K, void* codes, void* scales,
+                      void* stream);
+int lora_mx4_dequantize(const void* codes, const void* scales, int batch, int rows, int K, int dtype, void* dst,
+                        void* stream);
+int lora_mx4_pack_scales(const void* e8m0, int batch, int rows, int K, void* scales, void* stream);
+
+/*
+ * lora_linear over a base weight held in 4 bits:
+ *   y[t] = round(act(x[t]) What^T + (alpha_s / r_s) (x[t] A_s^T) B_s^T)
+ *   codes, scales  an MXFP4 matrix of d_out x d_in (What its values)
+ *   act            LORA_BF16: act(x) = x (16-bit activations);
+ *                  LORA_MX4: act(x) = each row of x rounded to MXFP4 by
+ *                  lora_mx4_quantize's rule, the base product on the scaled
+ *                  4-bit matrix instruction
+ * The adapter correction reads x itself in both forms. Sums are fp32, y is
+ * rounded once. bf16 pools only, of any d_in (rows of x, and the pool's A,
+ * are copied to padded rows in the workspace when d_in is not a multiple of
+ * 8; otherwise x must start on a 16-byte boundary). Every other argument,
+ * rows without an adapter, empty batches and errors are lora_linear's;
+ * LORA_EINVAL also for an fp32 pool, another act and misaligned pointers.
+ *   workspace      dev, at least lora_workspace_bytes_mx4(pool, T, act) bytes
+ *                  (0 for arguments without a result)
+ */
+size_t lora_workspace_bytes_mx4(const lora_pool* pool, int T, int act);
+int lora_linear_mx4(const lora_pool* pool, const void* x, const void* codes, const void* scales, int act,
+                    const int32_t* token_order, const int32_t* slot_indptr, const int32_t* work,
+                    const lora_plan_info* info, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* lora_linear_mx4 over a device plan from lora_plan_device, as
+ * lora_linear_device_plan is to lora_linear. */
+int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void* codes, const void* scales, int act,
+                                const int32_t* plan, int T, void* y, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens (at most LORA_MOE_MAX_PAIRS
+ * token and choice pairs), in two calls.
+ *
+ * lora_moe_route: logits = x R^T, summed in 64 bits; ids[t][0..k) the k
+ * experts of the largest logits, in falling order, equal logits to the lower
+ * index; weights[t][j] = exp(logit_j - max) over the sum of the same over the
+ * k chosen (renorm != 0) or over all E experts (renorm == 0), in fp32.
+ *   x        dev bf16 [T][H]
+ *   router   dev bf16 [E][H]
+ *   ids      dev int32 [T][k] out;  weights  dev float [T][k] out
+ *   workspace dev, at least lora_moe_route_workspace_bytes(T, E) bytes
+ * A NaN logit ranks below every number; ids stay valid and distinct, and the
+ * weights of that token are NaN.
+ *
+ * lora_moe_experts:
+ *   y[t] = round(sum_j weights[t][j] down_e(silu(gate_e x[t]) * up_e x[t])),
+ *   e = ids[t][j]
+ *   form     LORA_BF16: gate, up dev bf16 [E][I][H], down dev bf16 [E][H][I],
+ *            scale pointers ignored; LORA_MX4: the same shapes as batches of E
+ *            MXFP4 matrices
+ *   ids, weights  as lora_moe_route writes them, or the caller's own; a
+ *            choice whose id is outside [0, E) adds nothing, and a token may
+ *            name an expert twice
+ *   y        dev bf16 [T][H] out, overwritten completely; must not alias x
+ *   workspace dev, at least lora_moe_experts_workspace_bytes(T, I, k) bytes
+ * The terms of a token are added in the order of j: equal inputs give equal
+ * bits. Products take bf16 operands with fp32 sums; the inner values
+ * silu(.) * (.) are carried as two bf16 halves (16 bits of mantissa).
+ *
+ * H must be a multiple of 8, and I too for LORA_BF16; x, router and the
+ * weights start on 16-byte boundaries; 1 <= E <= LORA_MOE_MAX_EXPERTS,
+ * 1 <= k <= min(E, LORA_MOE_MAX_K) (lora_moe_experts: k may exceed E),
+ * T k <= LORA_MOE_MAX_PAIRS. Asynchronous on `stream`. Errors: LORA_EINVAL,
+ * LORA_ESPACE, LORA_EHIP. T == 0 launches nothing.
+ */
+#define LORA_MOE_MAX_EXPERTS 512
+#define LORA_MOE_MAX_K 16
+#define LORA_MOE_MAX_PAIRS 512
+size_t lora_moe_route_workspace_bytes(int T, int E);
+int lora_moe_route(const void* x, const void* router, int T, int H, int E, int k, int renorm, int32_t* ids,
+                   float* weights, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct lora_moe_weights {
+    const void *gate, *up, *down;                      /* bf16 values or MXFP4 codes */
+    const void *gate_scales, *up_scales, *down_scales; /* LORA_MX4 only */
+} lora_moe_weights;
+
+size_t lora_moe_experts_workspace_bytes(int T, int I, int k);
+int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* weights, const lora_moe_weights* w,
+                     int T, int H, int I, int E, int k, void* y, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
  * Per-kernel timing, for diagnostics and the benchmark's roofline figures.
  * Between lora_profile_begin and lora_profile_end, lora_linear,
- * lora_linear_multi and lora_shrink record a HIP event pair around every
+ * lora_linear_multi, lora_shrink, lora_linear_mx4 and lora_moe_* record a HIP event pair around every
  * kernel they launch, on the stream it is launched on (not while that stream
  * is being captured into a graph, and at most max_records kernels).
  * lora_profile_end waits for the recorded events and writes one entry per

@@ -13,6 +13,7 @@
 
 #include "../../include/lora.h"
 #include "kernels.h"
+#include "mx4_format.h"
 
 struct lora_pool {
     int S, r_max, d_in, d_out, dtype;
@@ -160,6 +161,25 @@ int check_plan(const lora_pool* p, const int32_t* token_order, const int32_t* sl
     if (info->T > 0 && (!token_order || !slot_indptr)) return LORA_EINVAL;
     if (info->n_items > 0 && !work) return LORA_EINVAL;
     return LORA_OK;
+}
+
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Sizes of an MXFP4 batch the kernels' grids take.
+inline bool mx4_sizes(int batch, int rows, int K) {
+    return batch >= 0 && batch <= 65535 && rows >= 0 && rows <= LORA_MX4_MAX_ROWS && K >= 1;
+}
+inline bool mx4_buffers(const void* codes, const void* scales) {
+    return codes && scales && aligned(codes, 16) && aligned(scales, 8);
+}
+
+static_assert(LORA_MOE_MAX_EXPERTS == lora::kMoeMaxExperts && LORA_MOE_MAX_K == lora::kMoeMaxK &&
+                  LORA_MOE_MAX_PAIRS == lora::kMoeMaxPairs,
+              "mixture-of-experts limits of the interface and the kernels");
+
+inline bool moe_sizes(int T, int H, int E, int k) {
+    return T >= 0 && H >= 1 && H % 8 == 0 && E >= 1 && E <= LORA_MOE_MAX_EXPERTS && k >= 1 && k <= LORA_MOE_MAX_K &&
+           T <= LORA_MOE_MAX_PAIRS / k;
 }
 
 }  // namespace
@@ -537,6 +557,151 @@ int lora_delta_bgmv(const lora_pool* p, const void* x, const int32_t* slot_ids, 
                             p->d_out, p->d_in, p->r_max, st, tm) == hipSuccess
                ? LORA_OK
                : LORA_EHIP;
+}
+
+size_t lora_mx4_row_bytes(int K) { return K < 1 ? 0 : (size_t)lora::mx4_row_bytes(K); }
+
+size_t lora_mx4_scale_bytes(int rows, int K) {
+    return K < 1 || rows < 1 ? 0 : (size_t)lora::mx4_scale_bytes(rows, K);
+}
+
+int lora_mx4_quantize(int dtype, const void* src, int batch, int rows, int K, void* codes, void* scales,
+                      void* stream) {
+    if ((dtype != LORA_F32 && dtype != LORA_BF16) || !mx4_sizes(batch, rows, K)) return LORA_EINVAL;
+    if (batch == 0 || rows == 0) return LORA_OK;
+    if (!src || !aligned(src, es_of(dtype)) || !mx4_buffers(codes, scales)) return LORA_EINVAL;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    return lora::mx4_quantize(dtype, src, batch, rows, K, nullptr, (uint8_t*)codes, (uint8_t*)scales, st,
+                              timer_for(st)) == hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+int lora_mx4_dequantize(const void* codes, const void* scales, int batch, int rows, int K, int dtype, void* dst,
+                        void* stream) {
+    if ((dtype != LORA_F32 && dtype != LORA_BF16) || !mx4_sizes(batch, rows, K)) return LORA_EINVAL;
+    if (batch == 0 || rows == 0) return LORA_OK;
+    if (!dst || !aligned(dst, es_of(dtype)) || !mx4_buffers(codes, scales)) return LORA_EINVAL;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    return lora::mx4_dequantize(dtype, (const uint8_t*)codes, (const uint8_t*)scales, batch, rows, K, dst, st,
+                                timer_for(st)) == hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+int lora_mx4_pack_scales(const void* e8m0, int batch, int rows, int K, void* scales, void* stream) {
+    if (!mx4_sizes(batch, rows, K)) return LORA_EINVAL;
+    if (batch == 0 || rows == 0) return LORA_OK;
+    if (!e8m0 || !scales || !aligned(scales, 8)) return LORA_EINVAL;
+    return lora::mx4_pack_scales((const uint8_t*)e8m0, batch, rows, K, (uint8_t*)scales, as_stream(stream)) ==
+                   hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+size_t lora_workspace_bytes_mx4(const lora_pool* p, int T, int act) {
+    if (!p || T < 0 || p->dtype != LORA_BF16 || (act != LORA_BF16 && act != LORA_MX4)) return 0;
+    return lora::mx4_linear_workspace(T, p->d_out, p->d_in, p->S, p->r_max, act == LORA_MX4);
+}
+
+int lora_linear_mx4(const lora_pool* p, const void* x, const void* codes, const void* scales, int act,
+                    const int32_t* token_order, const int32_t* slot_indptr, const int32_t* work,
+                    const lora_plan_info* info, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_plan(p, token_order, slot_indptr, work, info);
+    if (rc != LORA_OK) return rc;
+    if (p->dtype != LORA_BF16 || (act != LORA_BF16 && act != LORA_MX4)) return LORA_EINVAL;
+    const int T = info->T;
+    if (T > LORA_MX4_MAX_ROWS || p->d_out > LORA_MX4_MAX_ROWS) return LORA_EINVAL;
+    if (T == 0) return LORA_OK;
+    if (!x || !y || !mx4_buffers(codes, scales)) return LORA_EINVAL;
+    if (y == x || y == codes || y == scales) return LORA_EINVAL;
+    if (!aligned(x, p->d_in % 8 == 0 ? 16 : 2) || !aligned(y, p->d_out % 8 == 0 ? 16 : 2)) return LORA_EINVAL;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_workspace_bytes_mx4(p, T, act))
+        return LORA_ESPACE;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    lora::LinearArgs la{};
+    la.X = (const uint16_t*)x;
+    la.M = T;
+    la.K = p->d_in;
+    la.token_order = token_order;
+    la.slot_indptr = slot_indptr;
+    la.work = work;
+    la.n_items = info->n_items;
+    la.S = p->S;
+    la.r_max = p->r_max;
+    la.adapters = info->T_a > 0 && info->n_items > 0 ? 1 : 0;
+    la.workspace = workspace;
+    la.n_slices = 1;
+    la.slice[0] = {nullptr, (uint16_t*)y, p->d_out, (const uint16_t*)p->A, (const uint16_t*)p->B, p->rank_dev,
+                   p->scale_dev};
+    return lora::mx4_linear(la, (const uint8_t*)codes, (const uint8_t*)scales, act == LORA_MX4, st, timer_for(st)) ==
+                   hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+int lora_linear_mx4_device_plan(const lora_pool* p, const void* x, const void* codes, const void* scales, int act,
+                                const int32_t* plan, int T, void* y, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (!p || !plan || T < 0 || p->S > LORA_DEVICE_PLAN_MAX_SLOTS) return LORA_EINVAL;
+    const int cap = std::max(lora_plan_max_items(T, p->S), 1);
+    const int32_t* token_order = plan + 4 * (size_t)cap;
+    lora_plan_info info{T, p->S, T, 0, lora_plan_max_items(T, p->S), 0, LORA_PLAN_ROWS};
+    return lora_linear_mx4(p, x, codes, scales, act, token_order, token_order + T, plan, &info, y, workspace,
+                           workspace_bytes, stream);
+}
+
+size_t lora_moe_route_workspace_bytes(int T, int E) { return T < 0 || E < 1 ? 0 : lora::moe_route_workspace(T, E); }
+
+int lora_moe_route(const void* x, const void* router, int T, int H, int E, int k, int renorm, int32_t* ids,
+                   float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!moe_sizes(T, H, E, k) || k > E) return LORA_EINVAL;
+    if (T == 0) return LORA_OK;
+    if (!x || !router || !ids || !weights || !aligned(x, 16) || !aligned(router, 16)) return LORA_EINVAL;
+    if (!workspace || !aligned(workspace, 8) || workspace_bytes < lora_moe_route_workspace_bytes(T, E))
+        return LORA_ESPACE;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    return lora::moe_route((const uint16_t*)x, (const uint16_t*)router, T, H, E, k, renorm, ids, weights, workspace, st,
+                           timer_for(st)) == hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+size_t lora_moe_experts_workspace_bytes(int T, int I, int k) {
+    return T < 0 || I < 1 || k < 1 ? 0 : lora::moe_experts_workspace(T, I, k);
+}
+
+int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* weights, const lora_moe_weights* w,
+                     int T, int H, int I, int E, int k, void* y, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    if ((form != LORA_BF16 && form != LORA_MX4) || !moe_sizes(T, H, E, k) || I < 1 ||
+        I > LORA_MX4_MAX_ROWS || H > LORA_MX4_MAX_ROWS || (form == LORA_BF16 && I % 8 != 0) || !w)
+        return LORA_EINVAL;
+    if (T == 0) return LORA_OK;
+    if (!x || !ids || !weights || !y || y == x || !aligned(x, 16) || !aligned(y, 2)) return LORA_EINVAL;
+    const void* data[3] = {w->gate, w->up, w->down};
+    const void* scales[3] = {w->gate_scales, w->up_scales, w->down_scales};
+    for (int i = 0; i < 3; ++i) {
+        if (!data[i] || !aligned(data[i], 16) || y == data[i]) return LORA_EINVAL;
+        if (form == LORA_MX4 && (!scales[i] || !aligned(scales[i], 8) || y == scales[i])) return LORA_EINVAL;
+    }
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_moe_experts_workspace_bytes(T, I, k))
+        return LORA_ESPACE;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    const lora::MoeArgs a{(const uint16_t*)x, ids, weights, {data[0], (const uint8_t*)scales[0]},
+                          {data[1], (const uint8_t*)scales[1]}, {data[2], (const uint8_t*)scales[2]},
+                          (uint16_t*)y, T, H, I, E, k, workspace};
+    return lora::moe_experts(a, form == LORA_MX4, st, timer_for(st)) == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 
 int lora_profile_begin(int max_records) {

@@ -379,6 +379,13 @@ __device__ __forceinline__ void stage_barrier() {
 // concatenated columns (its n_nt is recomputed per slice).
 hipError_t splitk_forward_bf16(const LinearArgs& L, const GemmPlan& g, hipStream_t st, StageTimer* tm);
 
+// The tiled path's shrink of one slice (into fp32 h [M][r_max] or, with ext,
+// the operand of the expand's extra K steps) and the workspace it needs at ws
+// (h or ext first, then its split planes), defined in gemm_bf16.hip.
+size_t tiled_workspace(int M, int r_max);
+hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext, hipStream_t st,
+                        StageTimer* tm);
+
 // Kernel 2 of the split-K path for one slice whose fp32 partials (ks splits,
 // the 64 x 64 tile layout of kernel 1) were written by another kernel: adds
 // the splits, applies the expand from fp32 h (h_splits planes of [M][r_max],

@@ -513,7 +513,7 @@ static size_t split_workspace(int M, int n_nt_total, const GemmPlan& g, int n_sl
 
 // tiled path: fp32 h [M][r_max] or bf16 hi / lo [M][2][round_up(r_max, 8)],
 // then the K-split shrink's planes (at most kShrinkSplitMaxBlocks x 16 rows)
-static size_t tiled_workspace(int M, int r_max) {
+size_t tiled_workspace(int M, int r_max) {
     const size_t h_final = (size_t)M * ((r_max + 7) & ~7) * sizeof(float);
     const size_t planes = (size_t)kShrinkSplitMaxBlocks * 16 * r_max * sizeof(float);
     return ((h_final + 255) & ~size_t(255)) + planes;
@@ -614,8 +614,8 @@ static hipError_t launch_tile(const uint16_t* X, const uint16_t* W, uint16_t* Y,
 // The shrink of the tiled path, into fp32 h [M][r_max] or, with ext, the
 // expand operand of the extra K steps; ws: h_final bytes for h or ext, then
 // the K-split shrink's planes.
-static hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext,
-                               hipStream_t st, StageTimer* tm) {
+hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext,
+                        hipStream_t st, StageTimer* tm) {
     const int M = L.M, K = L.K;
     // few items over a long K: split K over more workgroups, then add the splits
     int hs = 1, hkc = K;

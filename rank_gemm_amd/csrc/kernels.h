@@ -143,6 +143,45 @@ hipError_t generic_expand(int dtype, const float* h, const void* B_pool, const i
                           const int32_t* token_order, const int32_t* work, int n_items, void* Y, int N, int r_max,
                           hipStream_t st, StageTimer* tm);
 
+// ---- MXFP4 rows (format: mx4_format.h) ----------------------------------------------
+// `batch` matrices of rows x K, one after another; dtype 0 = fp32, 1 = bf16.
+// With order, row r of the result is source row order[r].
+hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows, int64_t K, const int32_t* order,
+                        uint8_t* codes, uint8_t* scales, hipStream_t st, StageTimer* tm);
+hipError_t mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows,
+                          int64_t K, void* dst, hipStream_t st, StageTimer* tm);
+// scale bytes in row order, [batch][rows][ceil(K / 32)], to tiles
+hipError_t mx4_pack_scales(const uint8_t* plain, int64_t batch, int64_t rows, int64_t K, uint8_t* scales,
+                           hipStream_t st);
+
+// ---- linear layer over an MXFP4 base weight (bf16 pools) ------------------------
+// L.slice[0].W is not read; act4: the base product takes x rounded to MXFP4.
+size_t mx4_linear_workspace(int M, int N, int K, int S, int r_max, bool act4);
+hipError_t mx4_linear(const LinearArgs& L, const uint8_t* codes, const uint8_t* scales, bool act4, hipStream_t st,
+                      StageTimer* tm);
+
+// ---- mixture of experts for a few tokens ------------------------------------------
+constexpr int kMoeMaxExperts = 512, kMoeMaxPairs = 512, kMoeMaxK = 16;
+struct MoeWeights {  // [E] matrices: bf16 values, or 4-bit codes with their scale tiles
+    const void* data;
+    const uint8_t* scales;
+};
+struct MoeArgs {
+    const uint16_t* X;     // [T][H]
+    const int32_t* ids;    // [T][k]
+    const float* weights;  // [T][k]
+    MoeWeights gate, up;   // [E][I][H]
+    MoeWeights down;       // [E][H][I]
+    uint16_t* Y;           // [T][H]
+    int T, H, I, E, k;
+    void* workspace;
+};
+size_t moe_route_workspace(int T, int E);
+hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, int E, int k, int renorm, int32_t* ids,
+                     float* weights, void* workspace, hipStream_t st, StageTimer* tm);
+size_t moe_experts_workspace(int T, int I, int k);
+hipError_t moe_experts(const MoeArgs& a, bool mx4, hipStream_t st, StageTimer* tm);
+
 // ---- slot pool ------------------------------------------------------------
 hipError_t pool_check_finite(int dtype, const void* p, int64_t n, int* flag, hipStream_t st);
 hipError_t pool_write_slot(int dtype, void* A_pool, void* B_pool, int32_t* rank, float* scale, int slot,

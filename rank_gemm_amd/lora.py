@@ -22,7 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora.so")
 
 LORA_OK, LORA_EINVAL, LORA_ESLOT, LORA_ERANK, LORA_ENONFINITE, LORA_EHIP, LORA_ESPACE = 0, -1, -2, -3, -4, -5, -6
-LORA_F32, LORA_BF16 = 0, 1
+LORA_F32, LORA_BF16, LORA_MX4 = 0, 1, 2
 LORA_PLAN_ROWS = 16
 
 EXPORTS = (
@@ -31,14 +31,19 @@ EXPORTS = (
     "lora_status_string", "lora_profile_begin", "lora_profile_end", "lora_workspace_bytes_multi",
     "lora_linear_multi", "lora_plan_device_words", "lora_plan_device", "lora_linear_device_plan",
     "lora_shrink_bgmv", "lora_linear_multi_device_plan", "lora_plan_chunked", "lora_delta", "lora_delta_bgmv",
-    "lora_linear_noalloc", "lora_plan_upload",
+    "lora_linear_noalloc", "lora_plan_upload", "lora_mx4_row_bytes", "lora_mx4_scale_bytes", "lora_mx4_quantize",
+    "lora_mx4_dequantize", "lora_mx4_pack_scales", "lora_workspace_bytes_mx4", "lora_linear_mx4",
+    "lora_linear_mx4_device_plan", "lora_moe_route_workspace_bytes", "lora_moe_route",
+    "lora_moe_experts_workspace_bytes", "lora_moe_experts",
 )
 LORA_DEVICE_PLAN_MAX_SLOTS = 4096
 LORA_NOALLOC_MAX_WORKSPACE = 32 << 20
 LORA_MAX_SLICES = 4
+LORA_MOE_MAX_EXPERTS, LORA_MOE_MAX_K, LORA_MOE_MAX_PAIRS = 512, 16, 512
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
 _CODE = {"bf16": LORA_BF16, "f32": LORA_F32}
+_ACT = {"bf16": LORA_BF16, "mx4": LORA_MX4}
 
 
 class LoraError(RuntimeError):
@@ -55,6 +60,11 @@ class PlanInfo(ctypes.Structure):
 class SliceDesc(ctypes.Structure):
     """lora_slice: one projection of a multi-slice call."""
     _fields_ = [("pool", ctypes.c_void_p), ("W", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class MoeWeightsDesc(ctypes.Structure):
+    """lora_moe_weights: the experts' matrices of one layer."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scales", "up_scales", "down_scales")]
 
 
 class KernelStat(ctypes.Structure):
@@ -102,6 +112,22 @@ def lib():
             L.lora_linear_multi_device_plan.argtypes = [ctypes.POINTER(SliceDesc), _I, _P, _P, _I, _P, _SZ, _P]
             L.lora_shrink_bgmv.argtypes = [_P, _P, _P, _I, _P, _P, _SZ, _P]
             L.lora_shrink.argtypes = [_P, _P, _P, _P, _P, ctypes.POINTER(PlanInfo), _P, _P, _SZ, _P]
+            for name in ("lora_mx4_row_bytes", "lora_mx4_scale_bytes", "lora_workspace_bytes_mx4",
+                         "lora_moe_route_workspace_bytes", "lora_moe_experts_workspace_bytes"):
+                getattr(L, name).restype = _SZ
+            L.lora_mx4_row_bytes.argtypes = [_I]
+            L.lora_mx4_scale_bytes.argtypes = [_I, _I]
+            L.lora_mx4_quantize.argtypes = [_I, _P, _I, _I, _I, _P, _P, _P]
+            L.lora_mx4_dequantize.argtypes = [_P, _P, _I, _I, _I, _I, _P, _P]
+            L.lora_mx4_pack_scales.argtypes = [_P, _I, _I, _I, _P, _P]
+            L.lora_workspace_bytes_mx4.argtypes = [_P, _I, _I]
+            L.lora_linear_mx4.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, ctypes.POINTER(PlanInfo), _P, _P, _SZ, _P]
+            L.lora_linear_mx4_device_plan.argtypes = [_P, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P]
+            L.lora_moe_route_workspace_bytes.argtypes = [_I, _I]
+            L.lora_moe_route.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]
+            L.lora_moe_experts_workspace_bytes.argtypes = [_I, _I, _I]
+            L.lora_moe_experts.argtypes = [_I, _P, _P, _P, ctypes.POINTER(MoeWeightsDesc), _I, _I, _I, _I, _I, _P, _P,
+                                           _SZ, _P]
             L.lora_profile_begin.argtypes = [_I]
             L.lora_profile_end.argtypes = [ctypes.POINTER(KernelStat), _I, ctypes.POINTER(_I)]
             L.lora_status_string.argtypes = [_I]
@@ -511,6 +537,211 @@ def correction_bgmv(x: torch.Tensor, pool: Pool, slot_ids: torch.Tensor, y: torc
     ws = workspace if workspace is not None else pool.workspace(T)
     _check(lib().lora_delta_bgmv(pool.handle, x.data_ptr(), slot_ids.data_ptr(), T, y.data_ptr(), ws.data_ptr(),
                                  ws.numel() * ws.element_size(), _stream(x.device)), "lora_delta_bgmv")
+    return y
+
+
+class Mx4:
+    """A matrix, or a batch of matrices, held as MXFP4 rows: ``codes`` uint8
+    [..., rows, lora_mx4_row_bytes(K)] and ``scales`` uint8 [...,
+    lora_mx4_scale_bytes(rows, K)] in the order the products read them."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int):
+        self.codes, self.scales, self.K = codes, scales, int(K)
+
+    @property
+    def rows(self) -> int:
+        return int(self.codes.shape[-2])
+
+    @property
+    def shape(self):
+        """Shape of the values the codes stand for."""
+        return (*self.codes.shape[:-1], self.K)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @staticmethod
+    def empty(shape, device="cuda") -> "Mx4":
+        """Buffers for values of ``shape`` ([rows, K] or [batch, rows, K])."""
+        if len(shape) not in (2, 3) or shape[-1] < 1:
+            raise ValueError(f"MXFP4 rows need a shape [rows, K] or [batch, rows, K], got {tuple(shape)}")
+        *lead, rows, K = (int(n) for n in shape)
+        rb, sb = int(lib().lora_mx4_row_bytes(K)), int(lib().lora_mx4_scale_bytes(rows, K))
+        return Mx4(torch.empty((*lead, rows, rb), dtype=torch.uint8, device=device),
+                   torch.empty((*lead, sb), dtype=torch.uint8, device=device), K)
+
+
+def _mx4(q, name: str, shape=None) -> Mx4:
+    if not isinstance(q, Mx4):
+        raise ValueError(f"{name} must be an Mx4")
+    if shape is not None and tuple(q.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(q.shape)}, expected {tuple(shape)}")
+    if q.codes.dim() not in (2, 3) or q.K < 1:
+        raise ValueError(f"{name} needs codes [rows, bytes] or [batch, rows, bytes]")
+    lead, rows = q.codes.shape[:-2], q.rows
+    _dev_tensor(q.codes, torch.uint8, f"{name}.codes", (*lead, rows, int(lib().lora_mx4_row_bytes(q.K))))
+    _dev_tensor(q.scales, torch.uint8, f"{name}.scales", (*lead, int(lib().lora_mx4_scale_bytes(rows, q.K))))
+    return q
+
+
+def _same_device(*named):
+    dev = named[0][1].device
+    for name, t in named[1:]:
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {dev}")
+    return dev
+
+
+def _batch(shape) -> int:
+    return int(shape[0]) if len(shape) == 3 else 1
+
+
+def mx4_quantize(src: torch.Tensor, out: Mx4 | None = None) -> Mx4:
+    """lora_mx4_quantize: bf16 or fp32 rows ([rows, K] or [batch, rows, K]) to
+    MXFP4. ``out`` reuses buffers of the same shape."""
+    dt = {t: n for n, t in _TORCH_DTYPE.items()}.get(getattr(src, "dtype", None))
+    if dt is None:
+        raise ValueError("src must be a bf16 or fp32 device tensor")
+    _dev_tensor(src, src.dtype, "src")
+    if out is None:
+        out = Mx4.empty(src.shape, src.device)
+    _mx4(out, "out", src.shape)
+    with torch.cuda.device(_same_device(("src", src), ("out", out), ("out.scales", out.scales))):
+        _check(lib().lora_mx4_quantize(_CODE[dt], src.data_ptr(), _batch(src.shape), out.rows, out.K,
+                                       out.codes.data_ptr(), out.scales.data_ptr(), _stream(src.device)),
+               "lora_mx4_quantize")
+    return out
+
+
+def mx4_dequantize(q: Mx4, dtype: str = "bf16", out: torch.Tensor | None = None) -> torch.Tensor:
+    """lora_mx4_dequantize: the values MXFP4 codes stand for, in "bf16" or "f32"."""
+    _mx4(q, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=_TORCH_DTYPE[dtype], device=q.device)
+    _dev_tensor(out, _TORCH_DTYPE[dtype], "out", q.shape)
+    with torch.cuda.device(_same_device(("q", q), ("q.scales", q.scales), ("out", out))):
+        _check(lib().lora_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _batch(q.shape), q.rows, q.K,
+                                         _CODE[dtype], out.data_ptr(), _stream(q.device)), "lora_mx4_dequantize")
+    return out
+
+
+def mx4_pack(codes: torch.Tensor, e8m0: torch.Tensor, K: int) -> Mx4:
+    """MXFP4 rows as a checkpoint holds them (codes uint8 [..., rows, 16
+    ceil(K / 32)], one scale byte per block, [..., rows, ceil(K / 32)]) as an
+    Mx4: the codes stay, the scales are laid out by lora_mx4_pack_scales."""
+    if codes.dim() not in (2, 3) or int(K) < 1:
+        raise ValueError("codes must be [rows, bytes] or [batch, rows, bytes], K at least 1")
+    lead, rows = codes.shape[:-2], int(codes.shape[-2])
+    _dev_tensor(codes, torch.uint8, "codes", (*lead, rows, int(lib().lora_mx4_row_bytes(int(K)))))
+    _dev_tensor(e8m0, torch.uint8, "e8m0", (*lead, rows, (int(K) + 31) // 32))
+    scales = torch.empty((*lead, int(lib().lora_mx4_scale_bytes(rows, int(K)))), dtype=torch.uint8,
+                         device=codes.device)
+    q = Mx4(codes, scales, int(K))
+    with torch.cuda.device(_same_device(("codes", codes), ("e8m0", e8m0))):
+        _check(lib().lora_mx4_pack_scales(e8m0.data_ptr(), _batch(q.shape), rows, int(K), scales.data_ptr(),
+                                          _stream(codes.device)), "lora_mx4_pack_scales")
+    return q
+
+
+def linear_mx4(x: torch.Tensor, W: Mx4, pool: Pool, p, act: str = "bf16", y: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """lora_linear_mx4 (host plan) or lora_linear_mx4_device_plan (DevicePlan):
+    y = act(x) What^T + per-row adapter correction over a base weight in
+    MXFP4. ``act``: "bf16" (x as it is) or "mx4" (x rounded to MXFP4 for the
+    base product; the correction reads x itself)."""
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}")
+    if pool.dtype != "bf16":
+        raise ValueError("linear_mx4 needs a bf16 pool")
+    T = p.T
+    _dev_tensor(x, torch.bfloat16, "x", (T, pool.d_in))
+    _mx4(W, "W", (pool.d_out, pool.d_in))
+    if y is None:
+        y = torch.empty((T, pool.d_out), dtype=torch.bfloat16, device=x.device)
+    _dev_tensor(y, torch.bfloat16, "y", (T, pool.d_out))
+    device_plan = isinstance(p, DevicePlan)
+    if not device_plan and p.dev is None:
+        raise ValueError("plan was not uploaded")
+    if device_plan and p.S != pool.S:
+        raise ValueError("plan and pool have different S")
+    dev = _same_device(("x", x), ("W", W), ("W.scales", W.scales), ("pool", pool.A), ("y", y),
+                       ("plan", p.buf if device_plan else p.dev))
+    if workspace is None:
+        n = int(lib().lora_workspace_bytes_mx4(pool.handle, T, _ACT[act]))
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(dev))
+    base = (pool.handle, x.data_ptr(), W.codes.data_ptr(), W.scales.data_ptr(), _ACT[act])
+    with torch.cuda.device(dev):
+        if device_plan:
+            _check(lib().lora_linear_mx4_device_plan(*base, p.buf.data_ptr(), T, y.data_ptr(), *ws),
+                   "lora_linear_mx4_device_plan")
+        else:
+            _check(lib().lora_linear_mx4(*base, *p.dev_ptrs(), ctypes.byref(p.info), y.data_ptr(), *ws),
+                   "lora_linear_mx4")
+    return y
+
+
+def moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renorm: bool = True):
+    """lora_moe_route: (ids int32 [T, k], weights fp32 [T, k]) of the k experts
+    with the largest logits x router^T, their softmax taken over the chosen
+    (``renorm``) or over all experts. x [T, H], router [E, H], bf16."""
+    _dev_tensor(x, torch.bfloat16, "x")
+    _dev_tensor(router, torch.bfloat16, "router")
+    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and router {tuple(router.shape)} must be [T, H] and [E, H]")
+    (T, H), E = x.shape, int(router.shape[0])
+    dev = _same_device(("x", x), ("router", router))
+    ids = torch.empty((T, max(int(k), 0)), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, max(int(k), 0)), dtype=torch.float32, device=dev)
+    n = int(lib().lora_moe_route_workspace_bytes(T, E))
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().lora_moe_route(x.data_ptr(), router.data_ptr(), T, H, E, int(k), int(bool(renorm)),
+                                    ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
+               "lora_moe_route")
+    return ids, weights
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate, up, down,
+                y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """lora_moe_experts: y[t] = sum_j weights[t, j] down_e(silu(gate_e x_t) *
+    up_e x_t), e = ids[t, j]. gate, up [E, I, H] and down [E, H, I], all bf16
+    tensors or all Mx4 batches."""
+    _dev_tensor(x, torch.bfloat16, "x")
+    _dev_tensor(ids, torch.int32, "ids")
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise ValueError(f"x {tuple(x.shape)} and ids {tuple(ids.shape)} must be [T, H] and [T, k]")
+    (T, H), k = x.shape, int(ids.shape[1])
+    _dev_tensor(weights, torch.float32, "weights", (T, k))
+    mx4 = isinstance(gate, Mx4)
+    if len(gate.shape) != 3:
+        raise ValueError(f"gate must be [E, I, H], got {tuple(gate.shape)}")
+    E, I = int(gate.shape[0]), int(gate.shape[1])
+    d = MoeWeightsDesc()
+    named = [("x", x), ("ids", ids), ("weights", weights)]
+    for name, w, shape in (("gate", gate, (E, I, H)), ("up", up, (E, I, H)), ("down", down, (E, H, I))):
+        if mx4:
+            _mx4(w, name, shape)
+            setattr(d, name, w.codes.data_ptr())
+            setattr(d, name + "_scales", w.scales.data_ptr())
+            named.append((name + ".scales", w.scales))
+        else:
+            _dev_tensor(w, torch.bfloat16, name, shape)
+            setattr(d, name, w.data_ptr())
+        named.append((name, w))
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    _dev_tensor(y, torch.bfloat16, "y", (T, H))
+    dev = _same_device(*named, ("y", y))
+    if workspace is None:
+        n = int(lib().lora_moe_experts_workspace_bytes(T, I, k))
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().lora_moe_experts(LORA_MX4 if mx4 else LORA_BF16, x.data_ptr(), ids.data_ptr(),
+                                      weights.data_ptr(), ctypes.byref(d), T, H, I, E, k, y.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      _stream(dev)), "lora_moe_experts")
     return y
 
 
