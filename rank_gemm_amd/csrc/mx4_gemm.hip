@@ -1,0 +1,44 @@
+// The tiled GEMM of MXFP4 operands (x rounded to 4 bits in plan order, W in 4
+// bits): gemm_tile.h's pipeline with the scaled 16x16x128 product.
+#include "gemm_tile.h"
+#include "mx4_linear.h"
+
+namespace lora {
+
+template <int BM, int BN, int WM, int WN, int NS, bool EPI, bool KTAIL, bool BUF>
+__global__ __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4))) void mx4_tile_kernel(
+    const uint16_t* __restrict__ xc, const uint8_t* __restrict__ xs, const uint16_t* __restrict__ wc,
+    const uint8_t* __restrict__ wsc, uint16_t* __restrict__ Y, int M, int N, int K16, int tiles_m, int tiles_n,
+    Fuse f) {
+    gemm_tile<BM, BN, WM, WN, NS, EPI, KTAIL, false, BUF, true>(xc, wc, Y, M, N, K16, tiles_m, tiles_n, f,
+                                                                SplitOut{}, xs, wsc);
+}
+
+// BUF: loads through buffer resources, the expand as extra K steps only
+template <int BM, int BN, int WM, int WN, int NS, bool BUF>
+static hipError_t launch_mx4(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* wsc, uint16_t* Y,
+                             int M, int N, int K16, const Fuse& f, hipStream_t st, StageTimer* tm) {
+    const int tiles_m = cdiv(M, BM), tiles_n = cdiv(N, BN);
+    const bool ktail = K16 % 64 != 0;
+    auto ker = ktail ? mx4_tile_kernel<BM, BN, WM, WN, NS, false, true, BUF>
+                     : mx4_tile_kernel<BM, BN, WM, WN, NS, false, false, BUF>;
+    if constexpr (!BUF) {
+        if (f.adapters && !f.ext)
+            ker = ktail ? mx4_tile_kernel<BM, BN, WM, WN, NS, true, true, BUF>
+                        : mx4_tile_kernel<BM, BN, WM, WN, NS, true, false, BUF>;
+    }
+    return launch(tm, "mx4_gemm", ker, dim3(tiles_m * tiles_n), dim3(64 * WM * WN), st, (const uint16_t*)xc, xs,
+                  (const uint16_t*)wc, wsc, Y, M, N, K16, tiles_m, tiles_n, f);
+}
+
+hipError_t mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* wsc, uint16_t* Y, int M,
+                    int N, int K, const Fuse& f, hipStream_t st, StageTimer* tm) {
+    const int K16 = (int)(mx4_row_bytes(K) / 2);  // a row's bytes in the 16-bit units the tile counts in
+    const bool extra = !f.adapters || f.ext;
+    auto n_tiles = [&](int bm, int bn) { return (int64_t)cdiv(M, bm) * cdiv(N, bn); };
+    if (n_tiles(256, 256) >= 200 && extra && tile_buffers_fit(M, N, K16, 256, f))
+        return launch_mx4<256, 256, 2, 2, 2, true>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+    return launch_mx4<128, 128, 2, 4, 3, false>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+}
+
+}  // namespace lora

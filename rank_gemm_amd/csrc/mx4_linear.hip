@@ -4,6 +4,7 @@
 // or the MXFP4 rounding of each row of x; the adapters always read x itself.
 #include "fuse.h"
 #include "mx4.h"
+#include "mx4_linear.h"
 #include "shrink.h"
 
 namespace lora {
@@ -155,12 +156,18 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
         L.K = Kp;
     }
     float* h = reinterpret_cast<float*>(ws + sp.shrink);
+    Fuse f{L.token_order, L.slot_indptr, h, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
+           nullptr, (L.r_max + 7) & ~7};
+    const bool tiled = act4 && M > 64;
+    if (tiled && L.r_max % 8 == 0 && L.S <= kMetaSlots) {
+        f.ext = reinterpret_cast<uint16_t*>(h);
+        f.h = nullptr;
+    }
     if (L.adapters) {
-        e = tiled_shrink(L, sl, ws + sp.shrink, h, nullptr, st, tm);
+        e = tiled_shrink(L, sl, ws + sp.shrink, f.ext ? nullptr : h, const_cast<uint16_t*>(f.ext), st, tm);
         if (e != hipSuccess) return e;
     }
-    const Fuse f{L.token_order, L.slot_indptr, h, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
-                 nullptr, (L.r_max + 7) & ~7};
+    if (tiled) return mx4_gemm(xc, xs, codes, scales, sl.Y, M, N, L.K, f, st, tm);
     return launch(tm, "mx4_rows", act4 ? mx4_rows_kernel<true> : mx4_rows_kernel<false>,
                   dim3(cdiv(N, 64), cdiv(M, 64)), dim3(256), st, L.X, xc, xs, codes, scales, sl.Y, M, N, L.K, f);
 }

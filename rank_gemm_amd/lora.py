@@ -543,23 +543,33 @@ def correction_bgmv(x: torch.Tensor, pool: Pool, slot_ids: torch.Tensor, y: torc
 class Mx4:
     """A matrix, or a batch of matrices, held as MXFP4 rows: ``codes`` uint8
     [..., rows, lora_mx4_row_bytes(K)] and ``scales`` uint8 [...,
-    lora_mx4_scale_bytes(rows, K)] in the order the products read them."""
+    lora_mx4_scale_bytes(rows, K)] in the order the products read them.
+    ``shape`` is that of the values. Checked here once; the buffers stay."""
+
+    __slots__ = ("_codes", "_scales", "K", "rows", "batch", "shape", "device")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int):
-        self.codes, self.scales, self.K = codes, scales, int(K)
+        K = int(K)
+        if codes.dim() not in (2, 3) or K < 1:
+            raise ValueError("MXFP4 rows need codes [rows, bytes] or [batch, rows, bytes] and K of at least 1")
+        lead, rows = codes.shape[:-2], int(codes.shape[-2])
+        for name, t, shape in (("codes", codes, (*lead, rows, int(lib().lora_mx4_row_bytes(K)))),
+                               ("scales", scales, (*lead, int(lib().lora_mx4_scale_bytes(rows, K))))):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be contiguous uint8 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+        if codes.device != scales.device:
+            raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
+        self._codes, self._scales, self.K, self.rows = codes, scales, K, rows
+        self.batch = int(lead[0]) if lead else 1
+        self.shape, self.device = (*lead, rows, K), codes.device
 
     @property
-    def rows(self) -> int:
-        return int(self.codes.shape[-2])
+    def codes(self) -> torch.Tensor:
+        return self._codes
 
     @property
-    def shape(self):
-        """Shape of the values the codes stand for."""
-        return (*self.codes.shape[:-1], self.K)
-
-    @property
-    def device(self):
-        return self.codes.device
+    def scales(self) -> torch.Tensor:
+        return self._scales
 
     @staticmethod
     def empty(shape, device="cuda") -> "Mx4":
@@ -573,44 +583,52 @@ class Mx4:
 
 
 def _mx4(q, name: str, shape=None) -> Mx4:
-    if not isinstance(q, Mx4):
-        raise ValueError(f"{name} must be an Mx4")
-    if shape is not None and tuple(q.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(q.shape)}, expected {tuple(shape)}")
-    if q.codes.dim() not in (2, 3) or q.K < 1:
-        raise ValueError(f"{name} needs codes [rows, bytes] or [batch, rows, bytes]")
-    lead, rows = q.codes.shape[:-2], q.rows
-    _dev_tensor(q.codes, torch.uint8, f"{name}.codes", (*lead, rows, int(lib().lora_mx4_row_bytes(q.K))))
-    _dev_tensor(q.scales, torch.uint8, f"{name}.scales", (*lead, int(lib().lora_mx4_scale_bytes(rows, q.K))))
+    if not isinstance(q, Mx4) or q.device.type != "cuda":
+        raise ValueError(f"{name} must be an Mx4 on a GPU")
+    if shape is not None and q.shape != tuple(shape):
+        raise ValueError(f"{name} has shape {q.shape}, expected {tuple(shape)}")
     return q
 
 
 def _same_device(*named):
     dev = named[0][1].device
-    for name, t in named[1:]:
+    for name, t in named:
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {dev}")
     return dev
 
 
-def _batch(shape) -> int:
-    return int(shape[0]) if len(shape) == 3 else 1
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(dev, fn, what: str, *args):
+    """One call of the library on ``dev``'s current stream, with ``dev`` the
+    current device (a decode step makes many such calls: the stream's handle
+    is fetched without building a Stream object where torch offers it)."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    else:
+        rc = fn(*args, _raw_stream(dev.index) if _raw_stream is not None else _stream(dev))
+    if rc != LORA_OK:
+        raise LoraError(rc, what)
+
+
+_DTYPE_NAME = {t: n for n, t in _TORCH_DTYPE.items()}
 
 
 def mx4_quantize(src: torch.Tensor, out: Mx4 | None = None) -> Mx4:
     """lora_mx4_quantize: bf16 or fp32 rows ([rows, K] or [batch, rows, K]) to
     MXFP4. ``out`` reuses buffers of the same shape."""
-    dt = {t: n for n, t in _TORCH_DTYPE.items()}.get(getattr(src, "dtype", None))
+    dt = _DTYPE_NAME.get(getattr(src, "dtype", None))
     if dt is None:
         raise ValueError("src must be a bf16 or fp32 device tensor")
     _dev_tensor(src, src.dtype, "src")
     if out is None:
         out = Mx4.empty(src.shape, src.device)
     _mx4(out, "out", src.shape)
-    with torch.cuda.device(_same_device(("src", src), ("out", out), ("out.scales", out.scales))):
-        _check(lib().lora_mx4_quantize(_CODE[dt], src.data_ptr(), _batch(src.shape), out.rows, out.K,
-                                       out.codes.data_ptr(), out.scales.data_ptr(), _stream(src.device)),
-               "lora_mx4_quantize")
+    _call(_same_device(("src", src), ("out", out)), lib().lora_mx4_quantize, "lora_mx4_quantize", _CODE[dt],
+          src.data_ptr(), out.batch, out.rows, out.K, out._codes.data_ptr(), out._scales.data_ptr())
     return out
 
 
@@ -620,9 +638,8 @@ def mx4_dequantize(q: Mx4, dtype: str = "bf16", out: torch.Tensor | None = None)
     if out is None:
         out = torch.empty(q.shape, dtype=_TORCH_DTYPE[dtype], device=q.device)
     _dev_tensor(out, _TORCH_DTYPE[dtype], "out", q.shape)
-    with torch.cuda.device(_same_device(("q", q), ("q.scales", q.scales), ("out", out))):
-        _check(lib().lora_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _batch(q.shape), q.rows, q.K,
-                                         _CODE[dtype], out.data_ptr(), _stream(q.device)), "lora_mx4_dequantize")
+    _call(_same_device(("q", q), ("out", out)), lib().lora_mx4_dequantize, "lora_mx4_dequantize",
+          q._codes.data_ptr(), q._scales.data_ptr(), q.batch, q.rows, q.K, _CODE[dtype], out.data_ptr())
     return out
 
 
@@ -630,18 +647,28 @@ def mx4_pack(codes: torch.Tensor, e8m0: torch.Tensor, K: int) -> Mx4:
     """MXFP4 rows as a checkpoint holds them (codes uint8 [..., rows, 16
     ceil(K / 32)], one scale byte per block, [..., rows, ceil(K / 32)]) as an
     Mx4: the codes stay, the scales are laid out by lora_mx4_pack_scales."""
+    _dev_tensor(codes, torch.uint8, "codes")
     if codes.dim() not in (2, 3) or int(K) < 1:
         raise ValueError("codes must be [rows, bytes] or [batch, rows, bytes], K at least 1")
     lead, rows = codes.shape[:-2], int(codes.shape[-2])
-    _dev_tensor(codes, torch.uint8, "codes", (*lead, rows, int(lib().lora_mx4_row_bytes(int(K)))))
     _dev_tensor(e8m0, torch.uint8, "e8m0", (*lead, rows, (int(K) + 31) // 32))
-    scales = torch.empty((*lead, int(lib().lora_mx4_scale_bytes(rows, int(K)))), dtype=torch.uint8,
-                         device=codes.device)
-    q = Mx4(codes, scales, int(K))
-    with torch.cuda.device(_same_device(("codes", codes), ("e8m0", e8m0))):
-        _check(lib().lora_mx4_pack_scales(e8m0.data_ptr(), _batch(q.shape), rows, int(K), scales.data_ptr(),
-                                          _stream(codes.device)), "lora_mx4_pack_scales")
+    q = Mx4(codes, torch.empty((*lead, int(lib().lora_mx4_scale_bytes(rows, int(K)))), dtype=torch.uint8,
+                               device=codes.device), K)
+    _call(_same_device(("codes", codes), ("e8m0", e8m0)), lib().lora_mx4_pack_scales, "lora_mx4_pack_scales",
+          e8m0.data_ptr(), q.batch, rows, q.K, q._scales.data_ptr())
     return q
+
+
+def _space(workspace, n: int, dev):
+    """(address, bytes) of the caller's workspace, or of a new one of n bytes.
+    One per call: torch hands its memory on in stream order, and a captured
+    graph keeps its own, so no two calls that may overlap share one."""
+    if workspace is None:
+        workspace = torch.empty(max(int(n), 256), dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), workspace.numel()
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the inputs on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def linear_mx4(x: torch.Tensor, W: Mx4, pool: Pool, p, act: str = "bf16", y: torch.Tensor | None = None,
@@ -650,7 +677,8 @@ def linear_mx4(x: torch.Tensor, W: Mx4, pool: Pool, p, act: str = "bf16", y: tor
     y = act(x) What^T + per-row adapter correction over a base weight in
     MXFP4. ``act``: "bf16" (x as it is) or "mx4" (x rounded to MXFP4 for the
     base product; the correction reads x itself)."""
-    if act not in _ACT:
+    code = _ACT.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}")
     if pool.dtype != "bf16":
         raise ValueError("linear_mx4 needs a bf16 pool")
@@ -665,20 +693,17 @@ def linear_mx4(x: torch.Tensor, W: Mx4, pool: Pool, p, act: str = "bf16", y: tor
         raise ValueError("plan was not uploaded")
     if device_plan and p.S != pool.S:
         raise ValueError("plan and pool have different S")
-    dev = _same_device(("x", x), ("W", W), ("W.scales", W.scales), ("pool", pool.A), ("y", y),
-                       ("plan", p.buf if device_plan else p.dev))
-    if workspace is None:
-        n = int(lib().lora_workspace_bytes_mx4(pool.handle, T, _ACT[act]))
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(dev))
-    base = (pool.handle, x.data_ptr(), W.codes.data_ptr(), W.scales.data_ptr(), _ACT[act])
-    with torch.cuda.device(dev):
-        if device_plan:
-            _check(lib().lora_linear_mx4_device_plan(*base, p.buf.data_ptr(), T, y.data_ptr(), *ws),
-                   "lora_linear_mx4_device_plan")
-        else:
-            _check(lib().lora_linear_mx4(*base, *p.dev_ptrs(), ctypes.byref(p.info), y.data_ptr(), *ws),
-                   "lora_linear_mx4")
+    dev = _same_device(("x", x), ("W", W), ("pool", pool.A), ("y", y), ("plan", p.buf if device_plan else p.dev))
+    L = lib()
+    n = L.lora_workspace_bytes_mx4(pool.handle, T, code) if workspace is None else 0
+    keep, ws, nb = _space(workspace, n, dev)
+    base = (pool.handle, x.data_ptr(), W._codes.data_ptr(), W._scales.data_ptr(), code)
+    if device_plan:
+        _call(dev, L.lora_linear_mx4_device_plan, "lora_linear_mx4_device_plan", *base, p.buf.data_ptr(), T,
+              y.data_ptr(), ws, nb)
+    else:
+        _call(dev, L.lora_linear_mx4, "lora_linear_mx4", *base, *p.dev_ptrs(), ctypes.byref(p.info), y.data_ptr(),
+              ws, nb)
     return y
 
 
@@ -690,16 +715,14 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renorm: bool = True
     _dev_tensor(router, torch.bfloat16, "router")
     if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
         raise ValueError(f"x {tuple(x.shape)} and router {tuple(router.shape)} must be [T, H] and [E, H]")
-    (T, H), E = x.shape, int(router.shape[0])
+    (T, H), E, k = x.shape, router.shape[0], int(k)
     dev = _same_device(("x", x), ("router", router))
-    ids = torch.empty((T, max(int(k), 0)), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, max(int(k), 0)), dtype=torch.float32, device=dev)
-    n = int(lib().lora_moe_route_workspace_bytes(T, E))
-    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().lora_moe_route(x.data_ptr(), router.data_ptr(), T, H, E, int(k), int(bool(renorm)),
-                                    ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)),
-               "lora_moe_route")
+    out = torch.empty((2, T, max(k, 0)), dtype=torch.float32, device=dev)
+    ids, weights = out[0].view(torch.int32), out[1]
+    L = lib()
+    keep, ws, nb = _space(None, L.lora_moe_route_workspace_bytes(T, E), dev)
+    _call(dev, L.lora_moe_route, "lora_moe_route", x.data_ptr(), router.data_ptr(), T, H, E, k, int(bool(renorm)),
+          ids.data_ptr(), weights.data_ptr(), ws, nb)
     return ids, weights
 
 
@@ -712,36 +735,30 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate,
     _dev_tensor(ids, torch.int32, "ids")
     if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
         raise ValueError(f"x {tuple(x.shape)} and ids {tuple(ids.shape)} must be [T, H] and [T, k]")
-    (T, H), k = x.shape, int(ids.shape[1])
+    (T, H), k = x.shape, ids.shape[1]
     _dev_tensor(weights, torch.float32, "weights", (T, k))
     mx4 = isinstance(gate, Mx4)
     if len(gate.shape) != 3:
         raise ValueError(f"gate must be [E, I, H], got {tuple(gate.shape)}")
-    E, I = int(gate.shape[0]), int(gate.shape[1])
-    d = MoeWeightsDesc()
-    named = [("x", x), ("ids", ids), ("weights", weights)]
-    for name, w, shape in (("gate", gate, (E, I, H)), ("up", up, (E, I, H)), ("down", down, (E, H, I))):
-        if mx4:
-            _mx4(w, name, shape)
-            setattr(d, name, w.codes.data_ptr())
-            setattr(d, name + "_scales", w.scales.data_ptr())
-            named.append((name + ".scales", w.scales))
-        else:
+    E, I = gate.shape[:2]
+    if mx4:
+        _mx4(gate, "gate", (E, I, H)), _mx4(up, "up", (E, I, H)), _mx4(down, "down", (E, H, I))
+        d = MoeWeightsDesc(*(w._codes.data_ptr() for w in (gate, up, down)),
+                           *(w._scales.data_ptr() for w in (gate, up, down)))
+    else:
+        for name, w, shape in (("gate", gate, (E, I, H)), ("up", up, (E, I, H)), ("down", down, (E, H, I))):
             _dev_tensor(w, torch.bfloat16, name, shape)
-            setattr(d, name, w.data_ptr())
-        named.append((name, w))
+        d = MoeWeightsDesc(gate.data_ptr(), up.data_ptr(), down.data_ptr())
     if y is None:
         y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     _dev_tensor(y, torch.bfloat16, "y", (T, H))
-    dev = _same_device(*named, ("y", y))
-    if workspace is None:
-        n = int(lib().lora_moe_experts_workspace_bytes(T, I, k))
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().lora_moe_experts(LORA_MX4 if mx4 else LORA_BF16, x.data_ptr(), ids.data_ptr(),
-                                      weights.data_ptr(), ctypes.byref(d), T, H, I, E, k, y.data_ptr(),
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                      _stream(dev)), "lora_moe_experts")
+    dev = _same_device(("x", x), ("ids", ids), ("weights", weights), ("gate", gate), ("up", up), ("down", down),
+                       ("y", y))
+    L = lib()
+    n = L.lora_moe_experts_workspace_bytes(T, I, k) if workspace is None else 0
+    keep, ws, nb = _space(workspace, n, dev)
+    _call(dev, L.lora_moe_experts, "lora_moe_experts", LORA_MX4 if mx4 else LORA_BF16, x.data_ptr(), ids.data_ptr(),
+          weights.data_ptr(), ctypes.byref(d), T, H, I, E, k, y.data_ptr(), ws, nb)
     return y
 
 
