@@ -22,65 +22,140 @@ __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, SA, (int)sa, SB, (int)sb);
 }
 
-// 64 sorted rows x 64 columns per workgroup, a wave 16 rows x 64 columns over
-// all of K, operands straight from memory.
-template <bool ACT4>
-__global__ __launch_bounds__(256) void mx4_rows_kernel(const uint16_t* __restrict__ X,
-                                                       const uint8_t* __restrict__ xc,
-                                                       const uint8_t* __restrict__ xs,
-                                                       const uint8_t* __restrict__ wc,
-                                                       const uint8_t* __restrict__ wsc, uint16_t* __restrict__ Y,
-                                                       int M, int N, int K, Fuse f) {
-    __shared__ SlotMeta meta;
-    __shared__ u32x4 stg[4 * 128];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// ------------------------------------------------------------ decode-sized T --
+// Kernel 1 of two, as on the bf16 decode path: a workgroup takes 64 columns x
+// 16 NT rows over one K split and writes fp32 partials in that path's layout
+// ([split][64-row tile][64-column tile][16 blocks][64 lanes], splitk.hip),
+// which its kernel 2 adds, applies the expand to and rounds. A wave's unit is
+// 64 columns x 256 k: one 8-byte read of scales and eight 16-byte reads of
+// codes per lane, all issued at once. The four waves take the split's units
+// in turn and add their sums in wave order through LDS. The SGMV shrink runs
+// in extra workgroups of the same launch, over K ranges of its own.
+struct Mx4Split {
+    const uint16_t* X;
+    const uint8_t *xc, *xs;  // 4-bit activations, in plan order
+    const uint8_t *wc, *ws;
+    float* part;
+    int M, N, K, n_mt, n_nt, ks, upb;  // upb: units per split
+    const int32_t* token_order;
+    const Item* work;
+    const uint16_t* A_pool;
+    const int32_t* rank;
+    float* part_h;  // [hs][M][r_max]
+    int n_items, r_max, hs, hkc;
+};
+
+template <bool ACT4, int NT>
+__global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
+    __shared__ f32x4 red[4 * 4 * NT * 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n_shrink = a.n_items * a.hs;
+    if ((int)blockIdx.x < n_shrink) {
+        const int item = blockIdx.x % a.n_items, hz = blockIdx.x / a.n_items;
+        const Item it = a.work[item];
+        const int r = a.rank[it.slot];
+        if (r == 0) return;
+        const int kbeg = hz * a.hkc, kend = min(a.K, kbeg + a.hkc);
+        const ShrinkOut out{a.part_h + (int64_t)hz * a.M * a.r_max, nullptr, 0, 0.f};
+        shrink_item<4>(a.X, a.A_pool, r, a.token_order, it, out, a.K, kbeg, kend, a.r_max, red);
+        return;
+    }
+    const int b = blockIdx.x - n_shrink, tiles = a.n_mt * a.n_nt;
+    const int kz = b / tiles, t = b - kz * tiles, mt = t / a.n_nt, nt = t - mt * a.n_nt;
     const int fr = lane & 15, fc = lane >> 4;
-    const MetaView mv = stage_meta(f, &meta);
-    __syncthreads();
-    const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64, p0 = m0 + 16 * wave;
-    const int64_t rb = mx4_row_bytes(K), kts = mx4_k_tiles(K);
-    const int nb = (K + 31) / 32;
-    const int p = min(p0 + fr, M - 1);
-    const uint16_t* xrow = X + (int64_t)f.token_order[p] * K;
-    const uint8_t* xq = xc + (int64_t)p * rb;
-    f32x4 acc[1][4];
+    const int64_t rb = mx4_row_bytes(a.K), kts = mx4_k_tiles(a.K);
+    const int u1 = min((int)kts, (kz + 1) * a.upb);
+    const uint8_t* wrow[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int kt = 0; kt < kts; ++kt) {
-        const u32x2 ws = *reinterpret_cast<const u32x2*>(wsc + ((int64_t)blockIdx.x * kts + kt) * kMxTileBytes + lane * 8);
-        u32x2 xsc{0, 0};
+    for (int j = 0; j < 4; ++j) wrow[j] = a.wc + (int64_t)min(nt * 64 + 16 * j + fr, a.N - 1) * rb;
+    const uint16_t* xrow[NT];
+    const uint8_t* xq[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        // rows past M are not read: x comes from memory once per row and column tile
+        const int p = mt * 64 + 16 * i + fr;
+        if constexpr (ACT4) xq[i] = p < a.M ? a.xc + (int64_t)p * rb : nullptr;
+        else xrow[i] = p < a.M ? a.X + (int64_t)a.token_order[p] * a.K : nullptr;
+    }
+    f32x4 acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = kz * a.upb + wave; u < u1; u += 4) {
+        const u32x2 wsc = *as_global<u32x2>(a.ws + ((int64_t)nt * kts + u) * kMxTileBytes + lane * 8);
+        u32x4 w[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int blk = u * 8 + h * 4 + fc;
+                w[h][j] = __builtin_nontemporal_load(or_zero(blk * 32 < a.K, wrow[j] + blk * 16));
+            }
         if constexpr (ACT4) {
-            xsc = *reinterpret_cast<const u32x2*>(xs + ((int64_t)blockIdx.y * kts + kt) * kMxTileBytes + lane * 8);
-            xsc[0] >>= 8 * wave;
-            xsc[1] >>= 8 * wave;
-        }
+            const u32x2 xsc = *as_global<u32x2>(a.xs + ((int64_t)mt * kts + u) * kMxTileBytes + lane * 8);
+            u32x4 x[2][NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int blk = kt * 8 + h * 4 + fc;
-            u32x4 w[4];
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = *or_zero(blk < nb, wc + (int64_t)min(n0 + 16 * j + fr, N - 1) * rb + blk * 16);
-            if constexpr (ACT4) {
-                const u32x4 x = *or_zero(blk < nb, xq + blk * 16);
-                acc[0][0] = mfma_mx4<0, 0>(w[0], x, acc[0][0], ws[h], xsc[h]);
-                acc[0][1] = mfma_mx4<1, 0>(w[1], x, acc[0][1], ws[h], xsc[h]);
-                acc[0][2] = mfma_mx4<2, 0>(w[2], x, acc[0][2], ws[h], xsc[h]);
-                acc[0][3] = mfma_mx4<3, 0>(w[3], x, acc[0][3], ws[h], xsc[h]);
-            } else {
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int k = blk * 32 + 8 * m;
-                    const u32x4 x = *or_zero(k < K, xrow + k);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[0][j] = mfma16x16x32(mx4_bf16x8(w[j][m], mx4_scale(ws[h] >> (8 * j) & 255)), x, acc[0][j]);
+                for (int i = 0; i < NT; ++i) {
+                    const int blk = u * 8 + h * 4 + fc;
+                    x[h][i] = *or_zero(xq[i] && blk * 32 < a.K, xq[i] + blk * 16);
                 }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                auto row = [&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    if constexpr (i < NT) {
+                        acc[i][0] = mfma_mx4<i, 0>(x[h][i], w[h][0], acc[i][0], xsc[h], wsc[h]);
+                        acc[i][1] = mfma_mx4<i, 1>(x[h][i], w[h][1], acc[i][1], xsc[h], wsc[h]);
+                        acc[i][2] = mfma_mx4<i, 2>(x[h][i], w[h][2], acc[i][2], xsc[h], wsc[h]);
+                        acc[i][3] = mfma_mx4<i, 3>(x[h][i], w[h][3], acc[i][3], xsc[h], wsc[h]);
+                    }
+                };
+                row(std::integral_constant<int, 0>{});
+                row(std::integral_constant<int, 1>{});
+                row(std::integral_constant<int, 2>{});
+                row(std::integral_constant<int, 3>{});
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 x[4][NT];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const int k = (u * 8 + h * 4 + fc) * 32 + 8 * m;
+                        x[m][i] = *or_zero(xrow[i] && k < a.K, xrow[i] + k);
+                    }
+                float sc[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[j] = mx4_scale(wsc[h] >> (8 * j) & 255);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const u32x4 wf = mx4_bf16x8(w[h][j][m], sc[j]);
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) acc[i][j] = mfma16x16x32(x[m][i], wf, acc[i][j]);
+                    }
             }
         }
     }
-    fused_expand<1, 4>(acc, f, mv, p0, n0, M, N, lane);
-    store_tile<1, 4>(acc, reinterpret_cast<char*>(stg) + wave * 2048, Y, f.token_order, p0, n0, M, N, lane);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red[((wave * 4 + j) * NT + i) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    f32x4* out = reinterpret_cast<f32x4*>(a.part) + ((int64_t)(kz * a.n_mt + mt) * a.n_nt + nt) * 1024;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {  // wave w: column block w
+        f32x4 s = red[(wave * NT + i) * 64 + lane];
+#pragma unroll
+        for (int v = 1; v < 4; ++v) s += red[((v * 4 + wave) * NT + i) * 64 + lane];
+        out[(i * 4 + wave) * 64 + lane] = s;
+    }
 }
 
 // rows of any width -> rows of Kp elements (a multiple of 8), zeros behind
@@ -92,34 +167,69 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
     if (r < rows && k < Kp) dst[r * Kp + k] = k < K ? src[r * K + k] : uint16_t(0);
 }
 
-static inline size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
+// The path of a call, by its sizes and act alone (a base-only call takes the
+// same one).
+enum class Mx4Path { kSplit, kTile4, kDequant };
+constexpr int kMx4SplitRows = 64;
+static Mx4Path mx4_path(int M, bool act4) {
+    if (M <= kMx4SplitRows) return Mx4Path::kSplit;
+    return act4 ? Mx4Path::kTile4 : Mx4Path::kDequant;
+}
+
+// K splits of the decode path: about 512 workgroups, a unit for every wave
+struct Mx4SplitPlan {
+    int n_mt, n_nt, ks, upb, hs, hkc;
+};
+static Mx4SplitPlan mx4_split_plan(int M, int N, int K) {
+    Mx4SplitPlan p{};
+    p.n_mt = cdiv(M, 64);
+    p.n_nt = cdiv(N, 64);
+    const int kts = (int)mx4_k_tiles(K), tiles = p.n_mt * p.n_nt;
+    const int want = tiles >= 512 ? 1 : 512 / tiles;
+    p.upb = (cdiv(kts, want) + 3) / 4 * 4;
+    p.ks = cdiv(kts, p.upb);
+    p.hkc = max(256, (cdiv(K, 8) + 31) / 32 * 32);
+    p.hs = cdiv(K, p.hkc);
+    return p;
+}
 
 // Workspace: padded rows of x and A (d_in not a multiple of 8), the 4-bit
-// activations, then the shrink's h and planes.
+// activations, then the path's own (partials and h planes; h or the expand
+// operand; W in bf16 and the bf16 layer's workspace).
 struct Mx4Space {
-    size_t xpad, apad, codes, scales, shrink, total;
+    size_t xpad, apad, codes, scales, own, h, total;
 };
-static Mx4Space mx4_space(int M, int K, int S, int r_max, bool act4) {
-    const size_t Kp = (K + 7) / 8 * 8;
+static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
+    const int Kp = (K + 7) / 8 * 8;
     Mx4Space s{};
     size_t o = 0;
-    s.xpad = o;
-    if (K % 8) o += a256((size_t)M * Kp * 2);
-    s.apad = o;
-    if (K % 8) o += a256((size_t)S * r_max * Kp * 2);
-    s.codes = o;
-    if (act4) o += a256((size_t)M * mx4_row_bytes(K));
-    s.scales = o;
-    if (act4) o += a256((size_t)mx4_scale_bytes(M, K));
-    s.shrink = o;
-    o += tiled_workspace(M, r_max);
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o += (bytes + 255) & ~size_t(255);
+        return at;
+    };
+    s.xpad = take(K % 8 ? (size_t)M * Kp * 2 : 0);
+    s.apad = take(K % 8 ? (size_t)S * r_max * Kp * 2 : 0);
+    s.codes = take(act4 ? (size_t)M * mx4_row_bytes(K) : 0);
+    s.scales = take(act4 ? (size_t)mx4_scale_bytes(M, K) : 0);
+    switch (mx4_path(M, act4)) {
+        case Mx4Path::kSplit: {
+            const Mx4SplitPlan p = mx4_split_plan(M, N, K);
+            s.own = take((size_t)p.ks * p.n_mt * p.n_nt * 64 * 64 * sizeof(float));
+            s.h = take((size_t)p.hs * M * r_max * sizeof(float));
+            break;
+        }
+        case Mx4Path::kTile4: s.own = take(tiled_workspace(M, r_max)); break;
+        case Mx4Path::kDequant:
+            s.own = take((size_t)N * Kp * 2);
+            s.h = take(gemm_bf16_workspace(M, &N, 1, Kp, r_max));
+    }
     s.total = o;
     return s;
 }
 
 size_t mx4_linear_workspace(int M, int N, int K, int S, int r_max, bool act4) {
-    (void)N;
-    return M > 0 ? mx4_space(M, K, S, r_max, act4).total : 0;
+    return M > 0 ? mx4_space(M, N, K, S, r_max, act4).total : 0;
 }
 
 static hipError_t pad_rows(const uint16_t* src, int64_t rows, int K, int Kp, uint16_t* dst, hipStream_t st,
@@ -129,21 +239,24 @@ static hipError_t pad_rows(const uint16_t* src, int64_t rows, int K, int Kp, uin
                   dim3(256), st, src, rows, K, Kp, dst);
 }
 
+template <bool ACT4>
+static hipError_t launch_split(const Mx4Split& a, hipStream_t st, StageTimer* tm) {
+    auto ker = a.M <= 16 ? mx4_split_kernel<ACT4, 1> : a.M <= 32 ? mx4_split_kernel<ACT4, 2> : mx4_split_kernel<ACT4, 4>;
+    return launch(tm, "mx4_split", ker, dim3(a.n_items * a.hs + a.n_mt * a.n_nt * a.ks), dim3(256), st, a);
+}
+
 hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t* scales, bool act4, hipStream_t st,
                       StageTimer* tm) {
     LinearArgs L = L0;
-    SliceArgs sl = L.slice[0];
+    SliceArgs& sl = L.slice[0];
     const int M = L.M, N = sl.N;
     char* ws = static_cast<char*>(L.workspace);
-    const Mx4Space sp = mx4_space(M, L.K, L.S, L.r_max, act4);
+    const Mx4Space sp = mx4_space(M, N, L.K, L.S, L.r_max, act4);
     hipError_t e = hipSuccess;
-    const uint8_t *xc = nullptr, *xs = nullptr;
-    if (act4) {
-        xc = reinterpret_cast<uint8_t*>(ws + sp.codes);
-        xs = reinterpret_cast<uint8_t*>(ws + sp.scales);
-        e = mx4_quantize(1, L.X, 1, M, L.K, L.token_order, const_cast<uint8_t*>(xc), const_cast<uint8_t*>(xs), st, tm);
-        if (e != hipSuccess) return e;
-    }
+    uint8_t* xc = reinterpret_cast<uint8_t*>(ws + sp.codes);
+    uint8_t* xs = reinterpret_cast<uint8_t*>(ws + sp.scales);
+    if (act4) e = mx4_quantize(1, L.X, 1, M, L.K, L.token_order, xc, xs, st, tm);
+    if (e != hipSuccess) return e;
     if (L.K % 8) {
         const int Kp = (L.K + 7) / 8 * 8;
         uint16_t* xp = reinterpret_cast<uint16_t*>(ws + sp.xpad);
@@ -153,23 +266,42 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
         if (e != hipSuccess) return e;
         L.X = xp;
         sl.A_pool = ap;
-        L.K = Kp;
+        L.K = Kp;  // as many blocks and scale tiles
     }
-    float* h = reinterpret_cast<float*>(ws + sp.shrink);
-    Fuse f{L.token_order, L.slot_indptr, h, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
-           nullptr, (L.r_max + 7) & ~7};
-    const bool tiled = act4 && M > 64;
-    if (tiled && L.r_max % 8 == 0 && L.S <= kMetaSlots) {
-        f.ext = reinterpret_cast<uint16_t*>(h);
-        f.h = nullptr;
+    switch (mx4_path(M, act4)) {
+        case Mx4Path::kSplit: {
+            const Mx4SplitPlan p = mx4_split_plan(M, N, L.K);
+            const Mx4Split a{L.X, xc, xs, codes, scales, reinterpret_cast<float*>(ws + sp.own), M, N, L.K, p.n_mt,
+                             p.n_nt, p.ks, p.upb, L.token_order, reinterpret_cast<const Item*>(L.work), sl.A_pool,
+                             sl.rank, reinterpret_cast<float*>(ws + sp.h), L.adapters ? L.n_items : 0, L.r_max, p.hs,
+                             p.hkc};
+            e = act4 ? launch_split<true>(a, st, tm) : launch_split<false>(a, st, tm);
+            if (e != hipSuccess) return e;
+            return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
+        }
+        case Mx4Path::kTile4: {
+            float* h = reinterpret_cast<float*>(ws + sp.own);
+            Fuse f{L.token_order, L.slot_indptr, h, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
+                   nullptr, (L.r_max + 7) & ~7};
+            uint16_t* ext = nullptr;  // the expand as extra K steps, where its form allows
+            if (L.r_max % 8 == 0 && L.S <= kMetaSlots) {
+                ext = reinterpret_cast<uint16_t*>(h);
+                f.ext = ext;
+                f.h = nullptr;
+            }
+            if (L.adapters) e = tiled_shrink(L, sl, ws + sp.own, ext ? nullptr : h, ext, st, tm);
+            if (e != hipSuccess) return e;
+            return mx4_gemm(xc, xs, codes, scales, sl.Y, M, N, L.K, f, st, tm);
+        }
+        case Mx4Path::kDequant: break;
     }
-    if (L.adapters) {
-        e = tiled_shrink(L, sl, ws + sp.shrink, f.ext ? nullptr : h, const_cast<uint16_t*>(f.ext), st, tm);
-        if (e != hipSuccess) return e;
-    }
-    if (tiled) return mx4_gemm(xc, xs, codes, scales, sl.Y, M, N, L.K, f, st, tm);
-    return launch(tm, "mx4_rows", act4 ? mx4_rows_kernel<true> : mx4_rows_kernel<false>,
-                  dim3(cdiv(N, 64), cdiv(M, 64)), dim3(256), st, L.X, xc, xs, codes, scales, sl.Y, M, N, L.K, f);
+    // W's values are exact in bf16: the bf16 layer on them
+    uint16_t* W = reinterpret_cast<uint16_t*>(ws + sp.own);
+    e = mx4_dequantize(1, codes, scales, 1, N, L.K, W, st, tm);
+    if (e != hipSuccess) return e;
+    sl.W = W;
+    L.workspace = ws + sp.h;
+    return lora_forward_bf16(L, st, tm);
 }
 
 }  // namespace lora
