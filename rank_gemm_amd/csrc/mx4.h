@@ -58,6 +58,37 @@ __device__ __forceinline__ u32x4 mx4_bf16x8(uint32_t c, float sc) {
     return r;
 }
 
+// The other operand of products of 16-bit values with decoded 4-bit rows. A
+// lane (fr, fc) of the 4-bit side holds block fc of a 128-wide half tile, so
+// product m of the half (8 of each block's codes) needs k = 32 fc + 8 m of
+// the 16-bit row. Loaded in that order, a lane group's pieces lie 64 bytes
+// apart; so load i takes k = 32 i + 8 fc (64 consecutive bytes of a row) and
+// the four pieces are transposed across the four lane groups in registers.
+__device__ __forceinline__ void mx4_transpose(u32x4 (&x)[4]) {
+    auto swap32 = [](uint32_t& a, uint32_t& b) {  // a's upper half lanes <-> b's lower
+        const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+        a = r[0];
+        b = r[1];
+    };
+    auto swap16 = [](uint32_t& a, uint32_t& b) {  // a's odd groups of 16 <-> b's even ones
+        const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+        a = r[0];
+        b = r[1];
+    };
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        uint32_t a = x[0][d], b = x[1][d], c = x[2][d], e = x[3][d];
+        swap32(a, c);
+        swap32(b, e);
+        swap16(a, b);
+        swap16(c, e);
+        x[0][d] = a;
+        x[1][d] = b;
+        x[2][d] = c;
+        x[3][d] = e;
+    }
+}
+
 // Eight codes -> eight fp32 values of scale 1, times sc in fp32 (exact but
 // for results under 2^-149 or over the fp32 range).
 __device__ __forceinline__ void mx4_f32x8(uint32_t c, float sc, float (&v)[8]) {

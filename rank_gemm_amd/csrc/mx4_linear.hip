@@ -123,12 +123,17 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
             for (int h = 0; h < 2; ++h) {
                 u32x4 x[4][NT];
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
+                for (int i = 0; i < NT; ++i) {
+                    u32x4 v[4];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const int k = (u * 8 + h * 4 + fc) * 32 + 8 * m;
-                        x[m][i] = *or_zero(xrow[i] && k < a.K, xrow[i] + k);
+                    for (int m = 0; m < 4; ++m) {
+                        const int k = u * 256 + h * 128 + 32 * m + 8 * fc;
+                        v[m] = *or_zero(xrow[i] && k < a.K, xrow[i] + k);
                     }
+                    mx4_transpose(v);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) x[m][i] = v[m];
+                }
                 float sc[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sc[j] = mx4_scale(wsc[h] >> (8 * j) & 255);
