@@ -73,9 +73,13 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         // rows past M are not read: x comes from memory once per row and column tile
-        const int p = mt * 64 + 16 * i + fr;
-        if constexpr (ACT4) xq[i] = p < a.M ? a.xc + (int64_t)p * rb : nullptr;
-        else xrow[i] = p < a.M ? a.X + (int64_t)a.token_order[p] * a.K : nullptr;
+        const int p = mt * 64 + 16 * i + fr, pc = min(p, a.M - 1);
+        if constexpr (ACT4) {
+            xq[i] = p < a.M ? a.xc + (int64_t)pc * rb : nullptr;
+        } else {
+            const int tok = a.token_order[pc];  // loaded by every lane: no wait under a branch
+            xrow[i] = p < a.M ? a.X + (int64_t)tok * a.K : nullptr;
+        }
     }
     f32x4 acc[NT][4];
 #pragma unroll
@@ -163,6 +167,178 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
     }
 }
 
+// The 16-bit activations of more than 16 rows: their bytes, read once per
+// column tile, outweigh the 4-bit weights' (64 rows x 256 k are 32 KB, 64
+// columns of codes 8 KB), and the 64-column kernel above is bound by them. A
+// workgroup takes 128 columns over 16 NT rows with 8 waves, wave v columns
+// 32 (v % 4) .. + 31 over half v / 4 of every unit (two waves per SIMD: with
+// one, fragment reads, conversions and products wait on each other). A
+// unit's x goes to LDS by direct loads, once for the eight waves, while its
+// codes go to registers. In LDS a row of a unit is 32 chunks
+// of 16 bytes, chunk c of row r at slot c ^ (r % 16), through the source
+// address: the fragment reads of 16 rows then meet 16 distinct slots.
+constexpr int kWideCols = 128;
+
+template <int I, int N>
+__device__ __forceinline__ void tie(u32x4 (&a)[N]) {
+    if constexpr (I < N) {
+        asm volatile("" : "+v"(a[I]));
+        tie<I + 1, N>(a);
+    }
+}
+// at most P LDS reads of this wave outstanding; a is read after that
+template <int P, int N>
+__device__ __forceinline__ void reads_landed(u32x4 (&a)[N]) {
+    asm volatile("s_waitcnt lgkmcnt(%1)" : "+v"(a[0]) : "i"(P));
+    tie<1, N>(a);
+}
+
+// NS buffers: unit u + NS - 1 is loaded, into the buffer of unit u - 1, when
+// every wave has passed the barrier of unit u. Loads go through buffer
+// resources (x, the tile's code rows, its scales): codes past a row's end are
+// the next row's, or zeros at the end, and meet zeros of x.
+template <int NT, int NS>
+__global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
+    constexpr int ROWS = 16 * NT, UNIT = ROWS * 32, DMA = ROWS / 2 / 8;  // chunks of a unit; x loads per wave
+    constexpr int LOADS = 3 + DMA;                                      // a wave's loads of a unit
+    __shared__ u32x4 lds[NS * UNIT];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n_shrink = a.n_items * a.hs;
+    static_assert(NS * UNIT >= 8 * 4 * 64 && (NS - 2) * LOADS < 64, "shrink scratch, wait counter");
+    if ((int)blockIdx.x < n_shrink) {
+        const int item = blockIdx.x % a.n_items, hz = blockIdx.x / a.n_items;
+        const Item it = a.work[item];
+        const int r = a.rank[it.slot];
+        if (r == 0) return;
+        const int kbeg = hz * a.hkc, kend = min(a.K, kbeg + a.hkc);
+        const ShrinkOut out{a.part_h + (int64_t)hz * a.M * a.r_max, nullptr, 0, 0.f};
+        shrink_item<8>(a.X, a.A_pool, r, a.token_order, it, out, a.K, kbeg, kend, a.r_max,
+                       reinterpret_cast<f32x4*>(lds));
+        return;
+    }
+    const int n_bt = (a.n_nt + 1) / 2, b = blockIdx.x - n_shrink, tiles = a.n_mt * n_bt;
+    const int kz = b / tiles, t = b - kz * tiles, mt = t / n_bt, bt = t - mt * n_bt;
+    const int fr = lane & 15, fc = lane >> 4;
+    const int64_t rb = mx4_row_bytes(a.K), kts = mx4_k_tiles(a.K);
+    const int u0 = kz * a.upb, u1 = min((int)kts, u0 + a.upb);
+    const int half = wave >> 2, n0 = bt * kWideCols, c0 = n0 + (wave & 3) * 32, nt = c0 >> 6, cb = c0 >> 4 & 3;
+    const int g0 = n0 >> 6, ng = min(a.n_nt - g0, 2);  // scale groups of the tile
+    const brsrc rW = make_rsrc(a.wc + n0 * rb, (uint32_t)(min(a.N - n0, kWideCols) * rb));
+    const brsrc rS = make_rsrc(a.ws + g0 * kts * kMxTileBytes, (uint32_t)(ng * kts * kMxTileBytes));
+    const brsrc rX = make_rsrc(a.X, (uint32_t)a.M * (uint32_t)a.K * 2u);
+    uint32_t woff[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        woff[j] = (uint32_t)((min(c0 + 16 * j + fr, a.N - 1) - n0) * rb) + half * 64 + fc * 16;
+    const uint32_t soff = (uint32_t)((min(nt, a.n_nt - 1) - g0) * kts * kMxTileBytes) + lane * 8 + half * 4;
+    // x load d of this wave fetches rows 2 (DMA wave + d) + lane / 32 of a unit
+    uint32_t xoff[DMA];
+    int xk[DMA];
+#pragma unroll
+    for (int d = 0; d < DMA; ++d) {
+        const int r = 2 * (DMA * wave + d) + (lane >> 5), p = mt * 64 + r;
+        const int tok = a.token_order[min(p, a.M - 1)];
+        const int k = ((lane & 31) ^ (r & 15)) * 8;
+        xk[d] = p < a.M ? k : a.K;  // rows past M: past the row's end, zeros
+        xoff[d] = ((uint32_t)tok * (uint32_t)a.K + k) * 2u;
+    }
+    u32x4 w[NS][2];
+    uint32_t s[NS];
+    // units past the split's last load zeros of x, so that every unit waits on
+    // the same number of loads
+    auto load = [&](int u, auto bc) {
+        constexpr int buf = decltype(bc)::value;
+        const int k = u < u1 ? u * 256 : a.K, uc = min(u, u1 - 1);
+        s[buf] = __builtin_amdgcn_raw_buffer_load_b32(rS, soff, uc * kMxTileBytes, 0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)  // non-temporal: W is read once
+            w[buf][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rW, woff[j], uc * 128, 2));
+#pragma unroll
+        for (int d = 0; d < DMA; ++d)
+            bdma16(rX, k + xk[d] < a.K ? xoff[d] : kOutOfRange, (uint32_t)k * 2u, lds + buf * UNIT + (DMA * wave + d) * 64);
+        issue_fence();
+    };
+    f32x4 acc[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto unit = [&](int u, auto bc) {
+        constexpr int buf = decltype(bc)::value;
+        vm_landed<(NS - 2) * LOADS>();  // this unit's loads landed, later ones may not
+        stage_barrier();
+        load(u + NS - 1, std::integral_constant<int, (buf + NS - 1) % NS>{});
+        // products 0 .. 3 of the wave's half; the next one's fragments are
+        // read while a product runs
+        const uint32_t row = lds_offset(lds + buf * UNIT) + fr * 512;
+        u32x4 x[2][NT];
+        auto read = [&](auto mc, u32x4 (&f)[NT]) {
+            const uint32_t at = row + (((half * 4 + fc) * 4 + decltype(mc)::value) ^ fr) * 16;
+            f[0] = lds_read16<0>(at);
+            f[1] = lds_read16<16 * 512>(at);
+            if constexpr (NT > 2) {
+                f[2] = lds_read16<32 * 512>(at);
+                f[3] = lds_read16<48 * 512>(at);
+            }
+        };
+        read(std::integral_constant<int, 0>{}, x[0]);
+        float sc[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sc[j] = mx4_scale(s[buf] >> (8 * (cb + j)) & 255);
+        auto product = [&](auto mc) {
+            constexpr int m = decltype(mc)::value;
+            if constexpr (m < 3) {
+                read(std::integral_constant<int, m + 1>{}, x[(m + 1) & 1]);
+                reads_landed<NT>(x[m & 1]);
+            } else {
+                reads_landed<0>(x[m & 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x4 wf = mx4_bf16x8(w[buf][j][m], sc[j]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) acc[i][j] = mfma16x16x32(x[m & 1][i], wf, acc[i][j]);
+            }
+        };
+        product(std::integral_constant<int, 0>{});
+        product(std::integral_constant<int, 1>{});
+        product(std::integral_constant<int, 2>{});
+        product(std::integral_constant<int, 3>{});
+    };
+    load(u0, std::integral_constant<int, 0>{});
+    if constexpr (NS > 2) load(u0 + 1, std::integral_constant<int, 1>{});
+    if constexpr (NS > 3) load(u0 + 2, std::integral_constant<int, 2>{});
+    for (int u = u0; u < u1; u += NS) {
+        unit(u, std::integral_constant<int, 0>{});
+        if (u + 1 >= u1) break;  // uniform, as the others
+        unit(u + 1, std::integral_constant<int, 1>{});
+        if constexpr (NS > 2) {
+            if (u + 2 >= u1) break;
+            unit(u + 2, std::integral_constant<int, 2>{});
+        }
+        if constexpr (NS > 3) {
+            if (u + 3 >= u1) break;
+            unit(u + 3, std::integral_constant<int, 3>{});
+        }
+    }
+    // the halves' sums added; no load into LDS is in flight past this
+    vm_landed<0>();
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(lds) + (wave & 3) * 2 * NT * 64;
+    static_assert(NS * UNIT >= 4 * 2 * NT * 64, "reduction scratch");
+    if (half == 1) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) red[(i * 2 + j) * 64 + lane] = acc[i][j];
+    }
+    __syncthreads();
+    if (half == 1 || nt >= a.n_nt) return;
+    f32x4* out = reinterpret_cast<f32x4*>(a.part) + ((int64_t)(kz * a.n_mt + mt) * a.n_nt + nt) * 1024;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) out[(i * 4 + cb + j) * 64 + lane] = acc[i][j] + red[(i * 2 + j) * 64 + lane];
+}
+
 // rows of any width -> rows of Kp elements (a multiple of 8), zeros behind
 // the row's end: the kernels read rows in 16-byte pieces
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t rows, int K, int Kp,
@@ -175,25 +351,47 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 // The path of a call, by its sizes and act alone (a base-only call takes the
 // same one).
 enum class Mx4Path { kSplit, kTile4, kDequant };
-constexpr int kMx4SplitRows = 64;
-static Mx4Path mx4_path(int M, bool act4) {
-    if (M <= kMx4SplitRows) return Mx4Path::kSplit;
-    return act4 ? Mx4Path::kTile4 : Mx4Path::kDequant;
+static Mx4Path mx4_path(int M, int N, int K, bool act4) {
+    if (act4) return (int64_t)cdiv(M, 64) * cdiv(N, 64) <= 256 ? Mx4Path::kSplit : Mx4Path::kTile4;
+    return gemm_bf16_plan(M, N, K).nsub != 0 && (int64_t)M * K * 2 < int64_t(1) << 31 ? Mx4Path::kSplit
+                                                                                     : Mx4Path::kDequant;
 }
 
-// K splits of the decode path: about 512 workgroups, a unit for every wave
+static bool mx4_wide(int M, bool act4) { return !act4 && M > 16; }
+
+// K splits of the decode path. The shrink's work items count as tiles, as many
+// as M rows over S slots can give, so that a base-only call splits alike: an
+// item moves about the bytes of a unit per 256 k. The wide kernel takes the
+// splits of the least estimated time: 1.5 us per unit and workgroup of a CU
+// (two on one CU take about twice as long), and each split's partials,
+// written and read at 5 TB/s. The shrink takes K ranges of a
+// split's length, 8 at most.
 struct Mx4SplitPlan {
     int n_mt, n_nt, ks, upb, hs, hkc;
 };
-static Mx4SplitPlan mx4_split_plan(int M, int N, int K) {
+static Mx4SplitPlan mx4_split_plan(int M, int N, int K, int S, bool act4) {
     Mx4SplitPlan p{};
     p.n_mt = cdiv(M, 64);
     p.n_nt = cdiv(N, 64);
-    const int kts = (int)mx4_k_tiles(K), tiles = p.n_mt * p.n_nt;
-    const int want = tiles >= 512 ? 1 : 512 / tiles;
-    p.upb = (cdiv(kts, want) + 3) / 4 * 4;
+    const int kts = (int)mx4_k_tiles(K), items = M / 16 + min(S - 1, M);
+    if (mx4_wide(M, act4)) {
+        const int64_t tiles = (int64_t)p.n_mt * cdiv(N, kWideCols) + items;
+        double best = 0.0;
+        for (int ks = 1; ks <= 16 && ks <= kts; ++ks) {
+            const int upb = cdiv(kts, ks);
+            const int64_t rounds = (tiles * cdiv(kts, upb) + 255) / 256;  // workgroups per CU
+            const double cost = upb * 1.5 * rounds + ks * (M * 8e-6 / 5.0) * N;
+            if (p.upb == 0 || cost < best) {
+                best = cost;
+                p.upb = upb;
+            }
+        }
+    } else {  // a unit for every wave
+        const int tiles = p.n_mt * p.n_nt;
+        p.upb = (cdiv(kts, max(1, 512 / (tiles + items))) + 3) / 4 * 4;
+    }
     p.ks = cdiv(kts, p.upb);
-    p.hkc = max(256, (cdiv(K, 8) + 31) / 32 * 32);
+    p.hkc = max(p.upb * 256, (cdiv(K, 8) + 31) / 32 * 32);
     p.hs = cdiv(K, p.hkc);
     return p;
 }
@@ -217,9 +415,9 @@ static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
     s.apad = take(K % 8 ? (size_t)S * r_max * Kp * 2 : 0);
     s.codes = take(act4 ? (size_t)M * mx4_row_bytes(K) : 0);
     s.scales = take(act4 ? (size_t)mx4_scale_bytes(M, K) : 0);
-    switch (mx4_path(M, act4)) {
+    switch (mx4_path(M, N, K, act4)) {
         case Mx4Path::kSplit: {
-            const Mx4SplitPlan p = mx4_split_plan(M, N, K);
+            const Mx4SplitPlan p = mx4_split_plan(M, N, K, S, act4);
             s.own = take((size_t)p.ks * p.n_mt * p.n_nt * 64 * 64 * sizeof(float));
             s.h = take((size_t)p.hs * M * r_max * sizeof(float));
             break;
@@ -244,9 +442,12 @@ static hipError_t pad_rows(const uint16_t* src, int64_t rows, int K, int Kp, uin
                   dim3(256), st, src, rows, K, Kp, dst);
 }
 
-template <bool ACT4>
-static hipError_t launch_split(const Mx4Split& a, hipStream_t st, StageTimer* tm) {
-    auto ker = a.M <= 16 ? mx4_split_kernel<ACT4, 1> : a.M <= 32 ? mx4_split_kernel<ACT4, 2> : mx4_split_kernel<ACT4, 4>;
+static hipError_t launch_split(const Mx4Split& a, bool act4, hipStream_t st, StageTimer* tm) {
+    if (mx4_wide(a.M, act4))
+        return launch(tm, "mx4_wide", a.M <= 32 ? mx4_wide_kernel<2, 3> : mx4_wide_kernel<4, 3>,
+                      dim3(a.n_items * a.hs + a.n_mt * cdiv(a.N, kWideCols) * a.ks), dim3(512), st, a);
+    auto ker = !act4 ? mx4_split_kernel<false, 1>
+               : a.M <= 16 ? mx4_split_kernel<true, 1> : a.M <= 32 ? mx4_split_kernel<true, 2> : mx4_split_kernel<true, 4>;
     return launch(tm, "mx4_split", ker, dim3(a.n_items * a.hs + a.n_mt * a.n_nt * a.ks), dim3(256), st, a);
 }
 
@@ -273,14 +474,14 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
         sl.A_pool = ap;
         L.K = Kp;  // as many blocks and scale tiles
     }
-    switch (mx4_path(M, act4)) {
+    switch (mx4_path(M, N, L.K, act4)) {
         case Mx4Path::kSplit: {
-            const Mx4SplitPlan p = mx4_split_plan(M, N, L.K);
+            const Mx4SplitPlan p = mx4_split_plan(M, N, L.K, L.S, act4);
             const Mx4Split a{L.X, xc, xs, codes, scales, reinterpret_cast<float*>(ws + sp.own), M, N, L.K, p.n_mt,
                              p.n_nt, p.ks, p.upb, L.token_order, reinterpret_cast<const Item*>(L.work), sl.A_pool,
                              sl.rank, reinterpret_cast<float*>(ws + sp.h), L.adapters ? L.n_items : 0, L.r_max, p.hs,
                              p.hkc};
-            e = act4 ? launch_split<true>(a, st, tm) : launch_split<false>(a, st, tm);
+            e = launch_split(a, act4, st, tm);
             if (e != hipSuccess) return e;
             return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
         }
