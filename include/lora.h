@@ -481,13 +481,13 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  *            choice whose id is outside [0, E) adds nothing, and a token may
  *            name an expert twice
  *   y        dev bf16 [T][H] out, overwritten completely; must not alias x
- *   workspace dev, at least lora_moe_experts_workspace_bytes(T, I, k) bytes
+ *   workspace dev, at least lora_moe_experts_workspace_bytes(T, H, I, k) bytes
  * The terms of a token are added in the order of j: equal inputs give equal
  * bits. Products take bf16 operands with fp32 sums; the inner values
  * silu(.) * (.) are carried as two bf16 halves (16 bits of mantissa).
  *
  * H must be a multiple of 8, and I too for LORA_BF16; x, router and the
- * weights start on 16-byte boundaries; 1 <= E <= LORA_MOE_MAX_EXPERTS,
+ * weights start on 16-byte, y on 8-byte boundaries; 1 <= E <= LORA_MOE_MAX_EXPERTS,
  * 1 <= k <= min(E, LORA_MOE_MAX_K) (lora_moe_experts: k may exceed E),
  * T k <= LORA_MOE_MAX_PAIRS. Asynchronous on `stream`. Errors: LORA_EINVAL,
  * LORA_ESPACE, LORA_EHIP. T == 0 launches nothing.
@@ -504,7 +504,7 @@ typedef struct lora_moe_weights {
     const void *gate_scales, *up_scales, *down_scales; /* LORA_MX4 only */
 } lora_moe_weights;
 
-size_t lora_moe_experts_workspace_bytes(int T, int I, int k);
+size_t lora_moe_experts_workspace_bytes(int T, int H, int I, int k);
 int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* weights, const lora_moe_weights* w,
                      int T, int H, int I, int E, int k, void* y, void* workspace, size_t workspace_bytes,
                      void* stream);

@@ -182,6 +182,15 @@ inline bool moe_sizes(int T, int H, int E, int k) {
            T <= LORA_MOE_MAX_PAIRS / k;
 }
 
+// The experts' kernels address one matrix, x and the inner values through
+// buffer resources: each under 2 GiB.
+inline bool moe_fits(int form, int T, int H, int I, int k) {
+    const int64_t lim = int64_t(1) << 31;
+    const int64_t row_h = form == LORA_MX4 ? lora::mx4_row_bytes(H) : (int64_t)H * 2;
+    const int64_t row_i = form == LORA_MX4 ? lora::mx4_row_bytes(I) : (int64_t)I * 2;
+    return I * row_h < lim && H * row_i < lim && (int64_t)T * H * 2 < lim && (int64_t)T * k * 4 * (I + 127) < lim;
+}
+
 }  // namespace
 
 extern "C" {
@@ -675,25 +684,26 @@ int lora_moe_route(const void* x, const void* router, int T, int H, int E, int k
                : LORA_EHIP;
 }
 
-size_t lora_moe_experts_workspace_bytes(int T, int I, int k) {
-    return T < 0 || I < 1 || k < 1 ? 0 : lora::moe_experts_workspace(T, I, k);
+size_t lora_moe_experts_workspace_bytes(int T, int H, int I, int k) {
+    return T < 0 || H < 1 || I < 1 || k < 1 ? 0 : lora::moe_experts_workspace(T, H, I, k);
 }
 
 int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* weights, const lora_moe_weights* w,
                      int T, int H, int I, int E, int k, void* y, void* workspace, size_t workspace_bytes,
                      void* stream) {
     if ((form != LORA_BF16 && form != LORA_MX4) || !moe_sizes(T, H, E, k) || I < 1 ||
-        I > LORA_MX4_MAX_ROWS || H > LORA_MX4_MAX_ROWS || (form == LORA_BF16 && I % 8 != 0) || !w)
+        I > LORA_MX4_MAX_ROWS || H > LORA_MX4_MAX_ROWS || (form == LORA_BF16 && I % 8 != 0) || !w ||
+        !moe_fits(form, T, H, I, k))
         return LORA_EINVAL;
     if (T == 0) return LORA_OK;
-    if (!x || !ids || !weights || !y || y == x || !aligned(x, 16) || !aligned(y, 2)) return LORA_EINVAL;
+    if (!x || !ids || !weights || !y || y == x || !aligned(x, 16) || !aligned(y, 8)) return LORA_EINVAL;
     const void* data[3] = {w->gate, w->up, w->down};
     const void* scales[3] = {w->gate_scales, w->up_scales, w->down_scales};
     for (int i = 0; i < 3; ++i) {
         if (!data[i] || !aligned(data[i], 16) || y == data[i]) return LORA_EINVAL;
         if (form == LORA_MX4 && (!scales[i] || !aligned(scales[i], 8) || y == scales[i])) return LORA_EINVAL;
     }
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_moe_experts_workspace_bytes(T, I, k))
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < lora_moe_experts_workspace_bytes(T, H, I, k))
         return LORA_ESPACE;
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);

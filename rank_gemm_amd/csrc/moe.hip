@@ -9,10 +9,10 @@
 // Route: one wave per (expert, token) sums the logit in 64 bits, so that the
 // choice among close logits does not hang on the rounding of a sum; one wave
 // per token then takes the k largest.
-// Experts: two kernels. gate_up: a workgroup takes one reached expert and 32
-// inner columns (32 gate and 32 up rows); down: a workgroup takes 16 output
-// columns and goes through every reached expert, so that a token's k terms
-// meet in one workgroup and are added in the order of j.
+// Experts: gate_up (a workgroup takes one reached expert and 32 inner columns:
+// 32 gate and 32 up rows), down (one reached expert and 64 output columns),
+// combine (the weighted sum of a token's k terms, in the order of j).
+#include "fuse.h"
 #include "kernels.h"
 #include "mx4.h"
 
@@ -198,86 +198,104 @@ __device__ __forceinline__ void moe_plan(const int32_t* __restrict__ ids, int P,
     __syncthreads();
 }
 
-// 256 k of RB 16-row blocks of one expert's matrix, as a wave holds them: 2
-// (4-bit) or 8 (bf16) 16-byte pieces per row and lane.
-template <bool MX, int RB>
-struct WTile {
-    u32x4 w[RB][MX ? 2 : 8];
-    u32x2 sc;  // 4-bit: scale words of the tile's 64-row group
-};
-
-// rows r0 .. r0 + 16 RB (clamped to N rows) of expert e at k tile kt
-template <bool MX, int RB>
-__device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const MoeWeights& W, int e, int N, int K, int r0, int kt,
-                                           int lane) {
-    const int fr = lane & 15, fc = lane >> 4;
-    if constexpr (MX) {
-        const int64_t rb = mx4_row_bytes(K), kts = mx4_k_tiles(K);
-        const uint8_t* base = static_cast<const uint8_t*>(W.data) + (int64_t)e * N * rb;
-        t.sc = *reinterpret_cast<const u32x2*>(W.scales + (int64_t)e * mx4_scale_bytes(N, K) +
-                                               ((int64_t)(r0 >> 6) * kts + kt) * kMxTileBytes + lane * 8);
-#pragma unroll
-        for (int j = 0; j < RB; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int blk = kt * 8 + h * 4 + fc;
-                t.w[j][h] = *or_zero(blk * 32 < K, base + (int64_t)min(r0 + 16 * j + fr, N - 1) * rb + blk * 16);
-            }
-    } else {
-        const uint16_t* base = static_cast<const uint16_t*>(W.data) + (int64_t)e * N * K;
-#pragma unroll
-        for (int j = 0; j < RB; ++j)
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int k = kt * 256 + 32 * s + 8 * fc;
-                t.w[j][s] = *or_zero(k < K, base + (int64_t)min(r0 + 16 * j + fr, N - 1) * K + k);
-            }
-    }
-}
-
-// A tile's products go in steps: 128 k (4-bit, 2 a tile) or 32 k (bf16, 8), for
-// each of which a lane holds kPieces pieces of the 16-bit operand.
+// A tile's products go in steps: 128 k (4-bit, 2 a tile of 256 k) or 32 k
+// (bf16, 4 a tile of 128 k), for each of which a lane holds kPieces pieces of
+// the 16-bit operand.
 template <bool MX>
-constexpr int kSteps = MX ? 2 : 8;
+constexpr int kTileK = MX ? 256 : 128;
+template <bool MX>
+constexpr int kSteps = MX ? 2 : 4;
 template <bool MX>
 constexpr int kPieces = MX ? 4 : 1;
 
-// acc[j] += (16-row block j of the tile) (x)^T over step i. j0: the tile's
-// first 16-row block in its group of four.
+// RB 16-row blocks of one expert's matrix from row r0 on, read through buffer
+// resources: per-lane row offsets, the k of a tile in the uniform offset.
+// Codes or values past a row's end are the next row's (zeros at the matrix's
+// end); they meet zeros of the other operand.
 template <bool MX, int RB>
-__device__ __forceinline__ void mac_wtile(f32x4 (&acc)[RB], const WTile<MX, RB>& t, int j0, int i,
-                                          const u32x4 (&x)[kPieces<MX>]) {
+struct WRows {
+    brsrc data, scales;
+    uint32_t off[RB], soff;
+};
+template <bool MX, int RB>
+__device__ __forceinline__ WRows<MX, RB> rows_of(const MoeWeights& W, int e, int N, int K, int r0, int lane) {
+    const int fr = lane & 15, fc = lane >> 4;
+    const int64_t rb = MX ? mx4_row_bytes(K) : (int64_t)K * 2, kts = mx4_k_tiles(K);
+    const int64_t sb = mx4_scale_bytes(N, K);
+    WRows<MX, RB> r;
+    r.data = make_rsrc(static_cast<const uint8_t*>(W.data) + (int64_t)e * N * rb, (uint32_t)(N * rb));
+    r.scales = make_rsrc(MX ? W.scales + (int64_t)e * sb : nullptr, MX ? (uint32_t)sb : 0u);
+    r.soff = (uint32_t)((r0 >> 6) * kts * kMxTileBytes) + lane * 8;
+#pragma unroll
+    for (int j = 0; j < RB; ++j) r.off[j] = (uint32_t)(min(r0 + 16 * j + fr, N - 1) * rb) + fc * 16;
+    return r;
+}
+
+// A tile of those rows, as a wave holds it: a 16-byte piece per row, step and lane.
+template <bool MX, int RB>
+struct WTile {
+    u32x4 w[RB][kSteps<MX>];
+    u32x2 sc;  // 4-bit: scale words of the tile's 64-row group
+};
+template <bool MX, int RB>
+__device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>& r, int kt) {
+    constexpr int TB = kTileK<MX> * (MX ? 1 : 4) / 2;  // bytes of a row in a tile
+    if constexpr (MX)
+        t.sc = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r.scales, r.soff, kt * kMxTileBytes, 0));
+#pragma unroll
+    for (int s = 0; s < kSteps<MX>; ++s)
+#pragma unroll
+        for (int j = 0; j < RB; ++j)  // non-temporal: read once
+            t.w[j][s] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r.data, r.off[j], kt * TB + s * 64, 2));
+}
+
+// acc[c][j] += (16-row block j of the tile) (x[c][0] + x[c][1] + ..)^T over
+// step i for NC column tiles of NX operands each, every decoded weight used
+// for all of them. j0: the tile's first 16-row block in its group of four.
+template <bool MX, int RB, int NC, int NX>
+__device__ __forceinline__ void mac_wtile(f32x4 (&acc)[NC][RB], const WTile<MX, RB>& t, int j0, int i,
+                                          const u32x4 (&x)[NC][NX][kPieces<MX>]) {
     if constexpr (MX) {
         float sc[RB];
 #pragma unroll
         for (int j = 0; j < RB; ++j) sc[j] = mx4_scale(t.sc[i] >> (8 * (j0 + j)) & 255);
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < 4; ++m) {
 #pragma unroll
-            for (int j = 0; j < RB; ++j) acc[j] = mfma16x16x32(mx4_bf16x8(t.w[j][i][m], sc[j]), x[m], acc[j]);
+            for (int j = 0; j < RB; ++j) {
+                const u32x4 wf = mx4_bf16x8(t.w[j][i][m], sc[j]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int n = 0; n < NX; ++n) acc[c][j] = mfma16x16x32(wf, x[c][n][m], acc[c][j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one piece's decoded weights at a time
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < RB; ++j) acc[j] = mfma16x16x32(t.w[j][i], x[0], acc[j]);
+        for (int j = 0; j < RB; ++j)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int n = 0; n < NX; ++n) acc[c][j] = mfma16x16x32(t.w[j][i], x[c][n][0], acc[c][j]);
     }
 }
 
-// One lane's row of 16-bit values (null: zeros) at tile kt as mac_wtile takes
-// it. K: values in the row; PERM: stored in the 4-bit side's order (moe_at).
+// One lane's row of 16-bit values at tile kt and step i as mac_wtile takes it.
+// off: byte offset of the row's first value in x (kOutOfRange: zeros); K:
+// values in the row; PERM: stored in the 4-bit side's order (moe_at).
 template <bool MX, bool PERM>
-__device__ __forceinline__ void load_x(const uint16_t* row, int K, int kt, int i, int lane, u32x4 (&v)[kPieces<MX>]) {
-    const int fc = lane >> 4;
-    if constexpr (MX) {
-        const int k0 = kt * 256 + i * 128;
+__device__ __forceinline__ void load_x(brsrc x, uint32_t off, int K, int kt, int i, int lane,
+                                       u32x4 (&v)[kPieces<MX>]) {
+    const int fc = lane >> 4, k0 = kt * kTileK<MX> + i * (MX ? 128 : 32);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int k = PERM ? k0 + 32 * fc + 8 * m : k0 + 32 * m + 8 * fc;
-            v[m] = *or_zero(row && k < K, row + k0 + 32 * m + 8 * fc);
-        }
-        if constexpr (!PERM) mx4_transpose(v);
-    } else {
-        const int k = kt * 256 + 32 * i + 8 * fc;
-        v[0] = *or_zero(row && k < K, row + k);
+    for (int m = 0; m < kPieces<MX>; ++m) {
+        const int k = PERM && MX ? 32 * fc + 8 * m : 32 * m + 8 * fc;
+        v[m] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             x, k0 + k < K ? off + fc * 16 : kOutOfRange, k0 * 2 + m * 64, 0));
     }
+    if constexpr (MX && !PERM) mx4_transpose(v);
 }
 
 // The inner values of a pair: rows of whole 128-value groups, hi then lo;
@@ -295,147 +313,175 @@ __device__ __forceinline__ int moe_at(int i) {
 // over all of H, the k tiles dealt round the waves and their sums added in
 // wave order; then silu(g) * u, kept as bf16 hi + lo (two products in the
 // down kernel, which waits on memory: the inner values keep 16 bits of
-// mantissa instead of 8) in act[pair][2][moe_act_row(I)].
+// mantissa instead of 8) in act[pair][2][moe_act_row(I)]. A pass takes 16 or,
+// where more are left, 32 of the expert's pairs.
 template <bool MX, int NW>
-__global__ __launch_bounds__(64 * NW) void moe_gate_up_kernel(MoeArgs a, uint16_t* __restrict__ act) {
+__global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint16_t* __restrict__ act) {
     __shared__ MoePlan pl;
     __shared__ f32x4 red[NW][4][64];
     const int P = a.T * a.k;
     moe_plan(a.ids, P, a.E, pl);
     if ((int)blockIdx.y >= pl.n) return;
-    const int e = pl.expert[blockIdx.y], lo = pl.first[blockIdx.y], hi = pl.first[blockIdx.y + 1];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int r0 = blockIdx.x * 32, kts = (a.H + 255) / 256, Ir = moe_act_row(a.I);
-    for (int t0 = lo; t0 < hi; t0 += 16) {
-        const int p = t0 + (lane & 15);
-        const uint16_t* xr = p < hi ? a.X + (int64_t)(pl.order[p] / a.k) * a.H : nullptr;
-        f32x4 g[2], u[2];
+    const int e = __builtin_amdgcn_readfirstlane(pl.expert[blockIdx.y]);
+    const int lo = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y]);
+    const int hi = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y + 1]);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r0 = blockIdx.x * 32, kts = (a.H + kTileK<MX> - 1) / kTileK<MX>, Ir = moe_act_row(a.I);
+    const auto rg = rows_of<MX, 2>(a.gate, e, a.I, a.H, r0, lane), ru = rows_of<MX, 2>(a.up, e, a.I, a.H, r0, lane);
+    const brsrc rx = make_rsrc(a.X, (uint32_t)a.T * (uint32_t)a.H * 2u);
+    auto pass = [&](int t0, auto nc) {
+        constexpr int NC = decltype(nc)::value;
+        uint32_t xo[NC];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) g[j] = u[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < NC; ++c) {
+            const int p = t0 + 16 * c + (lane & 15);
+            xo[c] = p < hi ? (uint32_t)(pl.order[p] / a.k) * (uint32_t)a.H * 2u : kOutOfRange;
+        }
+        f32x4 g[NC][2], u[NC][2];
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) g[c][j] = u[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kt = wave; kt < kts; kt += NW) {
             WTile<MX, 2> wg, wu;
-            load_wtile(wg, a.gate, e, a.I, a.H, r0, kt, lane);
-            load_wtile(wu, a.up, e, a.I, a.H, r0, kt, lane);
+            load_wtile(wg, rg, kt);
+            load_wtile(wu, ru, kt);
 #pragma unroll
             for (int i = 0; i < kSteps<MX>; ++i) {
-                u32x4 x[kPieces<MX>];
-                load_x<MX, false>(xr, a.H, kt, i, lane, x);
+                u32x4 x[NC][1][kPieces<MX>];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) load_x<MX, false>(rx, xo[c], a.H, kt, i, lane, x[c][0]);
                 mac_wtile(g, wg, r0 >> 4 & 3, i, x);
                 mac_wtile(u, wu, r0 >> 4 & 3, i, x);
             }
         }
-        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            red[wave][j][lane] = g[j];
-            red[wave][2 + j][lane] = u[j];
-        }
-        __syncthreads();
-        // thread (j, l, c): element c of lane l's result in row block j
-        const int j = tid >> 8 & 1, l = tid >> 2 & 63, c = tid & 3;
-        if (tid >= 512) continue;  // uniform for a wave; the next barrier is met by all
-        float gs = 0.f, us = 0.f;
+        for (int cc = 0; cc < NC; ++cc) {
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            gs += red[w][j][l][c];
-            us += red[w][2 + j][l][c];
+            for (int j = 0; j < 2; ++j) {
+                red[wave][j][lane] = g[cc][j];
+                red[wave][2 + j][lane] = u[cc][j];
+            }
+            __syncthreads();
+            // thread (j, l, c): element c of lane l's result in row block j
+            const int j = tid >> 8 & 1, l = tid >> 2 & 63, c = tid & 3;
+            float gs = 0.f, us = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                gs += red[w][j][l][c];
+                us += red[w][2 + j][l][c];
+            }
+            const int q = t0 + 16 * cc + (l & 15), i = r0 + 16 * j + 4 * (l >> 4) + c;
+            if (q < hi && i < moe_inner(a.I)) {
+                const float v = i < a.I ? gs / (1.f + expf(-gs)) * us : 0.f;
+                uint16_t* ap = act + (int64_t)pl.order[q] * 2 * Ir + moe_at<MX>(i);
+                const uint16_t h = f32_to_bf16(v);
+                ap[0] = h;
+                // an infinite or NaN value has no remainder
+                const float rest = v - bf16_to_f32(h);
+                ap[Ir] = rest == rest ? f32_to_bf16(rest) : uint16_t(0);
+            }
         }
-        const int q = t0 + (l & 15), i = r0 + 16 * j + 4 * (l >> 4) + c;
-        if (q < hi && i < moe_inner(a.I)) {
-            const float v = i < a.I ? gs / (1.f + expf(-gs)) * us : 0.f;
-            uint16_t* ap = act + (int64_t)pl.order[q] * 2 * Ir + moe_at<MX>(i);
-            const uint16_t h = f32_to_bf16(v);
-            ap[0] = h;
-            // an infinite or NaN value has no remainder
-            const float rest = v - bf16_to_f32(h);
-            ap[Ir] = rest == rest ? f32_to_bf16(rest) : uint16_t(0);
-        }
-    }
+    };
+    int t0 = lo;
+    for (; hi - t0 > 16; t0 += 32) pass(t0, std::integral_constant<int, 2>{});
+    if (t0 < hi) pass(t0, std::integral_constant<int, 1>{});
 }
 
-// Workgroup: output columns 16 bx .. + 15 of every pair. Work items (active
-// expert, up to 32 of its pairs, k tiles of class kc mod KC) go round the
-// waves; an item's results land in o[kc][pair position][column], each written
-// once, and are added in the order of kc and then of j. A wave's tiles form
-// one sequence over all its items, the next tile's weights in flight while
-// the current one is multiplied.
-constexpr int kMoeOutFloats = kMoeMaxPairs * 16;  // 32 KB
+// Workgroup (output columns 64 bx .. + 63, active expert by): the down
+// product of the expert's pairs, k tiles dealt round the waves, sums in wave
+// order, into o[pair][H] in fp32; every pair has one expert, so each element
+// is written once.
 template <bool MX, int NW>
-__global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs a, const uint16_t* __restrict__ act, int KC) {
+__global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(MoeArgs a, const uint16_t* __restrict__ act,
+                                                              float* __restrict__ o) {
     __shared__ MoePlan pl;
-    __shared__ float o[kMoeOutFloats];
+    __shared__ f32x4 red[NW][4][64];
     const int P = a.T * a.k;
     moe_plan(a.ids, P, a.E, pl);
+    if ((int)blockIdx.y >= pl.n) return;
+    const int e = __builtin_amdgcn_readfirstlane(pl.expert[blockIdx.y]);
+    const int lo = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y]);
+    const int hi = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y + 1]);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r0 = blockIdx.x * 16, kts = (a.I + 255) / 256, Ip = moe_inner(a.I), Ir = moe_act_row(a.I);
-    const int n_items = pl.n * KC;
-    int it = wave, kt = 0, t0 = 0;  // the tile in hand: item, k tile, first pair of the pass
-    auto locate = [&](int item) {
-        kt = item % KC;
-        t0 = pl.first[min(item, n_items - 1) / KC];
-    };
-    WTile<MX, 1> w;
-    auto fetch = [&](WTile<MX, 1>& t, int item, int k_tile) {
-        load_wtile(t, a.down, pl.expert[item / KC], a.H, a.I, r0, k_tile, lane);
-    };
-    if (it < n_items) {
-        locate(it);
-        fetch(w, it, kt);
-    }
-    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    while (it < n_items) {
-        const int ai = it / KC, kc = it - ai * KC, hi = pl.first[ai + 1], ck = kt, ct = t0;
-        // the tile after this one: along K, then the item's next pairs, then the next item
-        bool last = false;  // this tile ends its pass
-        kt += KC;
-        if (kt >= kts) {
-            last = true;
-            t0 += 32;
-            if (t0 < hi) {
-                kt = kc;
-            } else {
-                it += NW;
-                locate(it);
-            }
-        }
-        WTile<MX, 1> next;
-        if (it < n_items) fetch(next, it, kt);
+    const int r0 = blockIdx.x * 64, kts = (a.I + kTileK<MX> - 1) / kTileK<MX>;
+    const int Ip = moe_inner(a.I), Ir = moe_act_row(a.I);
+    const auto rd = rows_of<MX, 4>(a.down, e, a.H, a.I, r0, lane);
+    const brsrc rx = make_rsrc(act, (uint32_t)P * 4u * (uint32_t)Ir);
+    auto pass = [&](int t0, auto nc) {
+        constexpr int NC = decltype(nc)::value;
+        uint32_t ao[NC];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (ct + 16 * i >= hi) break;  // uniform
-            const int p = ct + 16 * i + (lane & 15);
-            const uint16_t* ar = p < hi ? act + (int64_t)pl.order[p] * 2 * Ir : nullptr;
-            f32x4 c[1] = {acc[i]};
+        for (int c = 0; c < NC; ++c) {
+            const int p = t0 + 16 * c + (lane & 15);
+            ao[c] = p < hi ? (uint32_t)pl.order[p] * 4u * (uint32_t)Ir : kOutOfRange;
+        }
+        f32x4 acc[NC][4];
 #pragma unroll
-            for (int q = 0; q < kSteps<MX>; ++q) {
-                u32x4 hi16[kPieces<MX>], lo16[kPieces<MX>];
-                load_x<MX, true>(ar, Ip, ck, q, lane, hi16);
-                load_x<MX, true>(ar ? ar + Ir : nullptr, Ip, ck, q, lane, lo16);
-                mac_wtile(c, w, r0 >> 4 & 3, q, hi16);
-                mac_wtile(c, w, r0 >> 4 & 3, q, lo16);
-            }
-            acc[i] = c[0];
-            if (last) {
-                if (p < hi) *reinterpret_cast<f32x4*>(&o[(kc * P + p) * 16 + 4 * (lane >> 4)]) = acc[i];
-                acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int kt = wave; kt < kts; kt += NW) {
+            WTile<MX, 4> w;
+            load_wtile(w, rd, kt);
+#pragma unroll
+            for (int i = 0; i < kSteps<MX>; ++i) {
+                u32x4 x[NC][2][kPieces<MX>];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    load_x<MX, true>(rx, ao[c], Ip, kt, i, lane, x[c][0]);
+                    load_x<MX, true>(rx, ao[c] + 2u * (uint32_t)Ir, Ip, kt, i, lane, x[c][1]);
+                }
+                mac_wtile(acc, w, 0, i, x);
             }
         }
-        w = next;
-    }
-    __syncthreads();
-    for (int i = tid; i < a.T * 16; i += 64 * NW) {
-        const int t = i >> 4, n = i & 15;
-        if (r0 + n >= a.H) continue;
-        float y = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-            const int p = pl.pos[t * a.k + j];
-            if (p < 0) continue;
-            float v = 0.f;
-            for (int kc = 0; kc < KC; ++kc) v += o[(kc * P + p) * 16 + n];
-            y += a.weights[t * a.k + j] * v;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) red[wave][j][lane] = acc[c][j];
+            __syncthreads();
+            // thread (j, l) adds the waves' sums of lane l in row block j
+            if (tid < 256) {
+                const int j = tid >> 6, l = tid & 63;
+                f32x4 s = red[0][j][l];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) s += red[w][j][l];
+                const int q = t0 + 16 * c + (l & 15), n = r0 + 16 * j + 4 * (l >> 4);
+                if (q < hi && n < a.H)  // H is a multiple of 8
+                    *reinterpret_cast<f32x4*>(o + (int64_t)pl.order[q] * a.H + n) = s;
+            }
         }
-        a.Y[(int64_t)t * a.H + r0 + n] = f32_to_bf16(y);
+    };
+    int t0 = lo;
+    for (; hi - t0 > 16; t0 += 32) pass(t0, std::integral_constant<int, 2>{});
+    if (t0 < hi) pass(t0, std::integral_constant<int, 1>{});
+}
+
+// y[t] = sum_j w[t][j] o[t k + j], in the order of j; 4 columns a thread
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a, const float* __restrict__ o) {
+    const int t = blockIdx.y, n = (blockIdx.x * 256 + threadIdx.x) * 4;
+    if (n >= a.H) return;
+    f32x4 y{0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+        f32x4 v[4];
+        float w[4];
+        bool ok[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // all loads first; choices past k or without an expert are not added
+            const int64_t p = (int64_t)t * a.k + min(j0 + j, a.k - 1);
+            const int id = a.ids[p];
+            ok[j] = j0 + j < a.k && id >= 0 && id < a.E;
+            w[j] = a.weights[p];
+            v[j] = *reinterpret_cast<const f32x4*>(o + p * a.H + n);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (ok[j]) y += w[j] * v[j];
     }
+    const u32x2 r{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+    *reinterpret_cast<u32x2*>(a.Y + (int64_t)t * a.H + n) = r;
 }
 
 // Both forms sum a logit in the same order, so they choose alike.
@@ -456,23 +502,29 @@ hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, in
                   weights);
 }
 
-size_t moe_experts_workspace(int T, int I, int k) { return (size_t)T * k * 2 * moe_act_row(I) * sizeof(uint16_t); }
+// the inner values of every pair, then its down products
+static size_t moe_act_bytes(int T, int I, int k) {
+    return ((size_t)T * k * 2 * moe_act_row(I) * sizeof(uint16_t) + 255) & ~size_t(255);
+}
+size_t moe_experts_workspace(int T, int H, int I, int k) {
+    return moe_act_bytes(T, I, k) + (size_t)T * k * H * sizeof(float);
+}
 
 template <bool MX>
 static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
-    constexpr int NG = 8, ND = 16;  // waves of a workgroup
+    constexpr int NW = 8;  // waves of a workgroup
     uint16_t* act = static_cast<uint16_t*>(a.workspace);
-    const int P = a.T * a.k, kts = (a.I + 255) / 256;
-    hipError_t e = launch(tm, "moe_gate_up", moe_gate_up_kernel<MX, NG>,
-                          dim3(moe_inner(a.I) / 32, P < a.E ? P : a.E), dim3(64 * NG), st, a, act);
-    if (e != hipSuccess) return e;
-    // k classes per expert: as many as the planes of results hold and the
-    // tiles of K fill, 8 at most
-    int KC = kMoeOutFloats / (16 * P);
-    KC = KC < 8 ? KC : 8;
-    KC = KC < kts ? KC : kts;
-    return launch(tm, "moe_down", moe_down_kernel<MX, ND>, dim3((a.H + 15) / 16), dim3(64 * ND), st, a,
-                  (const uint16_t*)act, KC);
+    float* o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + moe_act_bytes(a.T, a.I, a.k));
+    const int P = a.T * a.k, reached = P < a.E ? P : a.E;  // experts at most
+    hipError_t e = launch(tm, "moe_gate_up", moe_gate_up_kernel<MX, NW>, dim3(moe_inner(a.I) / 32, reached),
+                          dim3(64 * NW), st, a, act);
+    if (e == hipSuccess)
+        e = launch(tm, "moe_down", moe_down_kernel<MX, NW>, dim3((a.H + 63) / 64, reached), dim3(64 * NW), st, a,
+                   (const uint16_t*)act, o);
+    if (e == hipSuccess)
+        e = launch(tm, "moe_combine", moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.T), dim3(256), st, a,
+                   (const float*)o);
+    return e;
 }
 
 hipError_t moe_experts(const MoeArgs& a, bool mx4, hipStream_t st, StageTimer* tm) {

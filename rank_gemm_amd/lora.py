@@ -125,7 +125,7 @@ def lib():
             L.lora_linear_mx4_device_plan.argtypes = [_P, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P]
             L.lora_moe_route_workspace_bytes.argtypes = [_I, _I]
             L.lora_moe_route.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]
-            L.lora_moe_experts_workspace_bytes.argtypes = [_I, _I, _I]
+            L.lora_moe_experts_workspace_bytes.argtypes = [_I, _I, _I, _I]
             L.lora_moe_experts.argtypes = [_I, _P, _P, _P, ctypes.POINTER(MoeWeightsDesc), _I, _I, _I, _I, _I, _P, _P,
                                            _SZ, _P]
             L.lora_profile_begin.argtypes = [_I]
@@ -755,7 +755,7 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate,
     dev = _same_device(("x", x), ("ids", ids), ("weights", weights), ("gate", gate), ("up", up), ("down", down),
                        ("y", y))
     L = lib()
-    n = L.lora_moe_experts_workspace_bytes(T, I, k) if workspace is None else 0
+    n = L.lora_moe_experts_workspace_bytes(T, H, I, k) if workspace is None else 0
     keep, ws, nb = _space(workspace, n, dev)
     _call(dev, L.lora_moe_experts, "lora_moe_experts", LORA_MX4 if mx4 else LORA_BF16, x.data_ptr(), ids.data_ptr(),
           weights.data_ptr(), ctypes.byref(d), T, H, I, E, k, y.data_ptr(), ws, nb)

@@ -41,7 +41,7 @@ class Moe:
             self.w64.append(v64)
 
     def experts(self, ids, weights, x=None, y=None):
-        n = lora.lib().lora_moe_experts_workspace_bytes(self.T, self.I, self.k)
+        n = lora.lib().lora_moe_experts_workspace_bytes(self.T, self.H, self.I, self.k)
         ws = torch.full((max(n, 16),), 255, dtype=torch.uint8, device="cuda")
         return lora.moe_experts(self.x if x is None else x, ids, weights, *self.w, y=y, workspace=ws)
 
