@@ -582,7 +582,7 @@ int lora_mx4_quantize(int dtype, const void* src, int batch, int rows, int K, vo
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
     if (profiler().on) lk.lock();
-    return lora::mx4_quantize(dtype, src, batch, rows, K, nullptr, (uint8_t*)codes, (uint8_t*)scales, st,
+    return lora::mx4_quantize(dtype, src, batch, rows, K, (uint8_t*)codes, (uint8_t*)scales, st,
                               timer_for(st)) == hipSuccess
                ? LORA_OK
                : LORA_EHIP;

@@ -386,6 +386,9 @@ size_t tiled_workspace(int M, int r_max);
 hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext, hipStream_t st,
                         StageTimer* tm);
 
+hipError_t tiled_forward_ready(const LinearArgs& L, const SliceArgs& s, uint16_t* ext, hipStream_t st,
+                               StageTimer* tm);
+
 // Kernel 2 of the split-K path for one slice whose fp32 partials (ks splits,
 // the 64 x 64 tile layout of kernel 1) were written by another kernel: adds
 // the splits, applies the expand from fp32 h (h_splits planes of [M][r_max],

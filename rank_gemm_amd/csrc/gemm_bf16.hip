@@ -308,6 +308,13 @@ static bool slices_share_shrink(const LinearArgs& L, const int* N, GemmPlan* gs)
     return true;
 }
 
+// One slice on the unsplit tiled path (the caller's choice of sizes) whose
+// expand operand was already written to ext.
+hipError_t tiled_forward_ready(const LinearArgs& L, const SliceArgs& s, uint16_t* ext, hipStream_t st,
+                               StageTimer* tm) {
+    return tiled_forward(L, s, gemm_bf16_plan(L.M, s.N, L.K), st, tm, ext);
+}
+
 hipError_t lora_forward_bf16(const LinearArgs& L, hipStream_t st, StageTimer* tm) {
     const int M = L.M, K = L.K, n = L.n_slices;
     if (M == 0 || n < 1) return hipSuccess;

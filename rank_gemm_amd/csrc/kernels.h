@@ -145,9 +145,8 @@ hipError_t generic_expand(int dtype, const float* h, const void* B_pool, const i
 
 // ---- MXFP4 rows (format: mx4_format.h) ----------------------------------------------
 // `batch` matrices of rows x K, one after another; dtype 0 = fp32, 1 = bf16.
-// With order, row r of the result is source row order[r].
-hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows, int64_t K, const int32_t* order,
-                        uint8_t* codes, uint8_t* scales, hipStream_t st, StageTimer* tm);
+hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows, int64_t K, uint8_t* codes,
+                        uint8_t* scales, hipStream_t st, StageTimer* tm);
 hipError_t mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows,
                           int64_t K, void* dst, hipStream_t st, StageTimer* tm);
 // scale bytes in row order, [batch][rows][ceil(K / 32)], to tiles

@@ -3,8 +3,8 @@
 // What the values of the 4-bit codes, act the identity (16-bit activations)
 // or the MXFP4 rounding of each row of x; the adapters always read x itself.
 #include "fuse.h"
-#include "mx4.h"
 #include "mx4_linear.h"
+#include "mx4_tile.h"
 #include "shrink.h"
 
 namespace lora {
@@ -339,6 +339,60 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
         for (int j = 0; j < 2; ++j) out[(i * 4 + cb + j) * 64 + lane] = acc[i][j] + red[(i * 2 + j) * 64 + lane];
 }
 
+// -------------------------------------------------- before the products --
+// What a call does to one operand (x to 4 bits in plan order, or W's values
+// to bf16) and the SGMV shrink depend on nothing of each other: one launch,
+// the shrink's workgroups (item, K range) first, then a workgroup per tile of
+// 64 rows x 256 k.
+struct Mx4Prep {
+    const uint16_t* X;
+    int M, N, K;
+    const int32_t* token_order;
+    uint8_t *xc, *xs;           // kQuantize
+    const uint8_t *wc, *ws;     // kDequantize
+    uint16_t* W;
+    const Item* work;
+    const uint16_t* A_pool;
+    const int32_t* rank;
+    const float* scale;
+    int n_items, r_max, hs, hkc;
+    float* h;       // [hs][M][r_max] (ext null)
+    uint16_t* ext;  // the expand operand (hs == 1)
+};
+
+template <bool QUANT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void mx4_prep_kernel(Mx4Prep a) {
+    __shared__ f32x4 red[WAVES * 4 * 64];
+    static_assert(sizeof(red) >= kMxTileBytes, "scale tile");
+    const int n_shrink = a.n_items * a.hs;
+    if ((int)blockIdx.x < n_shrink) {
+        const int item = blockIdx.x % a.n_items, hz = blockIdx.x / a.n_items;
+        const Item it = a.work[item];
+        const int r = a.rank[it.slot];
+        if (r == 0) return;
+        const int kbeg = hz * a.hkc, kend = min(a.K, kbeg + a.hkc);
+        const ShrinkOut out{a.h + (int64_t)hz * a.M * a.r_max, a.ext, (a.r_max + 7) & ~7, a.scale[it.slot]};
+        shrink_item<WAVES>(a.X, a.A_pool, r, a.token_order, it, out, a.K, kbeg, kend, a.r_max, red);
+        return;
+    }
+    const int kts = (int)mx4_k_tiles(a.K), t = blockIdx.x - n_shrink;
+    uint8_t* st = reinterpret_cast<uint8_t*>(red);
+    if constexpr (QUANT)
+        quantize_tile<uint16_t, true, 64 * WAVES>(a.X, a.M, a.K, a.token_order, a.xc, a.xs, t % kts, t / kts, st);
+    else
+        dequantize_tile<uint16_t, true, 64 * WAVES>(a.wc, a.ws, a.N, a.K, a.W, t % kts, t / kts, st);
+}
+
+template <bool QUANT>
+static hipError_t launch_prep(const Mx4Prep& a, hipStream_t st, StageTimer* tm) {
+    const int64_t tiles = ((int64_t)(QUANT ? a.M : a.N) + 63) / 64 * mx4_k_tiles(a.K);
+    const dim3 grid((uint32_t)(a.n_items * a.hs + tiles));
+    const char* name = QUANT ? "mx4_quantize+shrink" : "mx4_dequantize+shrink";
+    // few items: 16 waves each over the K range, as the stand-alone shrink
+    if (a.n_items * a.hs < 256) return launch(tm, name, mx4_prep_kernel<QUANT, 16>, grid, dim3(1024), st, a);
+    return launch(tm, name, mx4_prep_kernel<QUANT, 4>, grid, dim3(256), st, a);
+}
+
 // rows of any width -> rows of Kp elements (a multiple of 8), zeros behind
 // the row's end: the kernels read rows in 16-byte pieces
 __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t rows, int K, int Kp,
@@ -459,10 +513,14 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
     char* ws = static_cast<char*>(L.workspace);
     const Mx4Space sp = mx4_space(M, N, L.K, L.S, L.r_max, act4);
     hipError_t e = hipSuccess;
-    uint8_t* xc = reinterpret_cast<uint8_t*>(ws + sp.codes);
-    uint8_t* xs = reinterpret_cast<uint8_t*>(ws + sp.scales);
-    if (act4) e = mx4_quantize(1, L.X, 1, M, L.K, L.token_order, xc, xs, st, tm);
-    if (e != hipSuccess) return e;
+    Mx4Prep pr{};
+    pr.X = L.X;
+    pr.M = M;
+    pr.N = N;
+    pr.K = L.K;
+    pr.token_order = L.token_order;
+    pr.xc = reinterpret_cast<uint8_t*>(ws + sp.codes);
+    pr.xs = reinterpret_cast<uint8_t*>(ws + sp.scales);
     if (L.K % 8) {
         const int Kp = (L.K + 7) / 8 * 8;
         uint16_t* xp = reinterpret_cast<uint16_t*>(ws + sp.xpad);
@@ -472,15 +530,34 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
         if (e != hipSuccess) return e;
         L.X = xp;
         sl.A_pool = ap;
-        L.K = Kp;  // as many blocks and scale tiles
+        L.K = Kp;  // as many blocks and scale tiles; zeros quantise to zeros
+        pr.X = xp;
+        pr.K = Kp;
     }
+    pr.work = reinterpret_cast<const Item*>(L.work);
+    pr.A_pool = sl.A_pool;
+    pr.rank = sl.rank;
+    pr.scale = sl.scale;
+    pr.n_items = L.adapters ? L.n_items : 0;
+    pr.r_max = L.r_max;
+    pr.hs = 1;
+    pr.hkc = L.K;
+    // the expand as extra K steps of a tiled product, where its form allows
+    const bool ext_ok = L.r_max % 8 == 0 && L.S <= kMetaSlots;
     switch (mx4_path(M, N, L.K, act4)) {
         case Mx4Path::kSplit: {
             const Mx4SplitPlan p = mx4_split_plan(M, N, L.K, L.S, act4);
-            const Mx4Split a{L.X, xc, xs, codes, scales, reinterpret_cast<float*>(ws + sp.own), M, N, L.K, p.n_mt,
-                             p.n_nt, p.ks, p.upb, L.token_order, reinterpret_cast<const Item*>(L.work), sl.A_pool,
-                             sl.rank, reinterpret_cast<float*>(ws + sp.h), L.adapters ? L.n_items : 0, L.r_max, p.hs,
-                             p.hkc};
+            Mx4Split a{L.X, pr.xc, pr.xs, codes, scales, reinterpret_cast<float*>(ws + sp.own), M, N, L.K, p.n_mt,
+                       p.n_nt, p.ks, p.upb, L.token_order, pr.work, sl.A_pool, sl.rank,
+                       reinterpret_cast<float*>(ws + sp.h), pr.n_items, L.r_max, p.hs, p.hkc};
+            if (act4) {  // the shrink beside the quantisation
+                pr.hs = p.hs;
+                pr.hkc = p.hkc;
+                pr.h = a.part_h;
+                a.n_items = 0;
+                e = launch_prep<true>(pr, st, tm);
+                if (e != hipSuccess) return e;
+            }
             e = launch_split(a, act4, st, tm);
             if (e != hipSuccess) return e;
             return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
@@ -489,25 +566,30 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
             float* h = reinterpret_cast<float*>(ws + sp.own);
             Fuse f{L.token_order, L.slot_indptr, h, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
                    nullptr, (L.r_max + 7) & ~7};
-            uint16_t* ext = nullptr;  // the expand as extra K steps, where its form allows
-            if (L.r_max % 8 == 0 && L.S <= kMetaSlots) {
-                ext = reinterpret_cast<uint16_t*>(h);
-                f.ext = ext;
+            pr.h = h;
+            if (ext_ok) {
+                pr.ext = reinterpret_cast<uint16_t*>(h);
+                f.ext = pr.ext;
                 f.h = nullptr;
             }
-            if (L.adapters) e = tiled_shrink(L, sl, ws + sp.own, ext ? nullptr : h, ext, st, tm);
+            e = launch_prep<true>(pr, st, tm);
             if (e != hipSuccess) return e;
-            return mx4_gemm(xc, xs, codes, scales, sl.Y, M, N, L.K, f, st, tm);
+            return mx4_gemm(pr.xc, pr.xs, codes, scales, sl.Y, M, N, L.K, f, st, tm);
         }
         case Mx4Path::kDequant: break;
     }
     // W's values are exact in bf16: the bf16 layer on them
-    uint16_t* W = reinterpret_cast<uint16_t*>(ws + sp.own);
-    e = mx4_dequantize(1, codes, scales, 1, N, L.K, W, st, tm);
-    if (e != hipSuccess) return e;
-    sl.W = W;
+    pr.wc = codes;
+    pr.ws = scales;
+    pr.W = reinterpret_cast<uint16_t*>(ws + sp.own);
+    sl.W = pr.W;
     L.workspace = ws + sp.h;
-    return lora_forward_bf16(L, st, tm);
+    const bool beside = ext_ok && gemm_bf16_plan(M, N, L.K).tks < 2;
+    if (beside) pr.ext = reinterpret_cast<uint16_t*>(ws + sp.h);
+    else pr.n_items = 0;
+    e = launch_prep<false>(pr, st, tm);
+    if (e != hipSuccess) return e;
+    return beside ? tiled_forward_ready(L, sl, pr.ext, st, tm) : lora_forward_bf16(L, st, tm);
 }
 
 }  // namespace lora
