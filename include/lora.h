@@ -467,7 +467,8 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  *   x        dev bf16 [T][H]
  *   router   dev bf16 [E][H]
  *   ids      dev int32 [T][k] out;  weights  dev float [T][k] out
- *   workspace dev, at least lora_moe_route_workspace_bytes(T, E) bytes
+ *   workspace dev, at least lora_moe_route_workspace_bytes(T, H, E) bytes
+ *            (0 for a small router: workspace may then be null)
  * A NaN logit ranks below every number; ids stay valid and distinct, and the
  * weights of that token are NaN.
  *
@@ -495,7 +496,7 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
 #define LORA_MOE_MAX_EXPERTS 512
 #define LORA_MOE_MAX_K 16
 #define LORA_MOE_MAX_PAIRS 512
-size_t lora_moe_route_workspace_bytes(int T, int E);
+size_t lora_moe_route_workspace_bytes(int T, int H, int E);
 int lora_moe_route(const void* x, const void* router, int T, int H, int E, int k, int renorm, int32_t* ids,
                    float* weights, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -666,15 +666,17 @@ int lora_linear_mx4_device_plan(const lora_pool* p, const void* x, const void* c
                            workspace_bytes, stream);
 }
 
-size_t lora_moe_route_workspace_bytes(int T, int E) { return T < 0 || E < 1 ? 0 : lora::moe_route_workspace(T, E); }
+size_t lora_moe_route_workspace_bytes(int T, int H, int E) {
+    return T < 0 || H < 1 || E < 1 ? 0 : lora::moe_route_workspace(T, H, E);
+}
 
 int lora_moe_route(const void* x, const void* router, int T, int H, int E, int k, int renorm, int32_t* ids,
                    float* weights, void* workspace, size_t workspace_bytes, void* stream) {
     if (!moe_sizes(T, H, E, k) || k > E) return LORA_EINVAL;
     if (T == 0) return LORA_OK;
     if (!x || !router || !ids || !weights || !aligned(x, 16) || !aligned(router, 16)) return LORA_EINVAL;
-    if (!workspace || !aligned(workspace, 8) || workspace_bytes < lora_moe_route_workspace_bytes(T, E))
-        return LORA_ESPACE;
+    const size_t need = lora_moe_route_workspace_bytes(T, H, E);
+    if (need > 0 && (!workspace || !aligned(workspace, 8) || workspace_bytes < need)) return LORA_ESPACE;
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
     if (profiler().on) lk.lock();

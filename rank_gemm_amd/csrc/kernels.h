@@ -175,7 +175,7 @@ struct MoeArgs {
     int T, H, I, E, k;
     void* workspace;
 };
-size_t moe_route_workspace(int T, int E);
+size_t moe_route_workspace(int T, int H, int E);
 hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, int E, int k, int renorm, int32_t* ids,
                      float* weights, void* workspace, hipStream_t st, StageTimer* tm);
 size_t moe_experts_workspace(int T, int H, int I, int k);

@@ -6,9 +6,9 @@
 // in 16-byte pieces, for all of its tokens, which ride as the 16 columns of
 // the matrix-core products (weights are the left operand).
 //
-// Route: one wave per (expert, token) sums the logit in 64 bits, so that the
-// choice among close logits does not hang on the rounding of a sum; one wave
-// per token then takes the k largest.
+// Route: a wave sums the logit of an expert and a token in 64 bits, so that
+// the choice among close logits does not hang on the rounding of a sum; a
+// workgroup per token then ranks its logits.
 // Experts: gate_up (a workgroup takes one reached expert and 32 inner columns:
 // 32 gate and 32 up rows), down (one reached expert and 64 output columns),
 // combine (the weighted sum of a token's k terms, in the order of j).
@@ -19,132 +19,148 @@
 namespace lora {
 
 // ------------------------------------------------------------------ route --
-// A lane's part of the 64-bit dot product of two bf16 rows.
-__device__ __forceinline__ double dot_rows(const uint16_t* __restrict__ xp, const uint16_t* __restrict__ rp, int H,
-                                           int lane) {
-    double s[2] = {0.0, 0.0};
-#pragma unroll 4
-    for (int k = lane * 8; k < H; k += 512) {
-        const u32x4 a = *as_global<u32x4>(xp + k), b = *as_global<u32x4>(rp + k);
+// A lane's parts of the 64-bit dot products of one bf16 row with NE others
+// (rows of `stride` elements), in the order of k; CH pieces of every row in
+// flight at once.
+template <int NE, int CH>
+__device__ __forceinline__ void dot_rows(const uint16_t* __restrict__ xp, const uint16_t* __restrict__ rp,
+                                         int64_t stride, int H, int lane, double (&s)[NE]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // a product of two bf16 is exact in fp32
-            s[0] += (double)(__uint_as_float(a[i] << 16) * __uint_as_float(b[i] << 16));
-            s[1] += (double)(__uint_as_float(a[i] & 0xffff0000u) * __uint_as_float(b[i] & 0xffff0000u));
+    for (int e = 0; e < NE; ++e) s[e] = 0.0;
+    for (int k0 = lane * 8; k0 < H; k0 += 512 * CH) {
+        u32x4 a[CH], b[NE][CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const bool ok = k0 + 512 * c < H;
+            a[c] = *or_zero(ok, xp + k0 + 512 * c);
+#pragma unroll
+            for (int e = 0; e < NE; ++e) b[e][c] = *or_zero(ok, rp + e * stride + k0 + 512 * c);
         }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int e = 0; e < NE; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // a product of two bf16 is exact in fp32
+                    s[e] += (double)(__uint_as_float(a[c][i] << 16) * __uint_as_float(b[e][c][i] << 16));
+                    s[e] += (double)(__uint_as_float(a[c][i] & 0xffff0000u) *
+                                     __uint_as_float(b[e][c][i] & 0xffff0000u));
+                }
     }
-    return s[0] + s[1];
+}
+template <int NE>
+__device__ __forceinline__ void wave_sum(double (&s)[NE]) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < NE; ++e) s[e] += __shfl_xor(s[e], o);
 }
 
-// One wave, lane l holding logits l, l + 64, ...: k rounds of a maximum over
-// the wave, equal logits to the lower index. A NaN counts as the lowest of
-// all, so the ids stay valid and distinct; its weights are NaN.
-constexpr int kMoePerLane = kMoeMaxExperts / 64;
+// The order of logits as signed integers: NaN below every number, -0 as 0.
+__device__ __forceinline__ int64_t rank_key(double v) {
+    const int64_t b = __builtin_bit_cast(int64_t, v + 0.0);
+    return v != v ? INT64_MIN : b ^ ((b >> 63) & INT64_MAX);
+}
+
+// The k largest of the E logits in LDS, by rank: RT threads of the 1024 count
+// for one logit how many come before it (larger, or equal at a lower index);
+// ranks below k are the choices. No round waits on another, whatever k. A NaN
+// ranks last, so the ids stay valid and distinct; its weights are NaN.
 __device__ __forceinline__ void topk_token(const double* logits, int E, int k, int renorm, int32_t* ids,
-                                           float* weights, int lane) {
-    double v[kMoePerLane];
-    uint32_t taken = 0;
-#pragma unroll
-    for (int i = 0; i < kMoePerLane; ++i) v[i] = i * 64 + lane < E ? logits[i * 64 + lane] : 0.0;
-    double top = 0.0, mine = 0.0;  // the largest logit; the one chosen in round `lane`
-    int id = 0;
-    for (int j = 0; j < k; ++j) {
-        double best = 0.0;
-        int at = -1;
-#pragma unroll
-        for (int i = 0; i < kMoePerLane; ++i) {
-            if (i * 64 + lane >= E || (taken >> i & 1)) continue;
-            if (at < 0 || v[i] > best || (best != best && v[i] == v[i])) {
-                best = v[i];
-                at = i * 64 + lane;
-            }
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const double ov = __shfl_xor(best, o);
-            const int oa = __shfl_xor(at, o);
-            const bool bn = best != best, on = ov != ov;
-            bool take;
-            if (oa < 0 || at < 0) take = at < 0;
-            else if (bn != on) take = bn;
-            else if (bn || ov == best) take = oa < at;
-            else take = ov > best;
-            if (take) {
-                best = ov;
-                at = oa;
-            }
-        }
-        if ((at & 63) == lane) taken |= 1u << (at >> 6);
-        if (j == 0) top = best;
-        if (j == lane) {
-            mine = best;
-            id = at;
+                                           float* weights, double* sel) {
+    const int tid = threadIdx.x;
+    const int rt = E <= 64 ? 16 : E <= 128 ? 8 : E <= 256 ? 4 : 2;  // threads per logit, neighbours in a wave
+    const int e = tid / rt, part = tid % rt;
+    int before = 0;
+    if (e < E) {
+        const int64_t mine = rank_key(logits[e]);
+        for (int j = part; j < E; j += rt) {
+            const int64_t other = rank_key(logits[j]);
+            before += other > mine || (other == mine && j < e);
         }
     }
+    for (int o = 1; o < rt; o <<= 1) before += __shfl_xor(before, o);
+    if (e < E && part == 0 && before < k) {
+        ids[before] = e;
+        sel[before] = logits[e];
+    }
+    __syncthreads();
+    if (tid >= 64) return;
     // weights: exp(l_j - max) over the sum of the chosen (renorm) or of all
-    const float p = lane < k ? expf((float)(mine - top)) : 0.f;
+    const double top = sel[0];
+    const float p = tid < k ? expf((float)(sel[tid] - top)) : 0.f;
     float den = p;
     if (!renorm) {
         den = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMoePerLane; ++i)
-            if (i * 64 + lane < E) den += expf((float)(v[i] - top));
+        for (int i = tid; i < E; i += 64) den += expf((float)(logits[i] - top));
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) den += __shfl_xor(den, o);
-    if (lane < k) {
-        ids[lane] = id;
-        weights[lane] = p / den;
-    }
+    if (tid < k) weights[tid] = p / den;
 }
 
-// One workgroup per token: its 16 waves take the experts in turn, the first
-// wave then the k largest of the logits in LDS.
+// One workgroup per token: its 16 waves take four experts at a time.
 __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t* __restrict__ X,
                                                          const uint16_t* __restrict__ R, int H, int E, int k,
                                                          int renorm, int32_t* __restrict__ ids,
                                                          float* __restrict__ weights) {
     __shared__ double logits[kMoeMaxExperts];
+    __shared__ double sel[kMoeMaxK];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x;
-    for (int e = wave; e < E; e += 16) {
-        double s = dot_rows(X + (int64_t)t * H, R + (int64_t)e * H, H, lane);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-        if (lane == 0) logits[e] = s;
+    const uint16_t* xp = X + (int64_t)t * H;
+    for (int e0 = wave * 4; e0 < E; e0 += 64) {
+        double s[4];
+        if (e0 + 4 <= E) {  // uniform
+            dot_rows<4, 4>(xp, R + (int64_t)e0 * H, H, H, lane, s);
+            wave_sum(s);
+        } else {
+            for (int i = 0; i < 4; ++i) {
+                double one[1] = {0.0};
+                if (e0 + i < E) dot_rows<1, 4>(xp, R + (int64_t)(e0 + i) * H, H, H, lane, one);
+                wave_sum(one);
+                s[i] = one[0];
+            }
+        }
+        if (lane < 4 && e0 + lane < E) logits[e0 + lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
     }
     __syncthreads();
-    if (wave == 0) topk_token(logits, E, k, renorm, ids + t * k, weights + t * k, lane);
+    topk_token(logits, E, k, renorm, ids + t * k, weights + t * k, sel);
 }
 
-// The same over two launches, one wave per (expert, token) and then one per
-// token: a router too large for one CU to read quickly, and few tokens.
+// The same over two launches, one wave per (expert, token) and then one
+// workgroup per token: a router too large for one CU to read quickly.
 __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t* __restrict__ X,
                                                          const uint16_t* __restrict__ R, int H, int E,
                                                          double* __restrict__ logits) {
     const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6), t = blockIdx.y;
     if (e >= E) return;
-    double s = dot_rows(X + (int64_t)t * H, R + (int64_t)e * H, H, lane);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if (lane == 0) logits[(int64_t)t * E + e] = s;
+    double s[1];
+    dot_rows<1, 4>(X + (int64_t)t * H, R + (int64_t)e * H, H, H, lane, s);
+    wave_sum(s);
+    if (lane == 0) logits[(int64_t)t * E + e] = s[0];
 }
 
-__global__ __launch_bounds__(64) void moe_topk_kernel(const double* __restrict__ logits, int E, int k, int renorm,
-                                                      int32_t* __restrict__ ids, float* __restrict__ weights) {
+__global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict__ logits, int E, int k, int renorm,
+                                                        int32_t* __restrict__ ids, float* __restrict__ weights) {
+    __shared__ double lds[kMoeMaxExperts];
+    __shared__ double sel[kMoeMaxK];
     const int t = blockIdx.x;
-    topk_token(logits + (int64_t)t * E, E, k, renorm, ids + t * k, weights + t * k, threadIdx.x);
+    for (int i = threadIdx.x; i < E; i += 1024) lds[i] = logits[(int64_t)t * E + i];
+    __syncthreads();
+    topk_token(lds, E, k, renorm, ids + t * k, weights + t * k, sel);
 }
 
 // ---------------------------------------------------------------- experts --
 // The (token, choice) pairs grouped by expert: order lists the pairs of
 // active expert a at [first[a], first[a + 1]); pairs whose id is outside
-// [0, E) are left out. Every workgroup builds it in LDS from the ids.
+// [0, E) are left out. Every workgroup builds it in LDS from the ids (more
+// than 64 pairs; fewer take moe_find).
 constexpr int kMoePlanThreads = 512;
 struct MoePlan {
     int n;                         // experts reached
     int expert[kMoeMaxPairs];      // ascending
     int first[kMoeMaxPairs + 1];
     int16_t order[kMoeMaxPairs];   // sorted position -> pair
-    int16_t pos[kMoeMaxPairs];     // pair -> sorted position, or -1
     int cnt[kMoeMaxExperts];
     int wsum[2][kMoePlanThreads / 64];
 };
@@ -193,9 +209,50 @@ __device__ __forceinline__ void moe_plan(const int32_t* __restrict__ ids, int P,
         pl.cnt[tid] = s - c;  // first sorted position of expert tid
     }
     __syncthreads();
-    if (tid < P) pl.pos[tid] = ok ? (int16_t)(pl.cnt[id] + at) : (int16_t)-1;
     if (ok) pl.order[pl.cnt[id] + at] = (int16_t)tid;
     __syncthreads();
+}
+
+// Active expert z of at most 64 pairs, in the order of first mention, found by
+// every wave for itself with no barrier: its pairs as a lane mask (pair =
+// lane), each wave's list of them in its own part of LDS.
+constexpr int kMoeWavePairs = 64;
+struct MoeRun {
+    int e, n;              // expert (or -1: fewer than z + 1 are reached), its pairs
+    const int16_t* order;  // their indices
+};
+__device__ __forceinline__ MoeRun moe_find(const int32_t* __restrict__ ids, int P, int E, int z, int16_t* list,
+                                           int lane) {
+    const int id = lane < P ? ids[lane] : -1;
+    const bool ok = id >= 0 && id < E;
+    uint64_t left = __ballot(ok);
+    MoeRun r{-1, 0, list};
+    for (int c = 0; left; ++c) {
+        const int ex = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t mine = __ballot(ok && id == ex);
+        if (c == z) {
+            r.e = ex;
+            r.n = __popcll(mine);
+            if ((mine >> lane) & 1) list[__popcll(mine & ((1ull << lane) - 1))] = (int16_t)lane;
+            break;
+        }
+        left &= ~mine;
+    }
+    return r;
+}
+
+// The run of pairs a workgroup of the experts' kernels works on.
+template <int NW>
+__device__ __forceinline__ MoeRun moe_run(const MoeArgs& a, int z, MoePlan& pl, int lane, int wave) {
+    const int P = a.T * a.k;
+    if (P <= kMoeWavePairs) {
+        static_assert(NW * kMoeWavePairs * sizeof(int16_t) <= sizeof(pl.cnt), "a list per wave");
+        return moe_find(a.ids, P, a.E, z, reinterpret_cast<int16_t*>(pl.cnt) + wave * kMoeWavePairs, lane);
+    }
+    moe_plan(a.ids, P, a.E, pl);
+    if (z >= pl.n) return MoeRun{-1, 0, nullptr};
+    const int lo = __builtin_amdgcn_readfirstlane(pl.first[z]), hi = __builtin_amdgcn_readfirstlane(pl.first[z + 1]);
+    return MoeRun{__builtin_amdgcn_readfirstlane(pl.expert[z]), hi - lo, pl.order + lo};
 }
 
 // A tile's products go in steps: 128 k (4-bit, 2 a tile of 256 k) or 32 k
@@ -245,9 +302,9 @@ __device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>
 #pragma unroll
     for (int s = 0; s < kSteps<MX>; ++s)
 #pragma unroll
-        for (int j = 0; j < RB; ++j)  // non-temporal: read once
+        for (int j = 0; j < RB; ++j)
             t.w[j][s] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r.data, r.off[j], kt * TB + s * 64, 2));
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r.data, r.off[j], kt * TB + s * 64, 0));
 }
 
 // acc[c][j] += (16-row block j of the tile) (x[c][0] + x[c][1] + ..)^T over
@@ -319,13 +376,10 @@ template <bool MX, int NW>
 __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint16_t* __restrict__ act) {
     __shared__ MoePlan pl;
     __shared__ f32x4 red[NW][4][64];
-    const int P = a.T * a.k;
-    moe_plan(a.ids, P, a.E, pl);
-    if ((int)blockIdx.y >= pl.n) return;
-    const int e = __builtin_amdgcn_readfirstlane(pl.expert[blockIdx.y]);
-    const int lo = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y]);
-    const int hi = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y + 1]);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const MoeRun run = moe_run<NW>(a, blockIdx.y, pl, lane, wave);
+    if (run.e < 0) return;  // uniform for the workgroup
+    const int e = run.e, hi = run.n;
     const int r0 = blockIdx.x * 32, kts = (a.H + kTileK<MX> - 1) / kTileK<MX>, Ir = moe_act_row(a.I);
     const auto rg = rows_of<MX, 2>(a.gate, e, a.I, a.H, r0, lane), ru = rows_of<MX, 2>(a.up, e, a.I, a.H, r0, lane);
     const brsrc rx = make_rsrc(a.X, (uint32_t)a.T * (uint32_t)a.H * 2u);
@@ -335,7 +389,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int p = t0 + 16 * c + (lane & 15);
-            xo[c] = p < hi ? (uint32_t)(pl.order[p] / a.k) * (uint32_t)a.H * 2u : kOutOfRange;
+            xo[c] = p < hi ? (uint32_t)(run.order[p] / a.k) * (uint32_t)a.H * 2u : kOutOfRange;
         }
         f32x4 g[NC][2], u[NC][2];
 #pragma unroll
@@ -375,7 +429,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint
             const int q = t0 + 16 * cc + (l & 15), i = r0 + 16 * j + 4 * (l >> 4) + c;
             if (q < hi && i < moe_inner(a.I)) {
                 const float v = i < a.I ? gs / (1.f + expf(-gs)) * us : 0.f;
-                uint16_t* ap = act + (int64_t)pl.order[q] * 2 * Ir + moe_at<MX>(i);
+                uint16_t* ap = act + (int64_t)run.order[q] * 2 * Ir + moe_at<MX>(i);
                 const uint16_t h = f32_to_bf16(v);
                 ap[0] = h;
                 // an infinite or NaN value has no remainder
@@ -384,7 +438,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint
             }
         }
     };
-    int t0 = lo;
+    int t0 = 0;
     for (; hi - t0 > 16; t0 += 32) pass(t0, std::integral_constant<int, 2>{});
     if (t0 < hi) pass(t0, std::integral_constant<int, 1>{});
 }
@@ -398,24 +452,21 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(MoeArgs a, const u
                                                               float* __restrict__ o) {
     __shared__ MoePlan pl;
     __shared__ f32x4 red[NW][4][64];
-    const int P = a.T * a.k;
-    moe_plan(a.ids, P, a.E, pl);
-    if ((int)blockIdx.y >= pl.n) return;
-    const int e = __builtin_amdgcn_readfirstlane(pl.expert[blockIdx.y]);
-    const int lo = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y]);
-    const int hi = __builtin_amdgcn_readfirstlane(pl.first[blockIdx.y + 1]);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const MoeRun run = moe_run<NW>(a, blockIdx.y, pl, lane, wave);
+    if (run.e < 0) return;  // uniform for the workgroup
+    const int e = run.e, hi = run.n;
     const int r0 = blockIdx.x * 64, kts = (a.I + kTileK<MX> - 1) / kTileK<MX>;
     const int Ip = moe_inner(a.I), Ir = moe_act_row(a.I);
     const auto rd = rows_of<MX, 4>(a.down, e, a.H, a.I, r0, lane);
-    const brsrc rx = make_rsrc(act, (uint32_t)P * 4u * (uint32_t)Ir);
+    const brsrc rx = make_rsrc(act, (uint32_t)(a.T * a.k) * 4u * (uint32_t)Ir);
     auto pass = [&](int t0, auto nc) {
         constexpr int NC = decltype(nc)::value;
         uint32_t ao[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int p = t0 + 16 * c + (lane & 15);
-            ao[c] = p < hi ? (uint32_t)pl.order[p] * 4u * (uint32_t)Ir : kOutOfRange;
+            ao[c] = p < hi ? (uint32_t)run.order[p] * 4u * (uint32_t)Ir : kOutOfRange;
         }
         f32x4 acc[NC][4];
 #pragma unroll
@@ -450,11 +501,11 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(MoeArgs a, const u
                 for (int w = 1; w < NW; ++w) s += red[w][j][l];
                 const int q = t0 + 16 * c + (l & 15), n = r0 + 16 * j + 4 * (l >> 4);
                 if (q < hi && n < a.H)  // H is a multiple of 8
-                    *reinterpret_cast<f32x4*>(o + (int64_t)pl.order[q] * a.H + n) = s;
+                    *reinterpret_cast<f32x4*>(o + (int64_t)run.order[q] * a.H + n) = s;
             }
         }
     };
-    int t0 = lo;
+    int t0 = 0;
     for (; hi - t0 > 16; t0 += 32) pass(t0, std::integral_constant<int, 2>{});
     if (t0 < hi) pass(t0, std::integral_constant<int, 1>{});
 }
@@ -485,9 +536,11 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a, const float
 }
 
 // Both forms sum a logit in the same order, so they choose alike.
-constexpr int64_t kMoeRouteOne = 1 << 16;  // router values one workgroup reads: 128 KB
+constexpr int64_t kMoeRouteOne = 1 << 18;  // router values one workgroup reads: 512 KB
 
-size_t moe_route_workspace(int T, int E) { return (size_t)T * E * sizeof(double); }
+size_t moe_route_workspace(int T, int H, int E) {
+    return (int64_t)E * H <= kMoeRouteOne ? 0 : (size_t)T * E * sizeof(double);
+}
 
 hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, int E, int k, int renorm, int32_t* ids,
                      float* weights, void* workspace, hipStream_t st, StageTimer* tm) {
@@ -498,7 +551,7 @@ hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, in
     hipError_t e = launch(tm, "moe_logits", moe_logits_kernel, dim3((E + 3) / 4, T), dim3(256), st, X, router, H, E,
                           logits);
     if (e != hipSuccess) return e;
-    return launch(tm, "moe_topk", moe_topk_kernel, dim3(T), dim3(64), st, (const double*)logits, E, k, renorm, ids,
+    return launch(tm, "moe_topk", moe_topk_kernel, dim3(T), dim3(1024), st, (const double*)logits, E, k, renorm, ids,
                   weights);
 }
 

@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int blk = u * 8 + h * 4 + fc;
-                w[h][j] = __builtin_nontemporal_load(or_zero(blk * 32 < a.K, wrow[j] + blk * 16));
+                w[h][j] = *or_zero(blk * 32 < a.K, wrow[j] + blk * 16);
             }
         if constexpr (ACT4) {
             const u32x2 xsc = *as_global<u32x2>(a.xs + ((int64_t)mt * kts + u) * kMxTileBytes + lane * 8);
@@ -251,8 +251,8 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
         const int k = u < u1 ? u * 256 : a.K, uc = min(u, u1 - 1);
         s[buf] = __builtin_amdgcn_raw_buffer_load_b32(rS, soff, uc * kMxTileBytes, 0);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)  // non-temporal: W is read once
-            w[buf][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rW, woff[j], uc * 128, 2));
+        for (int j = 0; j < 2; ++j)
+            w[buf][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rW, woff[j], uc * 128, 0));
 #pragma unroll
         for (int d = 0; d < DMA; ++d)
             bdma16(rX, k + xk[d] < a.K ? xoff[d] : kOutOfRange, (uint32_t)k * 2u, lds + buf * UNIT + (DMA * wave + d) * 64);

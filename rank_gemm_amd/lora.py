@@ -123,7 +123,7 @@ def lib():
             L.lora_workspace_bytes_mx4.argtypes = [_P, _I, _I]
             L.lora_linear_mx4.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, ctypes.POINTER(PlanInfo), _P, _P, _SZ, _P]
             L.lora_linear_mx4_device_plan.argtypes = [_P, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P]
-            L.lora_moe_route_workspace_bytes.argtypes = [_I, _I]
+            L.lora_moe_route_workspace_bytes.argtypes = [_I, _I, _I]
             L.lora_moe_route.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]
             L.lora_moe_experts_workspace_bytes.argtypes = [_I, _I, _I, _I]
             L.lora_moe_experts.argtypes = [_I, _P, _P, _P, ctypes.POINTER(MoeWeightsDesc), _I, _I, _I, _I, _I, _P, _P,
@@ -255,6 +255,7 @@ class Plan:
         self.host = host  # pinned int32: [work 4*n_work][token_order T][slot_indptr S+1]
         self.dev = dev
         self._n_work = n_work
+        self._ptrs = None  # addresses in dev, which stays for the plan's lifetime
         # plan_into staging: two pinned buffers used in turn, the copy that
         # last read each (None: not read yet), the one to write next
         self._stage, self._ev, self._turn = [None, None], [None, None], 0
@@ -281,8 +282,10 @@ class Plan:
         return self.host[: 4 * self.info.n_items].numpy().reshape(-1, 4)
 
     def dev_ptrs(self):
-        base = self.dev.data_ptr() if self.dev is not None else 0
-        return (base + 4 * self._off("token_order"), base + 4 * self._off("slot_indptr"), base + 4 * self._off("work"))
+        if self._ptrs is None:
+            base = self.dev.data_ptr() if self.dev is not None else 0
+            self._ptrs = tuple(base + 4 * self._off(n) for n in ("token_order", "slot_indptr", "work"))
+        return self._ptrs
 
 
 def plan(slot_ids, S: int, device="cuda", upload: bool = True, chunk: int = LORA_PLAN_ROWS) -> Plan:
@@ -693,7 +696,9 @@ def linear_mx4(x: torch.Tensor, W: Mx4, pool: Pool, p, act: str = "bf16", y: tor
         raise ValueError("plan was not uploaded")
     if device_plan and p.S != pool.S:
         raise ValueError("plan and pool have different S")
-    dev = _same_device(("x", x), ("W", W), ("pool", pool.A), ("y", y), ("plan", p.buf if device_plan else p.dev))
+    dev, pd = x.device, p.buf if device_plan else p.dev
+    if W.device != dev or pool.A.device != dev or y.device != dev or pd.device != dev:
+        _same_device(("x", x), ("W", W), ("pool", pool.A), ("y", y), ("plan", pd))
     L = lib()
     n = L.lora_workspace_bytes_mx4(pool.handle, T, code) if workspace is None else 0
     keep, ws, nb = _space(workspace, n, dev)
@@ -717,10 +722,11 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renorm: bool = True
         raise ValueError(f"x {tuple(x.shape)} and router {tuple(router.shape)} must be [T, H] and [E, H]")
     (T, H), E, k = x.shape, router.shape[0], int(k)
     dev = _same_device(("x", x), ("router", router))
-    out = torch.empty((2, T, max(k, 0)), dtype=torch.float32, device=dev)
-    ids, weights = out[0].view(torch.int32), out[1]
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
     L = lib()
-    keep, ws, nb = _space(None, L.lora_moe_route_workspace_bytes(T, E), dev)
+    n = L.lora_moe_route_workspace_bytes(T, H, E)
+    keep, ws, nb = _space(None, n, dev) if n else (None, None, 0)
     _call(dev, L.lora_moe_route, "lora_moe_route", x.data_ptr(), router.data_ptr(), T, H, E, k, int(bool(renorm)),
           ids.data_ptr(), weights.data_ptr(), ws, nb)
     return ids, weights
