@@ -14,7 +14,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu
                                                                 SplitOut{}, xs, wsc);
 }
 
-// BUF: loads through buffer resources, the expand as extra K steps only
+// BUF: loads through buffer resources. The expand runs as extra K steps, in
+// the 128-row tile also in the epilogue.
 template <int BM, int BN, int WM, int WN, int NS, bool BUF>
 static hipError_t launch_mx4(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* wsc, uint16_t* Y,
                              int M, int N, int K16, const Fuse& f, hipStream_t st, StageTimer* tm) {
@@ -22,7 +23,7 @@ static hipError_t launch_mx4(const uint8_t* xc, const uint8_t* xs, const uint8_t
     const bool ktail = K16 % 64 != 0;
     auto ker = ktail ? mx4_tile_kernel<BM, BN, WM, WN, NS, false, true, BUF>
                      : mx4_tile_kernel<BM, BN, WM, WN, NS, false, false, BUF>;
-    if constexpr (!BUF) {
+    if constexpr (BM == 128) {
         if (f.adapters && !f.ext)
             ker = ktail ? mx4_tile_kernel<BM, BN, WM, WN, NS, true, true, BUF>
                         : mx4_tile_kernel<BM, BN, WM, WN, NS, true, false, BUF>;
@@ -35,10 +36,31 @@ hipError_t mx4_gemm(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, con
                     int N, int K, const Fuse& f, hipStream_t st, StageTimer* tm) {
     const int K16 = (int)(mx4_row_bytes(K) / 2);  // a row's bytes in the 16-bit units the tile counts in
     const bool extra = !f.adapters || f.ext;
-    auto n_tiles = [&](int bm, int bn) { return (int64_t)cdiv(M, bm) * cdiv(N, bn); };
-    if (n_tiles(256, 256) >= 200 && extra && tile_buffers_fit(M, N, K16, 256, f))
-        return launch_mx4<256, 256, 2, 2, 2, true>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
-    return launch_mx4<128, 128, 2, 4, 3, false>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+    // the macro tile with the least (rounds of 256 tiles) x (time of one
+    // tile); relative times measured at K = 4096 with every CU busy (a tile
+    // alone: 64 x 128 8 us, 128 x 128 11 us, 256 x 128 17 us)
+    struct Cand {
+        int bm, bn;
+        double t;
+    };
+    constexpr Cand cands[] = {{256, 256, 38.0}, {256, 128, 22.0}, {128, 128, 13.5}, {64, 128, 9.0}};
+    int best = 2;  // 128 x 128 has the epilogue form of the expand
+    double cost = 0.0;
+    for (int c = 0; c < 4 && extra; ++c) {
+        if (c == 0 && !tile_buffers_fit(M, N, K16, 256, f)) continue;
+        const int64_t n = (int64_t)cdiv(M, cands[c].bm) * cdiv(N, cands[c].bn);
+        const double t = (double)((n + 255) / 256) * cands[c].t;
+        if (cost == 0.0 || t < cost) {
+            cost = t;
+            best = c;
+        }
+    }
+    switch (best) {
+        case 0: return launch_mx4<256, 256, 2, 2, 2, true>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+        case 1: return launch_mx4<256, 128, 4, 2, 2, false>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+        case 2: return launch_mx4<128, 128, 2, 4, 3, false>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+        default: return launch_mx4<64, 128, 2, 4, 4, false>(xc, xs, wc, wsc, Y, M, N, K16, f, st, tm);
+    }
 }
 
 }  // namespace lora

@@ -357,7 +357,7 @@ struct Mx4Prep {
     const float* scale;
     int n_items, r_max, hs, hkc;
     float* h;       // [hs][M][r_max] (ext null)
-    uint16_t* ext;  // the expand operand (hs == 1)
+    uint16_t* ext;  // the expand operand (with hs > 1 h holds the planes before)
 };
 
 // 8 waves: 51 us for 2048 x 14336 rows (144 items) beside 4096 x 14336 of W,
@@ -387,12 +387,45 @@ __global__ __launch_bounds__(64 * kPrepWaves) void mx4_prep_kernel(Mx4Prep a) {
         dequantize_tile<uint16_t, true, 64 * WAVES>(a.wc, a.ws, a.N, a.K, a.W, t % kts, t / kts, st);
 }
 
+// The expand operand of an item's rows from hs planes of h, added in order.
+__global__ __launch_bounds__(256) void mx4_operand_kernel(Mx4Prep a) {
+    const Item it = a.work[blockIdx.x];
+    const int r = a.rank[it.slot];
+    if (r == 0) return;
+    const float sc = a.scale[it.slot];
+    const int rp = (a.r_max + 7) & ~7;
+    for (int i = threadIdx.x; i < it.count * rp; i += 256) {
+        const int m = i / rp, q = i - m * rp;
+        const int64_t p = it.begin + m;
+        float v = 0.f;
+        if (q < r)
+            for (int z = 0; z < a.hs; ++z) v += a.h[((int64_t)z * a.M + p) * a.r_max + q];
+        v *= sc;
+        const uint16_t hi = f32_to_bf16(v);
+        a.ext[(p * 2) * rp + q] = hi;
+        a.ext[(p * 2 + 1) * rp + q] = f32_to_bf16(v - bf16_to_f32(hi));
+    }
+}
+
+// K ranges of the shrink ahead of a tiled product. Over a long K and with few
+// items one range per item would outlast the other workgroups (8 waves take
+// about 1.3 us per 1024 k: 18 us at 14336), so that it is split and the planes
+// joined by one more launch (3 us): 512 x 14336 -> 4096 in 43 us against 65.
+// At K = 4096, or with 144 items at 14336, one range is as fast.
+static int prep_ranges(int K, int n_items) {
+    return K < 8192 ? 1 : max(1, min(min(8, K / 2048), 256 / max(n_items, 1)));
+}
+
 template <bool QUANT>
 static hipError_t launch_prep(const Mx4Prep& a, hipStream_t st, StageTimer* tm) {
     const int64_t tiles = ((int64_t)(QUANT ? a.M : a.N) + 63) / 64 * mx4_k_tiles(a.K);
     const dim3 grid((uint32_t)(a.n_items * a.hs + tiles));
     const char* name = QUANT ? "mx4_quantize+shrink" : "mx4_dequantize+shrink";
-    return launch(tm, name, mx4_prep_kernel<QUANT>, grid, dim3(64 * kPrepWaves), st, a);
+    Mx4Prep k = a;
+    if (a.ext && a.hs > 1) k.ext = nullptr;  // planes first
+    const hipError_t e = launch(tm, name, mx4_prep_kernel<QUANT>, grid, dim3(64 * kPrepWaves), st, k);
+    if (e != hipSuccess || !a.ext || a.hs == 1 || a.n_items == 0) return e;
+    return launch(tm, "mx4_operand", mx4_operand_kernel, dim3(a.n_items), dim3(256), st, a);
 }
 
 // rows of any width -> rows of Kp elements (a multiple of 8), zeros behind
@@ -408,7 +441,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 // same one).
 enum class Mx4Path { kSplit, kTile4, kDequant };
 static Mx4Path mx4_path(int M, int N, int K, bool act4) {
-    if (act4) return (int64_t)cdiv(M, 64) * cdiv(N, 64) <= 256 ? Mx4Path::kSplit : Mx4Path::kTile4;
+    if (act4) return M <= 64 || (int64_t)cdiv(M, 64) * cdiv(N, 64) <= 128 ? Mx4Path::kSplit : Mx4Path::kTile4;
     return gemm_bf16_plan(M, N, K).nsub != 0 && (int64_t)M * K * 2 < int64_t(1) << 31 ? Mx4Path::kSplit
                                                                                      : Mx4Path::kDequant;
 }
@@ -456,7 +489,7 @@ static Mx4SplitPlan mx4_split_plan(int M, int N, int K, int S, bool act4) {
 // activations, then the path's own (partials and h planes; h or the expand
 // operand; W in bf16 and the bf16 layer's workspace).
 struct Mx4Space {
-    size_t xpad, apad, codes, scales, own, h, total;
+    size_t xpad, apad, codes, scales, own, h, planes, total;
 };
 static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
     const int Kp = (K + 7) / 8 * 8;
@@ -478,10 +511,14 @@ static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
             s.h = take((size_t)p.hs * M * r_max * sizeof(float));
             break;
         }
-        case Mx4Path::kTile4: s.own = take(tiled_workspace(M, r_max)); break;
+        case Mx4Path::kTile4:
+            s.own = take(tiled_workspace(M, r_max));
+            s.planes = take((size_t)8 * M * r_max * sizeof(float));
+            break;
         case Mx4Path::kDequant:
             s.own = take((size_t)N * Kp * 2);
             s.h = take(gemm_bf16_workspace(M, &N, 1, Kp, r_max));
+            s.planes = take((size_t)8 * M * r_max * sizeof(float));
     }
     s.total = o;
     return s;
@@ -571,6 +608,9 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
             pr.h = h;
             if (ext_ok) {
                 pr.ext = reinterpret_cast<uint16_t*>(h);
+                pr.h = reinterpret_cast<float*>(ws + sp.planes);
+                pr.hs = prep_ranges(L.K, pr.n_items);
+                pr.hkc = (cdiv(L.K, pr.hs) + 31) / 32 * 32;
                 f.ext = pr.ext;
                 f.h = nullptr;
             }
@@ -587,8 +627,14 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
     sl.W = pr.W;
     L.workspace = ws + sp.h;
     const bool beside = ext_ok && gemm_bf16_plan(M, N, L.K).tks < 2;
-    if (beside) pr.ext = reinterpret_cast<uint16_t*>(ws + sp.h);
-    else pr.n_items = 0;
+    if (beside) {
+        pr.ext = reinterpret_cast<uint16_t*>(ws + sp.h);
+        pr.h = reinterpret_cast<float*>(ws + sp.planes);
+        pr.hs = prep_ranges(L.K, pr.n_items);
+        pr.hkc = (cdiv(L.K, pr.hs) + 31) / 32 * 32;
+    } else {
+        pr.n_items = 0;
+    }
     e = launch_prep<false>(pr, st, tm);
     if (e != hipSuccess) return e;
     return beside ? tiled_forward_ready(L, sl, pr.ext, st, tm) : lora_forward_bf16(L, st, tm);

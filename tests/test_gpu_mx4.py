@@ -197,6 +197,10 @@ SHAPES = [
     (1000, 512, 2048, [0] + [16] * 16, None),
     (700, 1288, 4096, [0] + [12] * 3, None),
     (520, 320, 8200, [0, 100, 8], None),
+    (520, 256, 8200, [0, 16, 8], None),
+    (300, 8200, 300, [0, 16, 0, 8], None),
+    (700, 8192, 1100, [0, 8, 24], None),
+    (1500, 520, 3100, [0, 16, 64], None),
     (3601, 288, 3500, [0, 16, 8, 0, 64], None),
     (3600, 512, 3591, [0] + [16] * 16, None),
     (3400, 264, 3900, [0, 12, 4], None),
