@@ -7,23 +7,23 @@
 
 namespace lora {
 
-template <class T, bool VEC>
+template <class T>
 __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__ src, int64_t rows, int64_t K,
                                                            uint8_t* __restrict__ codes,
                                                            uint8_t* __restrict__ scales) {
     __shared__ uint8_t st[kMxTileBytes];
     const int64_t mat = blockIdx.z;
-    quantize_tile<T, VEC, 256>(src + mat * rows * K, rows, K, nullptr, codes + mat * rows * mx4_row_bytes(K),
+    quantize_tile<T, 256>(src + mat * rows * K, rows, K, nullptr, codes + mat * rows * mx4_row_bytes(K),
                                scales + mat * mx4_scale_bytes(rows, K), blockIdx.x, blockIdx.y, st);
 }
 
-template <class T, bool VEC>
+template <class T>
 __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, int64_t rows,
                                                              int64_t K, T* __restrict__ dst) {
     __shared__ uint8_t st[kMxTileBytes];
     const int64_t mat = blockIdx.z;
-    dequantize_tile<T, VEC, 256>(codes + mat * rows * mx4_row_bytes(K), scales + mat * mx4_scale_bytes(rows, K), rows,
+    dequantize_tile<T, 256>(codes + mat * rows * mx4_row_bytes(K), scales + mat * mx4_scale_bytes(rows, K), rows,
                                  K, dst + mat * rows * K, blockIdx.x, blockIdx.y, st);
 }
 
@@ -49,9 +49,7 @@ static dim3 mx4_grid(int64_t batch, int64_t rows, int64_t K) {
 template <class T>
 static hipError_t quantize(const void* src, int64_t batch, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
                            hipStream_t st, StageTimer* tm) {
-    const bool vec = K % 8 == 0 && (uintptr_t)src % 16 == 0;
-    return launch(tm, "mx4_quantize", vec ? mx4_quantize_kernel<T, true> : mx4_quantize_kernel<T, false>,
-                  mx4_grid(batch, rows, K), dim3(256), st, (const T*)src, rows, K, codes, scales);
+    return launch(tm, "mx4_quantize", mx4_quantize_kernel<T>, mx4_grid(batch, rows, K), dim3(256), st, (const T*)src, rows, K, codes, scales);
 }
 
 hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows, int64_t K, uint8_t* codes,
@@ -63,9 +61,7 @@ hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows,
 template <class T>
 static hipError_t dequantize(const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows, int64_t K,
                              void* dst, hipStream_t st, StageTimer* tm) {
-    const bool vec = K % 8 == 0 && (uintptr_t)dst % 16 == 0;
-    return launch(tm, "mx4_dequantize", vec ? mx4_dequantize_kernel<T, true> : mx4_dequantize_kernel<T, false>,
-                  mx4_grid(batch, rows, K), dim3(256), st, codes, scales, rows, K, (T*)dst);
+    return launch(tm, "mx4_dequantize", mx4_dequantize_kernel<T>, mx4_grid(batch, rows, K), dim3(256), st, codes, scales, rows, K, (T*)dst);
 }
 
 hipError_t mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows,

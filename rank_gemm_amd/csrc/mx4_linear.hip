@@ -382,9 +382,9 @@ __global__ __launch_bounds__(64 * kPrepWaves) void mx4_prep_kernel(Mx4Prep a) {
     const int kts = (int)mx4_k_tiles(a.K), t = blockIdx.x - n_shrink;
     uint8_t* st = reinterpret_cast<uint8_t*>(red);
     if constexpr (QUANT)
-        quantize_tile<uint16_t, true, 64 * WAVES>(a.X, a.M, a.K, a.token_order, a.xc, a.xs, t % kts, t / kts, st);
+        quantize_tile<uint16_t, 64 * WAVES>(a.X, a.M, a.K, a.token_order, a.xc, a.xs, t % kts, t / kts, st);
     else
-        dequantize_tile<uint16_t, true, 64 * WAVES>(a.wc, a.ws, a.N, a.K, a.W, t % kts, t / kts, st);
+        dequantize_tile<uint16_t, 64 * WAVES>(a.wc, a.ws, a.N, a.K, a.W, t % kts, t / kts, st);
 }
 
 // The expand operand of an item's rows from hs planes of h, added in order.
@@ -411,9 +411,9 @@ __global__ __launch_bounds__(256) void mx4_operand_kernel(Mx4Prep a) {
 // items one range per item would outlast the other workgroups (8 waves take
 // about 1.3 us per 1024 k: 18 us at 14336), so that it is split and the planes
 // joined by one more launch (3 us): 512 x 14336 -> 4096 in 43 us against 65.
-// At K = 4096, or with 144 items at 14336, one range is as fast.
+// At K = 4096, or with 128 items at 14336, one range is as fast.
 static int prep_ranges(int K, int n_items) {
-    return K < 8192 ? 1 : max(1, min(min(8, K / 2048), 256 / max(n_items, 1)));
+    return K < 8192 ? 1 : max(1, min(min(8, K / 2048), 128 / max(n_items, 1)));
 }
 
 template <bool QUANT>
