@@ -153,32 +153,31 @@ __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict
 // ---------------------------------------------------------------- experts --
 // The (token, choice) pairs grouped by expert: order lists the pairs of
 // active expert a at [first[a], first[a + 1]); pairs whose id is outside
-// [0, E) are left out. Every workgroup builds it in LDS from the ids (more
-// than 64 pairs; fewer take moe_find).
-constexpr int kMoePlanThreads = 512;
+// [0, E) are left out. Over more than 64 pairs one workgroup makes it once
+// for both kernels (in each of their workgroups its barriers cost about as
+// much as the workgroup's loads); fewer take moe_find.
 struct MoePlan {
-    int n;                         // experts reached
-    int expert[kMoeMaxPairs];      // ascending
+    int n;                        // experts reached
+    int expert[kMoeMaxPairs];     // ascending
     int first[kMoeMaxPairs + 1];
-    int16_t order[kMoeMaxPairs];   // sorted position -> pair
-    int cnt[kMoeMaxExperts];
-    int wsum[2][kMoePlanThreads / 64];
+    int order[kMoeMaxPairs];      // sorted position -> pair
 };
 
-__device__ __forceinline__ void moe_plan(const int32_t* __restrict__ ids, int P, int E, MoePlan& pl) {
+__global__ __launch_bounds__(512) void moe_plan_kernel(const int32_t* __restrict__ ids, int P, int E,
+                                                       MoePlan* __restrict__ pl) {
+    __shared__ int cnt[kMoeMaxExperts];
+    __shared__ int wsum[2][8];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    static_assert(kMoeMaxExperts == kMoePlanThreads && kMoeMaxPairs == kMoePlanThreads,
-                  "one expert and one pair a thread");
-    const bool on = tid < kMoePlanThreads;
+    static_assert(kMoeMaxExperts == 512 && kMoeMaxPairs == 512, "one expert and one pair a thread");
     const int id = tid < P ? ids[tid] : -1;
-    if (on) pl.cnt[tid] = 0;
+    cnt[tid] = 0;
     __syncthreads();
     const bool ok = id >= 0 && id < E;
     // the place of a pair inside its expert's run only says which column of
     // the products it rides in: the results do not depend on it
-    const int at = ok ? atomicAdd(&pl.cnt[id], 1) : 0;
+    const int at = ok ? atomicAdd(&cnt[id], 1) : 0;
     __syncthreads();
-    const int c = on ? pl.cnt[tid] : 0;
+    const int c = cnt[tid];
     int s = c, a = c > 0;  // inclusive sums of pairs and of reached experts
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -188,29 +187,27 @@ __device__ __forceinline__ void moe_plan(const int32_t* __restrict__ ids, int P,
             a += pa;
         }
     }
-    if (on && lane == 63) {
-        pl.wsum[0][wave] = s;
-        pl.wsum[1][wave] = a;
+    if (lane == 63) {
+        wsum[0][wave] = s;
+        wsum[1][wave] = a;
     }
     __syncthreads();
-    if (on) {
-        for (int w = 0; w < wave; ++w) {
-            s += pl.wsum[0][w];
-            a += pl.wsum[1][w];
-        }
-        if (c > 0) {
-            pl.expert[a - 1] = tid;
-            pl.first[a - 1] = s - c;
-        }
-        if (tid == kMoePlanThreads - 1) {
-            pl.n = a;
-            pl.first[a] = s;
-        }
-        pl.cnt[tid] = s - c;  // first sorted position of expert tid
+    for (int w = 0; w < wave; ++w) {
+        s += wsum[0][w];
+        a += wsum[1][w];
+    }
+    if (c > 0) {
+        pl->expert[a - 1] = tid;
+        pl->first[a - 1] = s - c;
+    }
+    if (tid == 511) {
+        pl->n = a;
+        pl->first[a] = s;
     }
     __syncthreads();
-    if (ok) pl.order[pl.cnt[id] + at] = (int16_t)tid;
+    cnt[tid] = s - c;  // first sorted position of expert tid
     __syncthreads();
+    if (ok) pl->order[cnt[id] + at] = tid;
 }
 
 // Active expert z of at most 64 pairs, in the order of first mention, found by
@@ -218,11 +215,10 @@ __device__ __forceinline__ void moe_plan(const int32_t* __restrict__ ids, int P,
 // lane), each wave's list of them in its own part of LDS.
 constexpr int kMoeWavePairs = 64;
 struct MoeRun {
-    int e, n;              // expert (or -1: fewer than z + 1 are reached), its pairs
-    const int16_t* order;  // their indices
+    int e, n;          // expert (or -1: fewer than z + 1 are reached), its pairs
+    const int* order;  // their indices
 };
-__device__ __forceinline__ MoeRun moe_find(const int32_t* __restrict__ ids, int P, int E, int z, int16_t* list,
-                                           int lane) {
+__device__ __forceinline__ MoeRun moe_find(const int32_t* __restrict__ ids, int P, int E, int z, int* list, int lane) {
     const int id = lane < P ? ids[lane] : -1;
     const bool ok = id >= 0 && id < E;
     uint64_t left = __ballot(ok);
@@ -233,7 +229,7 @@ __device__ __forceinline__ MoeRun moe_find(const int32_t* __restrict__ ids, int 
         if (c == z) {
             r.e = ex;
             r.n = __popcll(mine);
-            if ((mine >> lane) & 1) list[__popcll(mine & ((1ull << lane) - 1))] = (int16_t)lane;
+            if ((mine >> lane) & 1) list[__popcll(mine & ((1ull << lane) - 1))] = lane;
             break;
         }
         left &= ~mine;
@@ -241,18 +237,14 @@ __device__ __forceinline__ MoeRun moe_find(const int32_t* __restrict__ ids, int 
     return r;
 }
 
-// The run of pairs a workgroup of the experts' kernels works on.
-template <int NW>
-__device__ __forceinline__ MoeRun moe_run(const MoeArgs& a, int z, MoePlan& pl, int lane, int wave) {
-    const int P = a.T * a.k;
-    if (P <= kMoeWavePairs) {
-        static_assert(NW * kMoeWavePairs * sizeof(int16_t) <= sizeof(pl.cnt), "a list per wave");
-        return moe_find(a.ids, P, a.E, z, reinterpret_cast<int16_t*>(pl.cnt) + wave * kMoeWavePairs, lane);
-    }
-    moe_plan(a.ids, P, a.E, pl);
-    if (z >= pl.n) return MoeRun{-1, 0, nullptr};
-    const int lo = __builtin_amdgcn_readfirstlane(pl.first[z]), hi = __builtin_amdgcn_readfirstlane(pl.first[z + 1]);
-    return MoeRun{__builtin_amdgcn_readfirstlane(pl.expert[z]), hi - lo, pl.order + lo};
+// The run of pairs a workgroup of the experts' kernels works on. lists: LDS,
+// kMoeWavePairs per wave.
+__device__ __forceinline__ MoeRun moe_run(const MoeArgs& a, const MoePlan* __restrict__ pl, int z, int* lists,
+                                          int lane, int wave) {
+    if (a.T * a.k <= kMoeWavePairs) return moe_find(a.ids, a.T * a.k, a.E, z, lists + wave * kMoeWavePairs, lane);
+    if (z >= pl->n) return MoeRun{-1, 0, nullptr};
+    const int lo = pl->first[z];
+    return MoeRun{pl->expert[z], pl->first[z + 1] - lo, pl->order + lo};
 }
 
 // A tile's products go in steps: 128 k (4-bit, 2 a tile of 256 k) or 32 k
@@ -373,11 +365,12 @@ __device__ __forceinline__ int moe_at(int i) {
 // mantissa instead of 8) in act[pair][2][moe_act_row(I)]. A pass takes 16 or,
 // where more are left, 32 of the expert's pairs.
 template <bool MX, int NW>
-__global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint16_t* __restrict__ act) {
-    __shared__ MoePlan pl;
+__global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, const MoePlan* __restrict__ pl,
+                                                                 uint16_t* __restrict__ act) {
+    __shared__ int lists[NW * kMoeWavePairs];
     __shared__ f32x4 red[NW][4][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const MoeRun run = moe_run<NW>(a, blockIdx.y, pl, lane, wave);
+    const MoeRun run = moe_run(a, pl, blockIdx.y, lists, lane, wave);
     if (run.e < 0) return;  // uniform for the workgroup
     const int e = run.e, hi = run.n;
     const int r0 = blockIdx.x * 32, kts = (a.H + kTileK<MX> - 1) / kTileK<MX>, Ir = moe_act_row(a.I);
@@ -448,12 +441,13 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, uint
 // order, into o[pair][H] in fp32; every pair has one expert, so each element
 // is written once.
 template <bool MX, int NW>
-__global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(MoeArgs a, const uint16_t* __restrict__ act,
+__global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(MoeArgs a, const MoePlan* __restrict__ pl,
+                                                              const uint16_t* __restrict__ act,
                                                               float* __restrict__ o) {
-    __shared__ MoePlan pl;
+    __shared__ int lists[NW * kMoeWavePairs];
     __shared__ f32x4 red[NW][4][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const MoeRun run = moe_run<NW>(a, blockIdx.y, pl, lane, wave);
+    const MoeRun run = moe_run(a, pl, blockIdx.y, lists, lane, wave);
     if (run.e < 0) return;  // uniform for the workgroup
     const int e = run.e, hi = run.n;
     const int r0 = blockIdx.x * 64, kts = (a.I + kTileK<MX> - 1) / kTileK<MX>;
@@ -536,7 +530,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs a, const float
 }
 
 // Both forms sum a logit in the same order, so they choose alike.
-constexpr int64_t kMoeRouteOne = 1 << 18;  // router values one workgroup reads: 512 KB
+constexpr int64_t kMoeRouteOne = 1 << 16;  // router values one workgroup reads: 128 KB
 
 size_t moe_route_workspace(int T, int H, int E) {
     return (int64_t)E * H <= kMoeRouteOne ? 0 : (size_t)T * E * sizeof(double);
@@ -555,25 +549,31 @@ hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, in
                   weights);
 }
 
-// the inner values of every pair, then its down products
+// the inner values of every pair, its down products, then the plan
+static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 static size_t moe_act_bytes(int T, int I, int k) {
-    return ((size_t)T * k * 2 * moe_act_row(I) * sizeof(uint16_t) + 255) & ~size_t(255);
+    return align256((size_t)T * k * 2 * moe_act_row(I) * sizeof(uint16_t));
 }
 size_t moe_experts_workspace(int T, int H, int I, int k) {
-    return moe_act_bytes(T, I, k) + (size_t)T * k * H * sizeof(float);
+    return moe_act_bytes(T, I, k) + align256((size_t)T * k * H * sizeof(float)) + align256(sizeof(MoePlan));
 }
 
 template <bool MX>
 static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
     constexpr int NW = 8;  // waves of a workgroup
-    uint16_t* act = static_cast<uint16_t*>(a.workspace);
-    float* o = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + moe_act_bytes(a.T, a.I, a.k));
     const int P = a.T * a.k, reached = P < a.E ? P : a.E;  // experts at most
-    hipError_t e = launch(tm, "moe_gate_up", moe_gate_up_kernel<MX, NW>, dim3(moe_inner(a.I) / 32, reached),
-                          dim3(64 * NW), st, a, act);
+    char* ws = static_cast<char*>(a.workspace);
+    uint16_t* act = reinterpret_cast<uint16_t*>(ws);
+    float* o = reinterpret_cast<float*>(ws + moe_act_bytes(a.T, a.I, a.k));
+    MoePlan* pl = reinterpret_cast<MoePlan*>(ws + moe_act_bytes(a.T, a.I, a.k) + align256((size_t)P * a.H * sizeof(float)));
+    hipError_t e = hipSuccess;
+    if (P > kMoeWavePairs) e = launch(tm, "moe_plan", moe_plan_kernel, dim3(1), dim3(512), st, a.ids, P, a.E, pl);
+    if (e == hipSuccess)
+        e = launch(tm, "moe_gate_up", moe_gate_up_kernel<MX, NW>, dim3(moe_inner(a.I) / 32, reached), dim3(64 * NW), st,
+                   a, (const MoePlan*)pl, act);
     if (e == hipSuccess)
         e = launch(tm, "moe_down", moe_down_kernel<MX, NW>, dim3((a.H + 63) / 64, reached), dim3(64 * NW), st, a,
-                   (const uint16_t*)act, o);
+                   (const MoePlan*)pl, (const uint16_t*)act, o);
     if (e == hipSuccess)
         e = launch(tm, "moe_combine", moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.T), dim3(256), st, a,
                    (const float*)o);
