@@ -512,6 +512,7 @@ __device__ __forceinline__ void gemm_tile(const uint16_t* __restrict__ X, const 
     for (; kt < nt; ++kt, adv()) step(kt, base_next, XF{}, bcr, XF{});
     frags_landed(A0);
     frags_landed(B0);
+    scales_landed(sA0, sB0);  // the last step's reads are waited on while their registers live
     vm_landed<0>();
 #pragma unroll
     for (int i = 0; i < 12; ++i) asm volatile("s_nop 7");  // last MFMA results written

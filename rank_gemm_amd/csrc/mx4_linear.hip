@@ -339,6 +339,159 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
         for (int j = 0; j < 2; ++j) out[(i * 4 + cb + j) * 64 + lane] = acc[i][j] + red[(i * 2 + j) * 64 + lane];
 }
 
+// Kernel 2: a wave takes 16 rows x 64 columns, adds the splits in order, runs
+// the expand on the matrix cores and stores whole row pieces. The bf16 path's
+// kernel 2 (splitk.hip) gives the same 16 x 64 to four waves, each of which
+// loads the rows' h and slot metadata again and holds 196 registers: it is
+// faster while its blocks fit the chip at once (two a CU; 4.0 against 5.4 us
+// at 64 x 4096) and falls behind past that (8.7 against 5.7 us at 64 x 14336,
+// 24 against 9.5 us at 256 x 14336).
+// ADAPT: pools of at most 64 slots (slot s on lane s) and ranks up to 32.
+constexpr int kFinishSlots = 64, kFinishRank = 32, kFinishBlocks = 512;
+
+struct Mx4Finish {
+    const float* part;  // [ks][n_mt][n_nt][16 blocks][64 lanes] f32x4
+    const float* h;     // [hs][M][r_max]
+    uint16_t* Y;
+    int M, N, ks, n_mt, n_nt, hs, S, r_max;
+    const int32_t *token_order, *slot_indptr, *rank;
+    const float* scale;
+    const uint16_t* B_pool;
+};
+
+template <bool ADAPT>
+__global__ __launch_bounds__(256) void mx4_finish_kernel(Mx4Finish a) {
+    __shared__ u32x4 stg[4][16 * 9];  // a wave's 16 rows of 64 columns, 16 bytes of padding each
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nt = blockIdx.x, mt = blockIdx.y, p0 = mt * 64 + wave * 16, n0 = nt * 64;
+    if (p0 >= a.M) return;  // the waves do not meet
+    const int fr = lane & 15, fc = lane >> 4;
+    const f32x4* in = reinterpret_cast<const f32x4*>(a.part) + ((int64_t)mt * a.n_nt + nt) * 1024 + wave * 256 + lane;
+    const int64_t plane = (int64_t)a.n_mt * a.n_nt * 1024;
+    f32x4 acc[4];
+    f32x4 p[2][4];
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[z][j] = in[min(z, a.ks - 1) * plane + j * 64];
+    int tok[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) tok[i] = a.token_order[min(p0 + 8 * i + (lane >> 3), a.M - 1)];
+    u32x4 hi{0, 0, 0, 0}, lo{0, 0, 0, 0};
+    int slot = 0, r = 0;  // of row p0 + fr
+    uint64_t slots = 0;   // the block's slots
+    if constexpr (ADAPT) {
+        const int ip = a.slot_indptr[min(lane, a.S)];
+        const int rk = a.rank[min(lane, a.S - 1)];
+        const float sv = a.scale[min(lane, a.S - 1)];
+        // lane (fr, fc): ranks 8 fc .. + 7 of row fr, every plane loaded
+        f32x4 hv[8][2];
+        const float* hp = a.h + (int64_t)min(p0 + fr, a.M - 1) * a.r_max + 8 * fc;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+            const bool ok = z < a.hs && 8 * fc < a.r_max;
+            const float* q = hp + (int64_t)z * a.M * a.r_max;
+            hv[z][0] = __builtin_bit_cast(f32x4, *or_zero(ok, q));
+            hv[z][1] = __builtin_bit_cast(f32x4, *or_zero(ok, q + 4));
+        }
+        issue_fence();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            // slot of row p0 + j: how many of the slots 1 .. S - 1 start at or before it
+            const int s = __popcll(__ballot(lane >= 1 && lane < a.S && ip <= p0 + j));
+            if (fr == j) slot = s;
+            if (p0 + j < a.M) slots |= 1ull << s;
+        }
+        slots &= ~1ull;
+        r = __shfl(rk, slot);  // by every lane: slot s is on lane s
+        r = slot == 0 ? 0 : r;
+        const float sc = __shfl(sv, slot);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float x = 0.f;
+#pragma unroll
+            for (int z = 0; z < 8; ++z) x += hv[z][e >> 2][e & 3];
+            // past the rank the planes hold nothing
+            v[e] = 8 * fc + e < r ? x * sc : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+            lo[e] = pack_bf16x2(v[2 * e] - __uint_as_float(hi[e] << 16),
+                                v[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = a.ks > 1 ? p[0][j] + p[1][j] : p[0][j];
+    for (int z0 = 2; z0 < a.ks; z0 += 2) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[z][j] = in[min(z0 + z, a.ks - 1) * plane + j * 64];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            acc[j] += p[0][j];
+            if (z0 + 1 < a.ks) acc[j] += p[1][j];
+        }
+    }
+    if constexpr (ADAPT) {
+        // two slots at a time: their B rows (lane (fr, fc): column fr of a
+        // block, ranks 8 fc ..) loaded together
+        while (slots) {
+            u32x4 b[2][4];
+            int s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[i] = slots ? (int)__builtin_ctzll(slots) : 0;
+                slots &= slots - 1;
+                const int rs = s[i] ? a.rank[s[i]] : 0;  // uniform
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = n0 + 16 * j + fr;
+                    b[i][j] = *or_zero(n < a.N && 8 * fc < rs,
+                                       a.B_pool + ((int64_t)s[i] * a.N + n) * a.r_max + 8 * fc);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool on = slot == s[i];
+                u32x4 h1, h2;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h1[e] = on ? hi[e] : 0u;
+                    h2[e] = on ? lo[e] : 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 d = mfma16x16x32(h2, b[i][j], mfma16x16x32(h1, b[i][j], f32x4{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+                }
+            }
+        }
+    }
+    // lane: rows 4 fc + e, column 16 j + fr -> rows of 128 bytes
+    uint16_t* t = reinterpret_cast<uint16_t*>(stg[wave]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[(4 * fc + e) * 72 + 16 * j + fr] = f32_to_bf16(acc[j][e]);
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + (lane >> 3), n = n0 + 8 * c;
+        const u32x4 v = stg[wave][row * 9 + c];
+        if (p0 + row >= a.M || n >= a.N) continue;
+        uint16_t* y = a.Y + (int64_t)tok[i] * a.N + n;
+        if (a.N % 8 == 0) {
+            *reinterpret_cast<u32x4*>(y) = v;
+        } else {
+            for (int e = 0; e < min(8, a.N - n); ++e) y[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
 // -------------------------------------------------- before the products --
 // What a call does to one operand (x to 4 bits in plan order, or W's values
 // to bf16) and the SGMV shrink depend on nothing of each other: one launch,
@@ -599,7 +752,13 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
             }
             e = launch_split(a, act4, st, tm);
             if (e != hipSuccess) return e;
-            return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
+            if (L.S > kFinishSlots || L.r_max > kFinishRank || L.r_max % 8 != 0 ||
+                (int64_t)p.n_nt * cdiv(M, 16) <= kFinishBlocks)
+                return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
+            const Mx4Finish fin{a.part, a.part_h, sl.Y, M, N, p.ks, p.n_mt, p.n_nt, p.hs, L.S, L.r_max, L.token_order,
+                                L.slot_indptr, sl.rank, sl.scale, sl.B_pool};
+            return launch(tm, "mx4_finish", L.adapters ? mx4_finish_kernel<true> : mx4_finish_kernel<false>,
+                          dim3(p.n_nt, p.n_mt), dim3(256), st, fin);
         }
         case Mx4Path::kTile4: {
             float* h = reinterpret_cast<float*>(ws + sp.own);

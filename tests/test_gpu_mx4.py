@@ -198,6 +198,10 @@ SHAPES = [
     (700, 1288, 4096, [0] + [12] * 3, None),
     (520, 320, 8200, [0, 100, 8], None),
     (520, 256, 8200, [0, 16, 8], None),
+    (64, 512, 14337, [0, 16, 8, 32, 0, 1], 32),
+    (50, 2304, 14336, [0] + [16] * 16, None),
+    (250, 512, 8200, [0] + [8, 24, 3] * 20, 24),
+    (64, 256, 14336, [0, 16] * 33, None),
     (300, 8200, 300, [0, 16, 0, 8], None),
     (700, 8192, 1100, [0, 8, 24], None),
     (1500, 520, 3100, [0, 16, 64], None),
