@@ -258,13 +258,16 @@ template <bool MX>
 constexpr int kPieces = MX ? 4 : 1;
 
 // RB 16-row blocks of one expert's matrix from row r0 on, read through buffer
-// resources: per-lane row offsets, the k of a tile in the uniform offset.
-// Codes or values past a row's end are the next row's (zeros at the matrix's
-// end); they meet zeros of the other operand.
+// resources: per-lane row offsets, the k of a tile in the uniform offset (at
+// most a row's bytes, so that it never passes the resource's). Codes past a
+// row's end are the next row's: any code under the zero scale bytes there is
+// finite, and they meet zeros of x. 16-bit values past a row's end are not
+// read: the next row's may be infinite.
 template <bool MX, int RB>
 struct WRows {
     brsrc data, scales;
     uint32_t off[RB], soff;
+    int bytes;  // of a row
 };
 template <bool MX, int RB>
 __device__ __forceinline__ WRows<MX, RB> rows_of(const MoeWeights& W, int e, int N, int K, int r0, int lane) {
@@ -274,6 +277,7 @@ __device__ __forceinline__ WRows<MX, RB> rows_of(const MoeWeights& W, int e, int
     WRows<MX, RB> r;
     r.data = make_rsrc(static_cast<const uint8_t*>(W.data) + (int64_t)e * N * rb, (uint32_t)(N * rb));
     r.scales = make_rsrc(MX ? W.scales + (int64_t)e * sb : nullptr, MX ? (uint32_t)sb : 0u);
+    r.bytes = (int)rb;
     r.soff = (uint32_t)((r0 >> 6) * kts * kMxTileBytes) + lane * 8;
 #pragma unroll
     for (int j = 0; j < RB; ++j) r.off[j] = (uint32_t)(min(r0 + 16 * j + fr, N - 1) * rb) + fc * 16;
@@ -287,16 +291,19 @@ struct WTile {
     u32x2 sc;  // 4-bit: scale words of the tile's 64-row group
 };
 template <bool MX, int RB>
-__device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>& r, int kt) {
+__device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>& r, int kt, int lane) {
     constexpr int TB = kTileK<MX> * (MX ? 1 : 4) / 2;  // bytes of a row in a tile
     if constexpr (MX)
         t.sc = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r.scales, r.soff, kt * kMxTileBytes, 0));
 #pragma unroll
-    for (int s = 0; s < kSteps<MX>; ++s)
+    for (int s = 0; s < kSteps<MX>; ++s) {
+        const int at = kt * TB + s * 64;
+        const bool in = MX || at + (lane >> 4) * 16 < r.bytes;
 #pragma unroll
         for (int j = 0; j < RB; ++j)
-            t.w[j][s] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r.data, r.off[j], kt * TB + s * 64, 0));
+            t.w[j][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      r.data, in ? r.off[j] : kOutOfRange, min(at, r.bytes), 0));
+    }
 }
 
 // acc[c][j] += (16-row block j of the tile) (x[c][0] + x[c][1] + ..)^T over
@@ -341,8 +348,11 @@ __device__ __forceinline__ void load_x(brsrc x, uint32_t off, int K, int kt, int
 #pragma unroll
     for (int m = 0; m < kPieces<MX>; ++m) {
         const int k = PERM && MX ? 32 * fc + 8 * m : 32 * m + 8 * fc;
+        // the uniform offset stays inside the rows: stored rows (PERM) are
+        // whole 128-value groups and come in pairs, others end at K
+        const int at = PERM ? k0 * 2 + m * 64 : min(k0 + 32 * m, K) * 2;
         v[m] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             x, k0 + k < K ? off + fc * 16 : kOutOfRange, k0 * 2 + m * 64, 0));
+                                             x, k0 + k < K ? off + fc * 16 : kOutOfRange, at, 0));
     }
     if constexpr (MX && !PERM) mx4_transpose(v);
 }
@@ -392,8 +402,8 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, cons
             for (int j = 0; j < 2; ++j) g[c][j] = u[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kt = wave; kt < kts; kt += NW) {
             WTile<MX, 2> wg, wu;
-            load_wtile(wg, rg, kt);
-            load_wtile(wu, ru, kt);
+            load_wtile(wg, rg, kt, lane);
+            load_wtile(wu, ru, kt, lane);
 #pragma unroll
             for (int i = 0; i < kSteps<MX>; ++i) {
                 u32x4 x[NC][1][kPieces<MX>];
@@ -426,9 +436,9 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, cons
                 uint16_t* ap = act + (int64_t)run.order[q] * 2 * Ir + moe_at<MX>(i);
                 const uint16_t h = f32_to_bf16(v);
                 ap[0] = h;
-                // an infinite or NaN value has no remainder
+                // a value that is infinite or NaN, or rounds to infinity, has no remainder
                 const float rest = v - bf16_to_f32(h);
-                ap[Ir] = rest == rest ? f32_to_bf16(rest) : uint16_t(0);
+                ap[Ir] = fabsf(rest) < INFINITY ? f32_to_bf16(rest) : uint16_t(0);
             }
         }
     };
@@ -470,7 +480,7 @@ __global__ __launch_bounds__(64 * NW, 3) void moe_down_kernel(MoeArgs a, const M
             for (int j = 0; j < 4; ++j) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kt = wave; kt < kts; kt += NW) {
             WTile<MX, 4> w;
-            load_wtile(w, rd, kt);
+            load_wtile(w, rd, kt, lane);
 #pragma unroll
             for (int i = 0; i < kSteps<MX>; ++i) {
                 u32x4 x[NC][2][kPieces<MX>];

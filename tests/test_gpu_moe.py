@@ -160,6 +160,64 @@ def test_nan_token_stays_in_its_row():
 
 
 @pytest.mark.parametrize("form", ["bf16", "mx4"])
+@pytest.mark.parametrize("T,H,I", [(1, 8, 8), (5, 40, 24), (70, 72, 40)])
+def test_non_finite_weight_stays_in_its_row(T, H, I, form):
+    """Rows that end inside a tile: an infinity at the start of a row does not
+    reach the row before it."""
+    m = Moe(T, H, I, 2, 1, form, seed=H)
+    ids, w = torch.zeros((T, 1), dtype=torch.int32, device="cuda"), torch.ones((T, 1), device="cuda")
+    clean = m.experts(ids, w)
+    v = m.w[2] if form == "bf16" else lora.mx4_dequantize(m.w[2], "f32")
+    v = v.clone()
+    v[0, 3, 0] = float("inf")
+    v[1, 0, 0] = float("inf")  # the row behind the last one of expert 0
+    m.w[2] = v if form == "bf16" else lora.mx4_quantize(v)
+    y = m.experts(ids, w)
+    keep = [n for n in range(H) if n != 3]
+    assert not bool(torch.isfinite(y[:, 3]).any())
+    assert torch.equal(y[:, keep], clean[:, keep])
+    v = (m.w[1] if form == "bf16" else lora.mx4_dequantize(m.w[1], "f32")).clone()
+    v[0, 4, 0] = float("inf")  # one inner value: in every output, of expert 0 only
+    m.w[1] = v if form == "bf16" else lora.mx4_quantize(v)
+    assert not bool(torch.isfinite(m.experts(ids, w)).any())
+
+
+def test_inner_value_at_the_types_edge():
+    """An inner value that rounds past bf16's largest is an infinity, not a NaN."""
+    H = I = 8
+    x = torch.zeros((1, H), dtype=torch.bfloat16, device="cuda")
+    x[0, 0] = 1.0
+    gate, up, down = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((1, I, H), (1, I, H), (1, H, I)))
+    gate[0, 0, 0] = 2.0 ** 7 * (1 + 2.0 ** -7)  # silu(g) = g: a product just under 2^128
+    up[0, 0, 0] = 2.0 ** 120 * (2 - 2.0 ** -6)
+    down[0, :, 0] = 1.0
+    ids, w = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones((1, 1), device="cuda")
+    y = lora.moe_experts(x, ids, w, gate, up, down)
+    assert bool(torch.isinf(y).all())
+
+
+def test_two_streams():
+    """Layers on two streams at once share no workspace."""
+    layers = [Moe(32, 512, 256, 64, 4, "mx4", seed=s) for s in (1, 2)]
+
+    def layer(m):
+        ids, w = lora.moe_route(m.x, m.router, 4)
+        return lora.moe_experts(m.x, ids, w, *m.w)
+
+    want = [layer(m) for m in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(layer(layers[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx4"])
 def test_same_bits_every_time(form):
     m = Moe(64, 512, 256, 8, 4, form)
     ids, w = lora.moe_route(m.x, m.router, 4)
