@@ -26,6 +26,10 @@
  *    mlinterviewnotes.com).
  *  - Element type is the pool's: LORA_BF16 (uint16 bf16 bit patterns,
  *    fp32 accumulation, y rounded to nearest even) or LORA_F32.
+ *  - Besides the layer over bf16 or fp32 weights there are MXFP4 rows
+ *    (lora_mx4_*), the layer over an MXFP4 base weight (lora_linear_mx4) and a
+ *    mixture-of-experts layer for a few tokens (lora_moe_*), whose weights are
+ *    gathered per token as adapters are; each states its own types.
  *  - A call over T = 0 tokens returns LORA_OK at once, after checking the
  *    pool and plan arguments; its x, W, y and workspace pointers may then be
  *    null.
@@ -441,7 +445,8 @@ int lora_mx4_pack_scales(const void* e8m0, int batch, int rows, int K, void* sca
  * are copied to padded rows in the workspace when d_in is not a multiple of
  * 8; otherwise x must start on a 16-byte boundary). Every other argument,
  * rows without an adapter, empty batches and errors are lora_linear's;
- * LORA_EINVAL also for an fp32 pool, another act and misaligned pointers.
+ * LORA_EINVAL also for an fp32 pool, another act, misaligned pointers, and T,
+ * d_in or d_out over LORA_MX4_MAX_ROWS.
  *   workspace      dev, at least lora_workspace_bytes_mx4(pool, T, act) bytes
  *                  (0 for arguments without a result)
  */
@@ -490,8 +495,9 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  * H must be a multiple of 8, and I too for LORA_BF16; x, router and the
  * weights start on 16-byte, y on 8-byte boundaries; 1 <= E <= LORA_MOE_MAX_EXPERTS,
  * 1 <= k <= min(E, LORA_MOE_MAX_K) (lora_moe_experts: k may exceed E),
- * T k <= LORA_MOE_MAX_PAIRS. Asynchronous on `stream`. Errors: LORA_EINVAL,
- * LORA_ESPACE, LORA_EHIP. T == 0 launches nothing.
+ * T k <= LORA_MOE_MAX_PAIRS; H and I at most LORA_MX4_MAX_ROWS, one expert's
+ * matrix, x and the inner values under 2 GiB each. Asynchronous on `stream`.
+ * Errors: LORA_EINVAL, LORA_ESPACE, LORA_EHIP. T == 0 launches nothing.
  */
 #define LORA_MOE_MAX_EXPERTS 512
 #define LORA_MOE_MAX_K 16
@@ -513,9 +519,10 @@ int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* w
 /*
  * Per-kernel timing, for diagnostics and the benchmark's roofline figures.
  * Between lora_profile_begin and lora_profile_end, lora_linear,
- * lora_linear_multi, lora_shrink, lora_linear_mx4 and lora_moe_* record a HIP event pair around every
- * kernel they launch, on the stream it is launched on (not while that stream
- * is being captured into a graph, and at most max_records kernels).
+ * lora_linear_multi, lora_shrink, lora_mx4_quantize, lora_mx4_dequantize,
+ * lora_linear_mx4 and lora_moe_* record a HIP event pair around every kernel
+ * they launch, on the stream it is launched on (not while that stream is being
+ * captured into a graph, and at most max_records kernels).
  * lora_profile_end waits for the recorded events and writes one entry per
  * kernel name, in first-launch order, into out[0..cap): count, mean, min,
  * max and median duration; *n_out receives the number of names. Profiling

@@ -613,7 +613,9 @@ int lora_mx4_pack_scales(const void* e8m0, int batch, int rows, int K, void* sca
 }
 
 size_t lora_workspace_bytes_mx4(const lora_pool* p, int T, int act) {
-    if (!p || T < 0 || p->dtype != LORA_BF16 || (act != LORA_BF16 && act != LORA_MX4)) return 0;
+    if (!p || T < 0 || T > LORA_MX4_MAX_ROWS || p->d_out > LORA_MX4_MAX_ROWS || p->d_in > LORA_MX4_MAX_ROWS ||
+        p->dtype != LORA_BF16 || (act != LORA_BF16 && act != LORA_MX4))
+        return 0;
     return lora::mx4_linear_workspace(T, p->d_out, p->d_in, p->S, p->r_max, act == LORA_MX4);
 }
 
@@ -624,7 +626,7 @@ int lora_linear_mx4(const lora_pool* p, const void* x, const void* codes, const 
     if (rc != LORA_OK) return rc;
     if (p->dtype != LORA_BF16 || (act != LORA_BF16 && act != LORA_MX4)) return LORA_EINVAL;
     const int T = info->T;
-    if (T > LORA_MX4_MAX_ROWS || p->d_out > LORA_MX4_MAX_ROWS) return LORA_EINVAL;
+    if (T > LORA_MX4_MAX_ROWS || p->d_out > LORA_MX4_MAX_ROWS || p->d_in > LORA_MX4_MAX_ROWS) return LORA_EINVAL;
     if (T == 0) return LORA_OK;
     if (!x || !y || !mx4_buffers(codes, scales)) return LORA_EINVAL;
     if (y == x || y == codes || y == scales) return LORA_EINVAL;

@@ -644,8 +644,8 @@ static Mx4SplitPlan mx4_split_plan(int M, int N, int K, int S, bool act4) {
 struct Mx4Space {
     size_t xpad, apad, codes, scales, own, h, planes, total;
 };
-static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
-    const int Kp = (K + 7) / 8 * 8;
+static Mx4Space mx4_space(int M, int N, int d_in, int S, int r_max, bool act4) {
+    const int K = (d_in + 7) / 8 * 8;  // padded rows, which the path and its kernels see too
     Mx4Space s{};
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -653,8 +653,8 @@ static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
         o += (bytes + 255) & ~size_t(255);
         return at;
     };
-    s.xpad = take(K % 8 ? (size_t)M * Kp * 2 : 0);
-    s.apad = take(K % 8 ? (size_t)S * r_max * Kp * 2 : 0);
+    s.xpad = take(d_in % 8 ? (size_t)M * K * 2 : 0);
+    s.apad = take(d_in % 8 ? (size_t)S * r_max * K * 2 : 0);
     s.codes = take(act4 ? (size_t)M * mx4_row_bytes(K) : 0);
     s.scales = take(act4 ? (size_t)mx4_scale_bytes(M, K) : 0);
     switch (mx4_path(M, N, K, act4)) {
@@ -669,8 +669,8 @@ static Mx4Space mx4_space(int M, int N, int K, int S, int r_max, bool act4) {
             s.planes = take((size_t)8 * M * r_max * sizeof(float));
             break;
         case Mx4Path::kDequant:
-            s.own = take((size_t)N * Kp * 2);
-            s.h = take(gemm_bf16_workspace(M, &N, 1, Kp, r_max));
+            s.own = take((size_t)N * K * 2);
+            s.h = take(gemm_bf16_workspace(M, &N, 1, K, r_max));
             s.planes = take((size_t)8 * M * r_max * sizeof(float));
     }
     s.total = o;

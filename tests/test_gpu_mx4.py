@@ -336,3 +336,51 @@ def test_linear_refuses():
     f32 = lora.Pool(2, 4, 64, 32, "f32")
     assert lora.lib().lora_workspace_bytes_mx4(f32.handle, 8, lora.LORA_MX4) == 0
     assert lora.lib().lora_workspace_bytes_mx4(L.pool.handle, 8, 0) == 0
+
+
+def test_linear_refuses_sizes():
+    d_in = 4194248  # a row past what the scale tiles' grid takes
+    pool = lora.Pool(2, 1, d_in, 8, "bf16")
+    for act in ("bf16", "mx4"):
+        assert lora.lib().lora_workspace_bytes_mx4(pool.handle, 1, lora._ACT[act]) == 0
+        with pytest.raises(lora.LoraError):
+            lora.linear_mx4(torch.zeros(1, d_in, dtype=torch.bfloat16, device="cuda"), lora.Mx4.empty((8, d_in)), pool,
+                            lora.plan(np.zeros(1, np.int32), 2), act=act)
+
+
+@pytest.mark.parametrize("act", ["bf16", "mx4"])
+@pytest.mark.parametrize("T", [3, 40, 1500])
+def test_scales_on_an_8_byte_boundary(act, T):
+    L = Layer(T, 520, 1100, [0, 16, 8], seed=T)
+    clean = L.run(act)
+    n = L.W.scales.numel()
+    moved = torch.empty(n + 8, dtype=torch.uint8, device="cuda")[8:]
+    moved.copy_(L.W.scales)
+    assert moved.data_ptr() % 16 == 8
+    L.W = lora.Mx4(L.W.codes, moved, 520)
+    assert torch.equal(L.run(act), clean)
+
+
+@pytest.mark.parametrize("T", [20, 700])
+def test_two_graphs_with_a_workspace_each(T):
+    """Two captured calls, replayed in turn and after one another, with the
+    eager call between them."""
+    L = [Layer(T, 512, 768, [0, 16, 8], seed=s) for s in (3, 4)]
+    plans = [lora.plan(m.ids, m.S) for m in L]
+    ys = [torch.empty((T, 768), dtype=torch.bfloat16, device="cuda") for _ in L]
+    graphs = []
+    for m, p, y in zip(L, plans, ys):
+        lora.linear_mx4(m.x, m.W, m.pool, p, act="mx4", y=y)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            lora.linear_mx4(m.x, m.W, m.pool, p, act="mx4", y=y)
+    want = [lora.linear_mx4(m.x, m.W, m.pool, p, act="mx4") for m, p in zip(L, plans)]
+    for _ in range(3):
+        for y in ys:
+            y.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        assert torch.equal(lora.linear_mx4(L[0].x, L[0].W, L[0].pool, plans[0], act="mx4"), want[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(ys, want))

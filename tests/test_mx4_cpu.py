@@ -127,3 +127,12 @@ def test_binding_refuses_host_tensors():
         lora.mx4_dequantize(q)
     with pytest.raises(ValueError):
         lora.moe_route(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16), 2)
+
+
+@pytest.mark.parametrize("form,H,I", [(lora.LORA_BF16, 32768, 32768), (lora.LORA_MX4, 65536, 65536),
+                                      (lora.LORA_MX4, 4194248, 8), (lora.LORA_MX4, 8, 4194241)])
+def test_experts_refuses_sizes(form, H, I):
+    """One expert's matrix of 2 GiB, and a side past LORA_MX4_MAX_ROWS."""
+    d = lora.MoeWeightsDesc(*[P16] * 6)
+    assert lora.lib().lora_moe_experts(form, P16, P16, P16, ctypes.byref(d), 1, H, I, 2, 1, P16 + 4096, P16, 1 << 60,
+                                       None) == lora.LORA_EINVAL
