@@ -307,9 +307,11 @@ __device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>
                                                                  decltype(end)::value ? min(at, r.bytes) : at, 0));
         }
     };
-    // the last, partial tile apart (uniform): the checks on every tile take 1 us
-    // of 14 at 7 tokens of 2 of 8 experts, 2056 x 1000
-    if ((kt + 1) * TB > r.bytes) pieces(std::true_type{});
+    // 16-bit values: the last, partial tile apart (uniform); the checks on every
+    // tile take 1 us of gate_up's 14 at 7 tokens of 2 of 8 experts, 2056 x 1000.
+    // Codes have one scalar minimum a step: less than the branch (gate_up 51
+    // against 58 us at 32 tokens of 4 of 32 experts, 4096 x 1792)
+    if (MX || (kt + 1) * TB > r.bytes) pieces(std::true_type{});
     else pieces(std::false_type{});
 }
 
@@ -459,7 +461,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, cons
 // order, into o[pair][H] in fp32; every pair has one expert, so each element
 // is written once.
 template <bool MX, int NW>
-__global__ __launch_bounds__(64 * NW, 3) void moe_down_kernel(MoeArgs a, const MoePlan* __restrict__ pl,
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 3) void moe_down_kernel(MoeArgs a, const MoePlan* __restrict__ pl,
                                                               const uint16_t* __restrict__ act,
                                                               float* __restrict__ o) {
     __shared__ int lists[NW * kMoeWavePairs];
@@ -488,6 +490,21 @@ __global__ __launch_bounds__(64 * NW, 3) void moe_down_kernel(MoeArgs a, const M
         for (int kt = wave; kt < kts; kt += NW) {
             WTile<MX, 4> w;
             load_wtile(w, rd, kt, lane);
+            if constexpr (MX && NC == 1) {
+                // the inner values of both steps asked for with the codes, one
+                // round of memory: 34 against 38 us at 32 tokens of 4 of 32
+                // experts, 1792 -> 4096 (two column tiles of them would spill)
+                u32x4 x[2][1][2][kPieces<MX>];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    load_x<MX, true>(rx, ao[0], Ip, kt, i, lane, x[i][0][0]);
+                    load_x<MX, true>(rx, ao[0] + 2u * (uint32_t)Ir, Ip, kt, i, lane, x[i][0][1]);
+                }
+                issue_fence();
+                mac_wtile(acc, w, 0, 0, x[0]);
+                mac_wtile(acc, w, 0, 1, x[1]);
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kSteps<MX>; ++i) {
                 u32x4 x[NC][2][kPieces<MX>];
@@ -579,9 +596,11 @@ size_t moe_experts_workspace(int T, int H, int I, int k) {
 template <bool MX>
 static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
     // waves of a workgroup: gate_up 8 (128 registers, 2 workgroups a CU), down 4
-    // (168 registers, 3 a CU): at 32 tokens of 4 of 32 experts, 4096 x 1792,
-    // gate_up takes 54 us against 58 with 4, down 39 against 45 with 8
-    constexpr int NW = 8, ND = 4;
+    // (168 registers, 3 a CU) or, where that leaves a CU one workgroup at most,
+    // 8: at 32 tokens of 4 of 32 experts, 4096 x 1792, gate_up takes 54 us
+    // against 58 with 4, down 34 against 45 with 8; at one token 7 us with 8
+    // against 8
+    constexpr int NW = 8;
     const int P = a.T * a.k, reached = P < a.E ? P : a.E;  // experts at most
     char* ws = static_cast<char*>(a.workspace);
     uint16_t* act = reinterpret_cast<uint16_t*>(ws);
@@ -592,9 +611,11 @@ static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
     if (e == hipSuccess)
         e = launch(tm, "moe_gate_up", moe_gate_up_kernel<MX, NW>, dim3(moe_inner(a.I) / 32, reached), dim3(64 * NW), st,
                    a, (const MoePlan*)pl, act);
+    const dim3 down((a.H + 63) / 64, reached);
+    const bool few = down.x * down.y <= 256;
     if (e == hipSuccess)
-        e = launch(tm, "moe_down", moe_down_kernel<MX, ND>, dim3((a.H + 63) / 64, reached), dim3(64 * ND), st, a,
-                   (const MoePlan*)pl, (const uint16_t*)act, o);
+        e = launch(tm, "moe_down", few ? moe_down_kernel<MX, 8> : moe_down_kernel<MX, 4>, down, dim3(few ? 512 : 256), st,
+                   a, (const MoePlan*)pl, (const uint16_t*)act, o);
     if (e == hipSuccess)
         e = launch(tm, "moe_combine", moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.T), dim3(256), st, a,
                    (const float*)o);
