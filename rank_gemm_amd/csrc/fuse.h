@@ -379,13 +379,11 @@ __device__ __forceinline__ void stage_barrier() {
 // concatenated columns (its n_nt is recomputed per slice).
 hipError_t splitk_forward_bf16(const LinearArgs& L, const GemmPlan& g, hipStream_t st, StageTimer* tm);
 
-// The tiled path's shrink of one slice (into fp32 h [M][r_max] or, with ext,
-// the operand of the expand's extra K steps) and the workspace it needs at ws
-// (h or ext first, then its split planes), defined in gemm_bf16.hip.
+// Workspace of the tiled path's shrink of one slice: h or the expand operand
+// first, then its split planes.
 size_t tiled_workspace(int M, int r_max);
-hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext, hipStream_t st,
-                        StageTimer* tm);
 
+// The tiled GEMM of one slice whose expand operand is ready in ext.
 hipError_t tiled_forward_ready(const LinearArgs& L, const SliceArgs& s, uint16_t* ext, hipStream_t st,
                                StageTimer* tm);
 

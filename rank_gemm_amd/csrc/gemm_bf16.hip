@@ -200,8 +200,8 @@ static hipError_t launch_tile(const uint16_t* X, const uint16_t* W, uint16_t* Y,
 // The shrink of the tiled path, into fp32 h [M][r_max] or, with ext, the
 // expand operand of the extra K steps; ws: h_final bytes for h or ext, then
 // the K-split shrink's planes.
-hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext,
-                        hipStream_t st, StageTimer* tm) {
+static hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* ws, float* h, uint16_t* ext,
+                               hipStream_t st, StageTimer* tm) {
     const int M = L.M, K = L.K;
     // few items over a long K: split K over more workgroups, then add the splits
     int hs = 1, hkc = K;

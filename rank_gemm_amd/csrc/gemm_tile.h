@@ -143,7 +143,8 @@ struct SplitOut {
 template <int BM, int BN, int WM, int WN, int NS, bool EPI, bool KTAIL, bool SPLIT, bool BUF, bool F4>
 __device__ __forceinline__ void gemm_tile(const uint16_t* __restrict__ X, const uint16_t* __restrict__ W,
                                           uint16_t* __restrict__ Y, int M, int N, int K, int tiles_m, int tiles_n,
-                                          const Fuse& f, const SplitOut& so, const uint8_t* __restrict__ xscales = nullptr,
+                                          const Fuse& f, const SplitOut& so,
+                                          const uint8_t* __restrict__ xscales = nullptr,
                                           const uint8_t* __restrict__ wscales = nullptr) {
     static_assert(!(SPLIT && EPI), "a split runs no expand");
     static_assert(!(SPLIT && F4), "4-bit products run unsplit");

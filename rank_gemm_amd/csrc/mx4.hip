@@ -1,7 +1,10 @@
 // MXFP4 rows to and from values, and scale bytes in row order to the tiles
 // the products read (format: mx4_format.h). Memory-bound: each value is read and
 // each code written once; the arithmetic is a maximum over 32 values and the
-// hardware's scaled conversion.
+// hardware's scaled conversion. 14336 x 4096 bf16: 24.8 us to codes and 30.1 us
+// back, 6.0 and 4.9 TB/s of what each moves (149 MB; part of it stays in the
+// memory-side cache between calls), where a 1 GiB copy reaches 5.1 TB/s; 16 rows
+// are a launch (4 us with its event pair).
 #include "kernels.h"
 #include "mx4_tile.h"
 
@@ -14,7 +17,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__
     __shared__ uint8_t st[kMxTileBytes];
     const int64_t mat = blockIdx.z;
     quantize_tile<T, 256>(src + mat * rows * K, rows, K, nullptr, codes + mat * rows * mx4_row_bytes(K),
-                               scales + mat * mx4_scale_bytes(rows, K), blockIdx.x, blockIdx.y, st);
+                          scales + mat * mx4_scale_bytes(rows, K), blockIdx.x, blockIdx.y, st);
 }
 
 template <class T>
@@ -23,8 +26,8 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t* __re
                                                              int64_t K, T* __restrict__ dst) {
     __shared__ uint8_t st[kMxTileBytes];
     const int64_t mat = blockIdx.z;
-    dequantize_tile<T, 256>(codes + mat * rows * mx4_row_bytes(K), scales + mat * mx4_scale_bytes(rows, K), rows,
-                                 K, dst + mat * rows * K, blockIdx.x, blockIdx.y, st);
+    dequantize_tile<T, 256>(codes + mat * rows * mx4_row_bytes(K), scales + mat * mx4_scale_bytes(rows, K), rows, K,
+                            dst + mat * rows * K, blockIdx.x, blockIdx.y, st);
 }
 
 // scale bytes [rows][ceil(K / 32)] -> tiles; a thread writes one word
@@ -49,7 +52,8 @@ static dim3 mx4_grid(int64_t batch, int64_t rows, int64_t K) {
 template <class T>
 static hipError_t quantize(const void* src, int64_t batch, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
                            hipStream_t st, StageTimer* tm) {
-    return launch(tm, "mx4_quantize", mx4_quantize_kernel<T>, mx4_grid(batch, rows, K), dim3(256), st, (const T*)src, rows, K, codes, scales);
+    return launch(tm, "mx4_quantize", mx4_quantize_kernel<T>, mx4_grid(batch, rows, K), dim3(256), st,
+                  (const T*)src, rows, K, codes, scales);
 }
 
 hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows, int64_t K, uint8_t* codes,
@@ -61,7 +65,8 @@ hipError_t mx4_quantize(int dtype, const void* src, int64_t batch, int64_t rows,
 template <class T>
 static hipError_t dequantize(const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows, int64_t K,
                              void* dst, hipStream_t st, StageTimer* tm) {
-    return launch(tm, "mx4_dequantize", mx4_dequantize_kernel<T>, mx4_grid(batch, rows, K), dim3(256), st, codes, scales, rows, K, (T*)dst);
+    return launch(tm, "mx4_dequantize", mx4_dequantize_kernel<T>, mx4_grid(batch, rows, K), dim3(256), st, codes,
+                  scales, rows, K, (T*)dst);
 }
 
 hipError_t mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t batch, int64_t rows,

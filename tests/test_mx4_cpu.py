@@ -78,7 +78,8 @@ def test_linear_refuses_without_pool():
 @pytest.mark.parametrize("bad,want", [
     (dict(T=-1), -1), (dict(H=60), -1), (dict(H=0), -1), (dict(E=0), -1), (dict(E=513), -1), (dict(k=0), -1),
     (dict(k=17, E=64), -1), (dict(k=9), -1), (dict(T=257), -1), (dict(x=None), -1), (dict(x=P16 + 2), -1),
-    (dict(router=None), -1), (dict(ids=None), -1), (dict(weights=None), -1), (dict(H=8192, E=64, ws=None), -6), (dict(H=8192, E=64, wsb=10), -6)])
+    (dict(router=None), -1), (dict(ids=None), -1), (dict(weights=None), -1), (dict(H=8192, E=64, ws=None), -6),
+    (dict(H=8192, E=64, wsb=10), -6)])
 def test_route_refuses(bad, want):
     a = dict(x=P16, router=P16, T=4, H=64, E=8, k=2, renorm=1, ids=P16, weights=P16, ws=P16, wsb=1 << 20)
     a.update(bad)
