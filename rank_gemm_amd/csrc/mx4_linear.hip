@@ -179,13 +179,17 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
 // 32 (v % 4) .. + 31 over half v / 4 of every unit (two waves per SIMD: with
 // one, fragment reads, conversions and products wait on each other). A
 // unit's x goes to LDS by direct loads, once for the eight waves, while its
-// codes go to registers. In LDS a row of a unit is 32 chunks
-// of 16 bytes, chunk c of row r at slot c ^ (r % 16), through the source
-// address: the fragment reads of 16 rows then meet 16 distinct slots. 64 rows,
+// codes go to registers. In LDS a row of a unit is 32 chunks of 16 bytes, chunk
+// c of row r at slot c ^ ((r + 4) % 16), through the source address. A 16-byte
+// read by 64 lanes is served 16 lanes at a time, rows 0 - 3 and 12 - 15 of one
+// lane group with rows 4 - 11 of its neighbour, whose chunk differs in bit 2:
+// the two sets of slots are then disjoint (with c ^ (r % 16) they are equal,
+// and conflicts take 48% of the LDS cycles). 64 rows,
 // 4096 -> 14336: 15 us (the 64-column kernel 27), bound by what a CU takes in:
 // twice as many bytes of x as of W; 2, 3 or 4 units in flight, one wave per
 // SIMD or two, and a rotated order of units per tile take the same time.
 constexpr int kWideCols = 128;
+__device__ __forceinline__ int wide_swizzle(int row) { return (row + 4) & 15; }
 
 template <int I, int N>
 __device__ __forceinline__ void tie(u32x4 (&a)[N]) {
@@ -246,7 +250,7 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
     for (int d = 0; d < DMA; ++d) {
         const int r = 2 * (DMA * wave + d) + (lane >> 5), p = mt * 64 + r;
         const int tok = a.token_order[min(p, a.M - 1)];
-        const int k = ((lane & 31) ^ (r & 15)) * 8;
+        const int k = ((lane & 31) ^ wide_swizzle(r)) * 8;
         xk[d] = p < a.M ? k : a.K;  // rows past M: past the row's end, zeros
         xoff[d] = ((uint32_t)tok * (uint32_t)a.K + k) * 2u;
     }
@@ -279,7 +283,7 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
         const uint32_t row = lds_offset(lds + buf * UNIT) + fr * 512;
         u32x4 x[2][NT];
         auto read = [&](auto mc, u32x4 (&f)[NT]) {
-            const uint32_t at = row + (((half * 4 + fc) * 4 + decltype(mc)::value) ^ fr) * 16;
+            const uint32_t at = row + (((half * 4 + fc) * 4 + decltype(mc)::value) ^ wide_swizzle(fr)) * 16;
             f[0] = lds_read16<0>(at);
             f[1] = lds_read16<16 * 512>(at);
             if constexpr (NT > 2) {
