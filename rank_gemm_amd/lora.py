@@ -7,7 +7,9 @@ library must be built (``python -m rank_gemm_amd.build``) and there is no
 fallback of any kind: if it is missing, or no GPU is present, calls raise.
 
 Names follow the C ABI: ``Pool.install`` -> lora_pool_install, ``plan`` ->
-lora_plan, ``linear`` -> lora_linear, ``shrink`` -> lora_shrink.
+lora_plan, ``linear`` -> lora_linear, ``shrink`` -> lora_shrink,
+``mx4_quantize`` -> lora_mx4_quantize, ``linear_mx4`` -> lora_linear_mx4,
+``moe_route`` -> lora_moe_route, ``moe_experts`` -> lora_moe_experts.
 """
 from __future__ import annotations
 
