@@ -263,11 +263,14 @@ template <bool MX>
 constexpr int kPieces = MX ? 4 : 1;
 
 // RB 16-row blocks of one expert's matrix from row r0 on, read through buffer
-// resources: per-lane row offsets, the k of a tile in the uniform offset (at
-// most a row's bytes, so that it never passes the resource's). Codes past a
-// row's end are the next row's: any code under the zero scale bytes there is
-// finite, and they meet zeros of x. 16-bit values past a row's end are not
-// read: the next row's may be infinite.
+// resources: per-lane row offsets, the k of a tile in the uniform offset, which
+// is not checked against the resource's end. So a row that ends inside a tile
+// (TAIL, chosen on the host) has 4-bit codes addressed by the per-lane offset
+// alone: past a row's end they are the next row's, and zeros past the last one;
+// any code under the zero scale bytes there is finite, and meets zeros of x.
+// 16-bit values past a row's end are not read: the next row's may be infinite.
+// (Codes by the per-lane offset on every call: gate_up 59 against 51 us at 32
+// tokens of 4 of 32 experts, 4096 x 1792.)
 template <bool MX, int RB>
 struct WRows {
     brsrc data, scales;
@@ -295,7 +298,7 @@ struct WTile {
     u32x4 w[RB][kSteps<MX>];
     u32x2 sc;  // 4-bit: scale words of the tile's 64-row group
 };
-template <bool MX, int RB>
+template <bool TAIL, bool MX, int RB>
 __device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>& r, int kt, int lane) {
     constexpr int TB = kTileK<MX> * (MX ? 1 : 4) / 2;  // bytes of a row in a tile
     if constexpr (MX)
@@ -304,19 +307,19 @@ __device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>
 #pragma unroll
         for (int s = 0; s < kSteps<MX>; ++s) {
             const int at = kt * TB + s * 64;
-            const bool in = MX || !decltype(end)::value || at + (lane >> 4) * 16 < r.bytes;
 #pragma unroll
-            for (int j = 0; j < RB; ++j)
+            for (int j = 0; j < RB; ++j) {
+                uint32_t off = r.off[j];
+                if constexpr (decltype(end)::value)
+                    off = MX ? off + at : at + (lane >> 4) * 16 < r.bytes ? off + at : kOutOfRange;
                 t.w[j][s] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(r.data, in ? r.off[j] : kOutOfRange,
-                                                                 decltype(end)::value ? min(at, r.bytes) : at, 0));
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(r.data, off, decltype(end)::value ? 0 : at, 0));
+            }
         }
     };
     // 16-bit values: the last, partial tile apart (uniform); the checks on every
-    // tile take 1 us of gate_up's 14 at 7 tokens of 2 of 8 experts, 2056 x 1000.
-    // Codes have one scalar minimum a step: less than the branch (gate_up 51
-    // against 58 us at 32 tokens of 4 of 32 experts, 4096 x 1792)
-    if (MX || (kt + 1) * TB > r.bytes) pieces(std::true_type{});
+    // tile take 1 us of gate_up's 14 at 7 tokens of 2 of 8 experts, 2056 x 1000
+    if (TAIL && (MX || (kt + 1) * TB > r.bytes)) pieces(std::true_type{});
     else pieces(std::false_type{});
 }
 
@@ -388,7 +391,7 @@ __device__ __forceinline__ int moe_at(int i) {
 // down kernel, which waits on memory: the inner values keep 16 bits of
 // mantissa instead of 8) in act[pair][2][moe_act_row(I)]. A pass takes 16 or,
 // where more are left, 32 of the expert's pairs.
-template <bool MX, int NW>
+template <bool MX, bool TAIL, int NW>
 __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, const MoePlan* __restrict__ pl,
                                                                  uint16_t* __restrict__ act) {
     static_assert(NW == 8, "a thread per element of a row block pair");
@@ -416,8 +419,8 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, cons
             for (int j = 0; j < 2; ++j) g[c][j] = u[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kt = wave; kt < kts; kt += NW) {
             WTile<MX, 2> wg, wu;
-            load_wtile(wg, rg, kt, lane);
-            load_wtile(wu, ru, kt, lane);
+            load_wtile<TAIL>(wg, rg, kt, lane);
+            load_wtile<TAIL>(wu, ru, kt, lane);
 #pragma unroll
             for (int i = 0; i < kSteps<MX>; ++i) {
                 u32x4 x[NC][1][kPieces<MX>];
@@ -465,7 +468,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, cons
 // product of the expert's pairs, k tiles dealt round the waves, sums in wave
 // order, into o[pair][H] in fp32; every pair has one expert, so each element
 // is written once.
-template <bool MX, int NW>
+template <bool MX, bool TAIL, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 3) void moe_down_kernel(MoeArgs a, const MoePlan* __restrict__ pl,
                                                               const uint16_t* __restrict__ act,
                                                               float* __restrict__ o) {
@@ -494,7 +497,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 3) void moe_down_kernel(MoeA
             for (int j = 0; j < 4; ++j) acc[c][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kt = wave; kt < kts; kt += NW) {
             WTile<MX, 4> w;
-            load_wtile(w, rd, kt, lane);
+            load_wtile<TAIL>(w, rd, kt, lane);
             if constexpr (MX && NC == 1) {
                 // the inner values of both steps asked for with the codes, one
                 // round of memory: 34 against 38 us at 32 tokens of 4 of 32
@@ -613,14 +616,16 @@ static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
     MoePlan* pl = reinterpret_cast<MoePlan*>(ws + moe_act_bytes(a.T, a.I, a.k) + align256((size_t)P * a.H * sizeof(float)));
     hipError_t e = hipSuccess;
     if (P > kMoeWavePairs) e = launch(tm, "moe_plan", moe_plan_kernel, dim3(1), dim3(512), st, a.ids, P, a.E, pl);
+    const bool tail_h = a.H % kTileK<MX> != 0, tail_i = a.I % kTileK<MX> != 0;
     if (e == hipSuccess)
-        e = launch(tm, "moe_gate_up", moe_gate_up_kernel<MX, NW>, dim3(moe_inner(a.I) / 32, reached), dim3(64 * NW), st,
-                   a, (const MoePlan*)pl, act);
+        e = launch(tm, "moe_gate_up", tail_h ? moe_gate_up_kernel<MX, true, NW> : moe_gate_up_kernel<MX, false, NW>,
+                   dim3(moe_inner(a.I) / 32, reached), dim3(64 * NW), st, a, (const MoePlan*)pl, act);
     const dim3 down((a.H + 63) / 64, reached);
     const bool few = down.x * down.y <= 256;
+    auto ker = few ? (tail_i ? moe_down_kernel<MX, true, 8> : moe_down_kernel<MX, false, 8>)
+                   : (tail_i ? moe_down_kernel<MX, true, 4> : moe_down_kernel<MX, false, 4>);
     if (e == hipSuccess)
-        e = launch(tm, "moe_down", few ? moe_down_kernel<MX, 8> : moe_down_kernel<MX, 4>, down, dim3(few ? 512 : 256), st,
-                   a, (const MoePlan*)pl, (const uint16_t*)act, o);
+        e = launch(tm, "moe_down", ker, down, dim3(few ? 512 : 256), st, a, (const MoePlan*)pl, (const uint16_t*)act, o);
     if (e == hipSuccess)
         e = launch(tm, "moe_combine", moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.T), dim3(256), st, a,
                    (const float*)o);

@@ -208,7 +208,9 @@ __device__ __forceinline__ void reads_landed(u32x4 (&a)[N]) {
 // NS buffers: unit u + NS - 1 is loaded, into the buffer of unit u - 1, when
 // every wave has passed the barrier of unit u. Loads go through buffer
 // resources (x, the tile's code rows, its scales): codes past a row's end are
-// the next row's, or zeros at the end, and meet zeros of x.
+// the next row's, or zeros past the tile's last row, and meet zeros of x. Only
+// the per-lane offset is checked against a resource's end, so a unit's offset
+// in the code rows is part of it.
 template <int NT, int NS>
 __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
     constexpr int ROWS = 16 * NT, UNIT = ROWS * 32, DMA = ROWS / 2 / 8;  // chunks of a unit; x loads per wave
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
         s[buf] = __builtin_amdgcn_raw_buffer_load_b32(rS, soff, uc * kMxTileBytes, 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            w[buf][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rW, woff[j], uc * 128, 0));
+            w[buf][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rW, woff[j] + uc * 128, 0, 0));
 #pragma unroll
         for (int d = 0; d < DMA; ++d)
             bdma16(rX, k + xk[d] < a.K ? xoff[d] : kOutOfRange, (uint32_t)k * 2u, lds + buf * UNIT + (DMA * wave + d) * 64);
