@@ -604,13 +604,28 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
     if (r < rows && k < Kp) dst[r * Kp + k] = k < K ? src[r * K + k] : uint16_t(0);
 }
 
-// The path of a call, by its sizes and act alone (a base-only call takes the
-// same one).
+// The second kernel of the decode path: mx4_finish past kFinishBlocks blocks
+// where it takes the pool, else the bf16 path's.
+static bool finish_takes(int S, int r_max) { return S <= kFinishSlots && r_max <= kFinishRank && r_max % 8 == 0; }
+static bool finish_few(int M, int N) { return (int64_t)cdiv(N, 64) * cdiv(M, 16) <= kFinishBlocks; }
+
+// The path of a call, by its sizes, the pool's and act alone (a base-only call
+// takes the same one).
+// 16-bit activations: the wide kernel wherever the bf16 layer splits K, up to
+// 768 rows (decoding all of W costs more than it saves there: 320 x 14336 ->
+// 4096 71 against 97 us, 320 x 4096 -> 4096 25 against 38, 512 x 4096 -> 4096 35
+// against 37, 640 x 4096 -> 28672 198 against 268; 512 x 4096 -> 14336, 88
+// against 86, is the worst; from 1024 rows of 4096 columns on it loses, 58
+// against 48), and at most 128 of its tiles (1024 x 4096 -> 1024 25 against 33;
+// 192 tiles 38 against 33), unless a pool that mx4_finish does not take would
+// leave many blocks to the bf16 path's kernel 2.
 enum class Mx4Path { kSplit, kTile4, kDequant };
-static Mx4Path mx4_path(int M, int N, int K, bool act4) {
+static Mx4Path mx4_path(int M, int N, int K, int S, int r_max, bool act4) {
     if (act4) return M <= 64 || (int64_t)cdiv(M, 64) * cdiv(N, 64) <= 128 ? Mx4Path::kSplit : Mx4Path::kTile4;
-    return gemm_bf16_plan(M, N, K).nsub != 0 && (int64_t)M * K * 2 < int64_t(1) << 31 ? Mx4Path::kSplit
-                                                                                     : Mx4Path::kDequant;
+    const bool few = (M <= 768 || (int64_t)cdiv(M, 64) * cdiv(N, kWideCols) <= 128) &&
+                     (finish_takes(S, r_max) || finish_few(M, N));
+    return (few || gemm_bf16_plan(M, N, K).nsub != 0) && (int64_t)M * K * 2 < int64_t(1) << 31 ? Mx4Path::kSplit
+                                                                                              : Mx4Path::kDequant;
 }
 
 static bool mx4_wide(int M, bool act4) { return !act4 && M > 16; }
@@ -671,7 +686,7 @@ static Mx4Space mx4_space(int M, int N, int d_in, int S, int r_max, bool act4) {
     s.apad = take(d_in % 8 ? (size_t)S * r_max * K * 2 : 0);
     s.codes = take(act4 ? (size_t)M * mx4_row_bytes(K) : 0);
     s.scales = take(act4 ? (size_t)mx4_scale_bytes(M, K) : 0);
-    switch (mx4_path(M, N, K, act4)) {
+    switch (mx4_path(M, N, K, S, r_max, act4)) {
         case Mx4Path::kSplit: {
             const Mx4SplitPlan p = mx4_split_plan(M, N, K, S, act4);
             s.own = take((size_t)p.ks * p.n_mt * p.n_nt * 64 * 64 * sizeof(float));
@@ -750,7 +765,7 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
     pr.hkc = L.K;
     // the expand as extra K steps of a tiled product, where its form allows
     const bool ext_ok = L.r_max % 8 == 0 && L.S <= kMetaSlots;
-    switch (mx4_path(M, N, L.K, act4)) {
+    switch (mx4_path(M, N, L.K, L.S, L.r_max, act4)) {
         case Mx4Path::kSplit: {
             const Mx4SplitPlan p = mx4_split_plan(M, N, L.K, L.S, act4);
             Mx4Split a{L.X, pr.xc, pr.xs, codes, scales, reinterpret_cast<float*>(ws + sp.own), M, N, L.K, p.n_mt,
@@ -766,8 +781,7 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
             }
             e = launch_split(a, act4, st, tm);
             if (e != hipSuccess) return e;
-            if (L.S > kFinishSlots || L.r_max > kFinishRank || L.r_max % 8 != 0 ||
-                (int64_t)p.n_nt * cdiv(M, 16) <= kFinishBlocks)
+            if (!finish_takes(L.S, L.r_max) || finish_few(M, N))
                 return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
             const Mx4Finish fin{a.part, a.part_h, sl.Y, M, N, p.ks, p.n_mt, p.n_nt, p.hs, L.S, L.r_max, L.token_order,
                                 L.slot_indptr, sl.rank, sl.scale, sl.B_pool};

@@ -208,6 +208,11 @@ SHAPES = [
     (3601, 288, 3500, [0, 16, 8, 0, 64], None),
     (3600, 512, 3591, [0] + [16] * 16, None),
     (3400, 264, 3900, [0, 12, 4], None),
+    (768, 520, 1290, [0, 16, 8], None),
+    (769, 8200, 1500, [0, 16, 8], None),
+    (1030, 14336, 1100, [0, 16, 0, 8], None),
+    (1100, 520, 1300, [0, 16] * 40, None),
+    (1600, 72, 100, [0, 5, 16], None),
 ]
 
 
