@@ -359,9 +359,10 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
 // loads the rows' h and slot metadata again and holds 196 registers: it is
 // faster while its blocks fit the chip at once (two a CU; 4.0 against 5.4 us
 // at 64 x 4096) and falls behind past that (8.7 against 5.7 us at 64 x 14336,
-// 24 against 9.5 us at 256 x 14336).
-// ADAPT: pools of at most 64 slots (slot s on lane s) and ranks up to 32.
-constexpr int kFinishSlots = 64, kFinishRank = 32, kFinishBlocks = 512;
+// 24 against 9.5 us at 256 x 14336; rank 64 at 200 x 14336, 28 against 16 us).
+// NC: chunks of 32 ranks (0: no adapters), pools of at most 64 slots (slot s on
+// lane s). HALF: rows of B start on 8-byte boundaries (r_max % 8 == 4).
+constexpr int kFinishSlots = 64, kFinishRank = 64, kFinishBlocks = 512;
 
 struct Mx4Finish {
     const float* part;  // [ks][n_mt][n_nt][16 blocks][64 lanes] f32x4
@@ -373,8 +374,9 @@ struct Mx4Finish {
     const uint16_t* B_pool;
 };
 
-template <bool ADAPT>
+template <int NC, bool HALF>
 __global__ __launch_bounds__(256) void mx4_finish_kernel(Mx4Finish a) {
+    constexpr bool ADAPT = NC > 0;
     __shared__ u32x4 stg[4][16 * 9];  // a wave's 16 rows of 64 columns, 16 bytes of padding each
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nt = blockIdx.x, mt = blockIdx.y, p0 = mt * 64 + wave * 16, n0 = nt * 64;
@@ -391,23 +393,27 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(Mx4Finish a) {
     int tok[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) tok[i] = a.token_order[min(p0 + 8 * i + (lane >> 3), a.M - 1)];
-    u32x4 hi{0, 0, 0, 0}, lo{0, 0, 0, 0};
-    int slot = 0, r = 0;  // of row p0 + fr
-    uint64_t slots = 0;   // the block's slots
+    u32x4 hi[ADAPT ? NC : 1], lo[ADAPT ? NC : 1];
+    int slot = 0;        // of row p0 + fr
+    uint64_t slots = 0;  // the block's slots
     if constexpr (ADAPT) {
         const int ip = a.slot_indptr[min(lane, a.S)];
         const int rk = a.rank[min(lane, a.S - 1)];
         const float sv = a.scale[min(lane, a.S - 1)];
-        // lane (fr, fc): ranks 8 fc .. + 7 of row fr, every plane loaded
+        // lane (fr, fc): ranks 32 c + 8 fc .. + 7 of row fr, every plane loaded
         f32x4 hv[8][2];
         const float* hp = a.h + (int64_t)min(p0 + fr, a.M - 1) * a.r_max + 8 * fc;
+        auto load_h = [&](int c) {
 #pragma unroll
-        for (int z = 0; z < 8; ++z) {
-            const bool ok = z < a.hs && 8 * fc < a.r_max;
-            const float* q = hp + (int64_t)z * a.M * a.r_max;
-            hv[z][0] = __builtin_bit_cast(f32x4, *or_zero(ok, q));
-            hv[z][1] = __builtin_bit_cast(f32x4, *or_zero(ok, q + 4));
-        }
+            for (int z = 0; z < 8; ++z) {
+                const float* q = hp + (int64_t)z * a.M * a.r_max + 32 * c;
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    hv[z][g] = __builtin_bit_cast(
+                        f32x4, *or_zero(z < a.hs && 32 * c + 8 * fc + 4 * g < a.r_max, q + 4 * g));
+            }
+        };
+        load_h(0);
         issue_fence();
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -417,23 +423,27 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(Mx4Finish a) {
             if (p0 + j < a.M) slots |= 1ull << s;
         }
         slots &= ~1ull;
-        r = __shfl(rk, slot);  // by every lane: slot s is on lane s
+        int r = __shfl(rk, slot);  // by every lane: slot s is on lane s
         r = slot == 0 ? 0 : r;
         const float sc = __shfl(sv, slot);
-        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float x = 0.f;
+        for (int c = 0; c < NC; ++c) {
+            if (c > 0) load_h(c);
+            float v[8];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) x += hv[z][e >> 2][e & 3];
-            // past the rank the planes hold nothing
-            v[e] = 8 * fc + e < r ? x * sc : 0.f;
-        }
+            for (int e = 0; e < 8; ++e) {
+                float x = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            hi[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-            lo[e] = pack_bf16x2(v[2 * e] - __uint_as_float(hi[e] << 16),
-                                v[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                for (int z = 0; z < 8; ++z) x += hv[z][e >> 2][e & 3];
+                // past the rank the planes hold nothing
+                v[e] = 32 * c + 8 * fc + e < r ? x * sc : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                hi[c][e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                lo[c][e] = pack_bf16x2(v[2 * e] - __uint_as_float(hi[c][e] << 16),
+                                       v[2 * e + 1] - __uint_as_float(hi[c][e] & 0xffff0000u));
+            }
         }
     }
 #pragma unroll
@@ -453,34 +463,46 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(Mx4Finish a) {
         // two slots at a time: their B rows (lane (fr, fc): column fr of a
         // block, ranks 8 fc ..) loaded together
         while (slots) {
-            u32x4 b[2][4];
-            int s[2];
+            int s[2], rs[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 s[i] = slots ? (int)__builtin_ctzll(slots) : 0;
                 slots &= slots - 1;
-                const int rs = s[i] ? a.rank[s[i]] : 0;  // uniform
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int n = n0 + 16 * j + fr;
-                    b[i][j] = *or_zero(n < a.N && 8 * fc < rs,
-                                       a.B_pool + ((int64_t)s[i] * a.N + n) * a.r_max + 8 * fc);
-                }
+                rs[i] = s[i] ? a.rank[s[i]] : 0;  // uniform
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool on = slot == s[i];
-                u32x4 h1, h2;
+            for (int c = 0; c < NC; ++c) {
+                if (c > 0 && max(rs[0], rs[1]) <= 32 * c) break;  // uniform
+                u32x4 b[2][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    h1[e] = on ? hi[e] : 0u;
-                    h2[e] = on ? lo[e] : 0u;
-                }
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 d = mfma16x16x32(h2, b[i][j], mfma16x16x32(h1, b[i][j], f32x4{0.f, 0.f, 0.f, 0.f}));
+                    for (int j = 0; j < 4; ++j) {
+                        const int n = n0 + 16 * j + fr, q = 32 * c + 8 * fc;
+                        const uint16_t* row = a.B_pool + ((int64_t)s[i] * a.N + n) * a.r_max + q;
+                        if constexpr (HALF) {
+                            const u32x2 b0 = *(gptr<u32x2>)or_zero(n < a.N && q < rs[i], row);
+                            const u32x2 b1 = *(gptr<u32x2>)or_zero(n < a.N && q + 4 < rs[i], row + 4);
+                            b[i][j] = u32x4{b0[0], b0[1], b1[0], b1[1]};
+                        } else {
+                            b[i][j] = *or_zero(n < a.N && q < rs[i], row);
+                        }
+                    }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+                for (int i = 0; i < 2; ++i) {
+                    const bool on = slot == s[i];
+                    u32x4 h1, h2;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h1[e] = on ? hi[c][e] : 0u;
+                        h2[e] = on ? lo[c][e] : 0u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4 d = mfma16x16x32(h2, b[i][j], mfma16x16x32(h1, b[i][j], f32x4{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][e] += d[e];
+                    }
                 }
             }
         }
@@ -606,7 +628,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
 
 // The second kernel of the decode path: mx4_finish past kFinishBlocks blocks
 // where it takes the pool, else the bf16 path's.
-static bool finish_takes(int S, int r_max) { return S <= kFinishSlots && r_max <= kFinishRank && r_max % 8 == 0; }
+static bool finish_takes(int S, int r_max) { return S <= kFinishSlots && r_max <= kFinishRank && r_max % 4 == 0; }
 static bool finish_few(int M, int N) { return (int64_t)cdiv(N, 64) * cdiv(M, 16) <= kFinishBlocks; }
 
 // The path of a call, by its sizes, the pool's and act alone (a base-only call
@@ -785,8 +807,11 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
                 return splitk_finish_bf16(L, sl, a.part, p.ks, p.n_mt, a.part_h, p.hs, st, tm);
             const Mx4Finish fin{a.part, a.part_h, sl.Y, M, N, p.ks, p.n_mt, p.n_nt, p.hs, L.S, L.r_max, L.token_order,
                                 L.slot_indptr, sl.rank, sl.scale, sl.B_pool};
-            return launch(tm, "mx4_finish", L.adapters ? mx4_finish_kernel<true> : mx4_finish_kernel<false>,
-                          dim3(p.n_nt, p.n_mt), dim3(256), st, fin);
+            const bool half = L.r_max % 8 != 0;
+            auto ker = !L.adapters     ? mx4_finish_kernel<0, false>
+                       : L.r_max <= 32 ? (half ? mx4_finish_kernel<1, true> : mx4_finish_kernel<1, false>)
+                                       : (half ? mx4_finish_kernel<2, true> : mx4_finish_kernel<2, false>);
+            return launch(tm, "mx4_finish", ker, dim3(p.n_nt, p.n_mt), dim3(256), st, fin);
         }
         case Mx4Path::kTile4: {
             float* h = reinterpret_cast<float*>(ws + sp.own);
