@@ -626,6 +626,34 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restric
     if (r < rows && k < Kp) dst[r * Kp + k] = k < K ? src[r * K + k] : uint16_t(0);
 }
 
+// B's rows of r_max values (not a multiple of 8) -> rows of rp, zeros behind:
+// the tiles' extra steps read them in 16-byte pieces. A thread writes a piece.
+__global__ __launch_bounds__(256) void pad_ranks_kernel(const uint16_t* __restrict__ src, int64_t rows, int r_max,
+                                                        int rp, u32x4* __restrict__ dst) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / (rp / 8);
+    if (row >= rows) return;
+    const int q = (int)(i - row * (rp / 8)) * 8;
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = q + e < r_max ? src[row * r_max + q + e] : 0u;
+    dst[i] = u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+}
+
+// Whether a tiled product pads the pool's B for its extra K steps, rather than
+// run the expand in the epilogue of 128 x 128 tiles. The copy (4 to 5 us) moves S
+// rp values a column, so it needs rows in proportion; with 4-bit x, where all
+// else stays, also a large output: rank 12, 16 adapters, 2048 x 4096 -> 14336 92
+// against 123 us, 600 x 4096 -> 14336 57 against 62, 2048 x 4096 -> 4096 43
+// against 47, but 600 x 4096 -> 4096 33 against 30. With 16-bit x it also brings
+// the shrink into the launch before: 2048 x 4096 -> 4096 78 against 82, 2048 x
+// 1024 -> 2048 27 against 33.
+static bool tile_pads(int M, int N, int S, int r_max, bool act4) {
+    const int rp = (r_max + 7) & ~7;
+    return r_max % 8 != 0 && S <= kMetaSlots && (int64_t)M >= (int64_t)2 * S * rp &&
+           (!act4 || (int64_t)M * N >= int64_t(1) << 23);
+}
+
 // The second kernel of the decode path: mx4_finish past kFinishBlocks blocks
 // where it takes the pool, else the bf16 path's.
 static bool finish_takes(int S, int r_max) { return S <= kFinishSlots && r_max <= kFinishRank && r_max % 4 == 0; }
@@ -693,7 +721,7 @@ static Mx4SplitPlan mx4_split_plan(int M, int N, int K, int S, bool act4) {
 // activations, then the path's own (partials and h planes; h or the expand
 // operand; W in bf16 and the bf16 layer's workspace).
 struct Mx4Space {
-    size_t xpad, apad, codes, scales, own, h, planes, total;
+    size_t xpad, apad, bpad, codes, scales, own, h, planes, total;
 };
 static Mx4Space mx4_space(int M, int N, int d_in, int S, int r_max, bool act4) {
     const int K = (d_in + 7) / 8 * 8;  // padded rows, which the path and its kernels see too
@@ -706,6 +734,8 @@ static Mx4Space mx4_space(int M, int N, int d_in, int S, int r_max, bool act4) {
     };
     s.xpad = take(d_in % 8 ? (size_t)M * K * 2 : 0);
     s.apad = take(d_in % 8 ? (size_t)S * r_max * K * 2 : 0);
+    const bool pads = mx4_path(M, N, K, S, r_max, act4) != Mx4Path::kSplit && tile_pads(M, N, S, r_max, act4);
+    s.bpad = take(pads ? (size_t)S * N * ((r_max + 7) & ~7) * 2 : 0);
     s.codes = take(act4 ? (size_t)M * mx4_row_bytes(K) : 0);
     s.scales = take(act4 ? (size_t)mx4_scale_bytes(M, K) : 0);
     switch (mx4_path(M, N, K, S, r_max, act4)) {
@@ -786,7 +816,19 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
     pr.hs = 1;
     pr.hkc = L.K;
     // the expand as extra K steps of a tiled product, where its form allows
-    const bool ext_ok = L.r_max % 8 == 0 && L.S <= kMetaSlots;
+    const bool pads = tile_pads(M, N, L.S, L.r_max, act4), ext_ok = pads || (L.r_max % 8 == 0 && L.S <= kMetaSlots);
+    auto pad_ranks = [&] {  // after it L describes a pool of padded ranks (pr's A is the pool's)
+        const int rp = (L.r_max + 7) & ~7;
+        const int64_t rows = (int64_t)L.S * N;
+        u32x4* bp = reinterpret_cast<u32x4*>(ws + sp.bpad);
+        const hipError_t pe = !L.adapters ? hipSuccess
+                                          : launch(tm, "pad_ranks", pad_ranks_kernel,
+                                                   dim3((uint32_t)((rows * (rp / 8) + 255) / 256)), dim3(256), st,
+                                                   sl.B_pool, rows, L.r_max, rp, bp);
+        sl.B_pool = reinterpret_cast<const uint16_t*>(bp);
+        L.r_max = rp;
+        return pe;
+    };
     switch (mx4_path(M, N, L.K, L.S, L.r_max, act4)) {
         case Mx4Path::kSplit: {
             const Mx4SplitPlan p = mx4_split_plan(M, N, L.K, L.S, act4);
@@ -815,6 +857,8 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
         }
         case Mx4Path::kTile4: {
             float* h = reinterpret_cast<float*>(ws + sp.own);
+            if (pads) e = pad_ranks();
+            if (e != hipSuccess) return e;
             Fuse f{L.token_order, L.slot_indptr, h, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
                    nullptr, (L.r_max + 7) & ~7};
             pr.h = h;
@@ -840,6 +884,8 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
     L.workspace = ws + sp.h;
     const bool beside = ext_ok && gemm_bf16_plan(M, N, L.K).tks < 2;
     if (beside) {
+        if (pads) e = pad_ranks();
+        if (e != hipSuccess) return e;
         pr.ext = reinterpret_cast<uint16_t*>(ws + sp.h);
         pr.h = reinterpret_cast<float*>(ws + sp.planes);
         pr.hs = prep_ranges(L.K, pr.n_items);

@@ -213,6 +213,7 @@ SHAPES = [
     (1030, 14336, 1100, [0, 16, 0, 8], None),
     (1100, 520, 1300, [0, 16] * 40, None),
     (1600, 72, 100, [0, 5, 16], None),
+    (4000, 264, 2104, [0, 12, 4, 0, 9], 13),
     (600, 264, 4100, [0, 12, 4, 0, 9], 12),
     (260, 520, 8200, [0, 64, 40, 4, 33], 64),
     (300, 4104, 4096, [0, 44, 20, 3] * 15, 44),
