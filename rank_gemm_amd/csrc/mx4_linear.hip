@@ -617,13 +617,36 @@ static hipError_t launch_prep(const Mx4Prep& a, hipStream_t st, StageTimer* tm) 
     return launch(tm, "mx4_operand", mx4_operand_kernel, dim3(a.n_items), dim3(256), st, a);
 }
 
-// rows of any width -> rows of Kp elements (a multiple of 8), zeros behind
-// the row's end: the kernels read rows in 16-byte pieces
-__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t* __restrict__ src, int64_t rows, int K, int Kp,
-                                                       uint16_t* __restrict__ dst) {
-    const int64_t r = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    if (r < rows && k < Kp) dst[r * Kp + k] = k < K ? src[r * K + k] : uint16_t(0);
+// Rows of any width (x, and with adapters the pool's A up to each slot's rank)
+// -> rows of Kp elements, a multiple of 8, zeros behind the row's end: the
+// kernels read rows in 16-byte pieces. One launch for both; a wave takes 64
+// pieces of a row, loaded off 16-byte boundaries.
+struct Mx4Pad {
+    const uint16_t *x, *A;
+    uint16_t *xp, *Ap;
+    int64_t M, rows;  // rows: M + S r_max
+    int K, Kp, r_max;
+    const int32_t* rank;
+};
+__global__ __launch_bounds__(256) void pad_rows_kernel(Mx4Pad a) {
+    const int64_t r = (blockIdx.y + (int64_t)blockIdx.z * gridDim.y) * 4 + (threadIdx.x >> 6);
+    const int k = (blockIdx.x * 64 + (threadIdx.x & 63)) * 8;
+    if (r >= a.rows || k >= a.Kp) return;
+    const int64_t q = r - a.M;  // row of A
+    if (q >= 0 && (int)(q % a.r_max) >= a.rank[q / a.r_max]) return;
+    const uint16_t* src = (q < 0 ? a.x + r * a.K : a.A + q * a.K) + k;
+    uint16_t* dst = (q < 0 ? a.xp + r * a.Kp : a.Ap + q * a.Kp) + k;
+    u32x4 v{0, 0, 0, 0};
+    if (k + 8 <= a.K) {
+        Raw8<uint16_t> p;
+        p.load(src);
+        v = p.v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < a.K) v[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+    }
+    *reinterpret_cast<u32x4*>(dst) = v;
 }
 
 // B's rows of r_max values (not a multiple of 8) -> rows of rp, zeros behind:
@@ -762,11 +785,11 @@ size_t mx4_linear_workspace(int M, int N, int K, int S, int r_max, bool act4) {
     return M > 0 ? mx4_space(M, N, K, S, r_max, act4).total : 0;
 }
 
-static hipError_t pad_rows(const uint16_t* src, int64_t rows, int K, int Kp, uint16_t* dst, hipStream_t st,
-                           StageTimer* tm) {
-    const uint32_t gy = (uint32_t)(rows < 65535 ? rows : 65535);
-    return launch(tm, "pad_rows", pad_rows_kernel, dim3((Kp + 255) / 256, gy, (uint32_t)((rows + gy - 1) / gy)),
-                  dim3(256), st, src, rows, K, Kp, dst);
+static hipError_t pad_rows(const Mx4Pad& a, hipStream_t st, StageTimer* tm) {
+    const int64_t blocks = (a.rows + 3) / 4;
+    const uint32_t gy = (uint32_t)(blocks < 65535 ? blocks : 65535);
+    return launch(tm, "pad_rows", pad_rows_kernel, dim3((a.Kp + 511) / 512, gy, (uint32_t)((blocks + gy - 1) / gy)),
+                  dim3(256), st, a);
 }
 
 static hipError_t launch_split(const Mx4Split& a, bool act4, hipStream_t st, StageTimer* tm) {
@@ -798,8 +821,9 @@ hipError_t mx4_linear(const LinearArgs& L0, const uint8_t* codes, const uint8_t*
         const int Kp = (L.K + 7) / 8 * 8;
         uint16_t* xp = reinterpret_cast<uint16_t*>(ws + sp.xpad);
         uint16_t* ap = reinterpret_cast<uint16_t*>(ws + sp.apad);
-        e = pad_rows(L.X, M, L.K, Kp, xp, st, tm);
-        if (e == hipSuccess && L.adapters) e = pad_rows(sl.A_pool, (int64_t)L.S * L.r_max, L.K, Kp, ap, st, tm);
+        const Mx4Pad pad{L.X, sl.A_pool, xp, ap, M, M + (L.adapters ? (int64_t)L.S * L.r_max : 0), L.K, Kp, L.r_max,
+                         sl.rank};
+        e = pad_rows(pad, st, tm);
         if (e != hipSuccess) return e;
         L.X = xp;
         sl.A_pool = ap;
