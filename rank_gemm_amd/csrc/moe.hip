@@ -613,7 +613,7 @@ static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
     char* ws = static_cast<char*>(a.workspace);
     uint16_t* act = reinterpret_cast<uint16_t*>(ws);
     float* o = reinterpret_cast<float*>(ws + moe_act_bytes(a.T, a.I, a.k));
-    MoePlan* pl = reinterpret_cast<MoePlan*>(ws + moe_act_bytes(a.T, a.I, a.k) + align256((size_t)P * a.H * sizeof(float)));
+    MoePlan* pl = reinterpret_cast<MoePlan*>(reinterpret_cast<char*>(o) + align256((size_t)P * a.H * sizeof(float)));
     hipError_t e = hipSuccess;
     if (P > kMoeWavePairs) e = launch(tm, "moe_plan", moe_plan_kernel, dim3(1), dim3(512), st, a.ids, P, a.E, pl);
     const bool tail_h = a.H % kTileK<MX> != 0, tail_i = a.I % kTileK<MX> != 0;
@@ -625,7 +625,8 @@ static hipError_t experts(const MoeArgs& a, hipStream_t st, StageTimer* tm) {
     auto ker = few ? (tail_i ? moe_down_kernel<MX, true, 8> : moe_down_kernel<MX, false, 8>)
                    : (tail_i ? moe_down_kernel<MX, true, 4> : moe_down_kernel<MX, false, 4>);
     if (e == hipSuccess)
-        e = launch(tm, "moe_down", ker, down, dim3(few ? 512 : 256), st, a, (const MoePlan*)pl, (const uint16_t*)act, o);
+        e = launch(tm, "moe_down", ker, down, dim3(few ? 512 : 256), st, a, (const MoePlan*)pl, (const uint16_t*)act,
+                   o);
     if (e == hipSuccess)
         e = launch(tm, "moe_combine", moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.T), dim3(256), st, a,
                    (const float*)o);

@@ -33,9 +33,10 @@ __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa
 // in extra workgroups of the same launch, over K ranges of its own.
 // One row, 4096 -> 4096: 4.8 us with its event pair for 9 MB, two dependent
 // rounds of memory (token order, then the units) and a launch; 48 rows of 4-bit
-// x: 5.8 us. W is loaded without the non-temporal hint: with 24 layers of 4096
-// -> 14336 in turn (744 MB, more than the caches hold) 64 rows take 25.3 us
-// against 27.4 with it, and 22.7 against 26.4 while W stays cached.
+// x: 5.8 us. W is loaded without the non-temporal hint, here and below: with 24
+// layers of 4096 -> 14336 in turn (744 MB, more than the caches hold) a call of
+// 64 rows takes 22.8 us against 24.3 with it, and 20.0 against 23.4 while W
+// stays cached.
 struct Mx4Split {
     const uint16_t* X;
     const uint8_t *xc, *xs;  // 4-bit activations, in plan order
@@ -269,7 +270,8 @@ __global__ __launch_bounds__(512) void mx4_wide_kernel(Mx4Split a) {
             w[buf][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rW, woff[j] + uc * 128, 0, 0));
 #pragma unroll
         for (int d = 0; d < DMA; ++d)
-            bdma16(rX, k + xk[d] < a.K ? xoff[d] : kOutOfRange, (uint32_t)k * 2u, lds + buf * UNIT + (DMA * wave + d) * 64);
+            bdma16(rX, k + xk[d] < a.K ? xoff[d] : kOutOfRange, (uint32_t)k * 2u,
+                   lds + buf * UNIT + (DMA * wave + d) * 64);
         issue_fence();
     };
     f32x4 acc[NT][2];
@@ -796,8 +798,10 @@ static hipError_t launch_split(const Mx4Split& a, bool act4, hipStream_t st, Sta
     if (mx4_wide(a.M, act4))
         return launch(tm, "mx4_wide", a.M <= 32 ? mx4_wide_kernel<2, 3> : mx4_wide_kernel<4, 3>,
                       dim3(a.n_items * a.hs + a.n_mt * cdiv(a.N, kWideCols) * a.ks), dim3(512), st, a);
-    auto ker = !act4 ? mx4_split_kernel<false, 1>
-               : a.M <= 16 ? mx4_split_kernel<true, 1> : a.M <= 32 ? mx4_split_kernel<true, 2> : mx4_split_kernel<true, 4>;
+    auto ker = !act4       ? mx4_split_kernel<false, 1>
+               : a.M <= 16 ? mx4_split_kernel<true, 1>
+               : a.M <= 32 ? mx4_split_kernel<true, 2>
+                           : mx4_split_kernel<true, 4>;
     return launch(tm, "mx4_split", ker, dim3(a.n_items * a.hs + a.n_mt * a.n_nt * a.ks), dim3(256), st, a);
 }
 
