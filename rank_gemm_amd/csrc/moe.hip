@@ -312,8 +312,8 @@ __device__ __forceinline__ void load_wtile(WTile<MX, RB>& t, const WRows<MX, RB>
                 uint32_t off = r.off[j];
                 if constexpr (decltype(end)::value)
                     off = MX ? off + at : at + (lane >> 4) * 16 < r.bytes ? off + at : kOutOfRange;
-                // the minimum never takes effect; with it the compiler keeps the
-                // steps' offsets apart (gate_up 51.5 against 54.6 us, as above)
+                // the minimum never takes effect; without it register reuse puts a
+                // wait between a tile's loads (gate_up 54.6 against 51.5 us, as above)
                 t.w[j][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                           r.data, off, decltype(end)::value ? 0 : min(at, r.bytes), 0));
             }
