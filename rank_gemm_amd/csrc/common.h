@@ -54,6 +54,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// The value whose bf16 rounding is the hi half of v = hi + lo, two halves that
+// keep 16 bits of its mantissa: v, up to the largest finite bf16. A finite v
+// past that would round to infinity and leave -inf as its remainder, whose
+// products add up to NaN; here hi stays finite and lo holds the rest, also
+// where the rest is infinite (or NaN).
+__device__ __forceinline__ float hi_half(float v) {
+    constexpr float kMax = 0x1.fep127f;
+    return __builtin_amdgcn_fmed3f(v, -kMax, kMax);
+}
+
 // 16x16x32 bf16 matrix-core product: lane l supplies row (l % 16) of the
 // left operand and column (l % 16) of the right one, 8 consecutive k each
 // (k = 8 * (l / 16) + e); lane l receives rows 4 * (l / 16) + i, column l % 16.

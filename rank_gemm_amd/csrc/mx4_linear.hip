@@ -442,7 +442,7 @@ __global__ __launch_bounds__(256) void mx4_finish_kernel(Mx4Finish a) {
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                hi[c][e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                hi[c][e] = pack_bf16x2(hi_half(v[2 * e]), hi_half(v[2 * e + 1]));
                 lo[c][e] = pack_bf16x2(v[2 * e] - __uint_as_float(hi[c][e] << 16),
                                        v[2 * e + 1] - __uint_as_float(hi[c][e] & 0xffff0000u));
             }
@@ -592,7 +592,7 @@ __global__ __launch_bounds__(256) void mx4_operand_kernel(Mx4Prep a) {
         if (q < r)
             for (int z = 0; z < a.hs; ++z) v += a.h[((int64_t)z * a.M + p) * a.r_max + q];
         v *= sc;
-        const uint16_t hi = f32_to_bf16(v);
+        const uint16_t hi = f32_to_bf16(hi_half(v));
         a.ext[(p * 2) * rp + q] = hi;
         a.ext[(p * 2 + 1) * rp + q] = f32_to_bf16(v - bf16_to_f32(hi));
     }

@@ -593,16 +593,19 @@ __global__ __launch_bounds__(kThreads) void splitk_epilogue_kernel(const float* 
                     const float* hr = hs + (lane & 15) * r_max + (q0 < r_max ? q0 : 0);
                     const f32x4 h0 = reinterpret_cast<const f32x4*>(hr)[0];
                     const f32x4 h1 = reinterpret_cast<const f32x4*>(hr)[1];
-                    float v[8], lo[8];
+                    float v[8], hi[8], lo[8];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         v[t] = mine && q0 + t < r_row ? sc_row * h0[t] : 0.f;
                         v[4 + t] = mine && q0 + 4 + t < r_row ? sc_row * h1[t] : 0.f;
                     }
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) lo[t] = v[t] - bf16_to_f32(f32_to_bf16(v[t]));
-                    const u32x4 ahi{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                    pack_bf16x2(v[6], v[7])};
+                    for (int t = 0; t < 8; ++t) {
+                        hi[t] = hi_half(v[t]);
+                        lo[t] = v[t] - bf16_to_f32(f32_to_bf16(hi[t]));
+                    }
+                    const u32x4 ahi{pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3]), pack_bf16x2(hi[4], hi[5]),
+                                    pack_bf16x2(hi[6], hi[7])};
                     const u32x4 alo{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(lo[4], lo[5]),
                                     pack_bf16x2(lo[6], lo[7])};
                     dm = mfma16x16x32(ahi, bf[k][c], dm);

@@ -307,3 +307,25 @@ def test_block_with_adapters():
     delta, lost = mx4_ref.linear(h64, np.zeros((H, H)), ids, A[1], B[1], [16.0] * S)
     ref = as64(moe) + delta
     assert (np.abs(as64(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 1.01 * lost).all()
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx4"])
+def test_inner_value_past_the_largest_bf16(form):
+    """An inner value of 2^128 - 2^114 (finite in fp32, over every finite bf16)
+    times 2^-100 rounds to 2^28; a weight of 0 gives 0."""
+    H = I = 8
+    x = torch.zeros((1, H), dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[0, 1], x[0, 2] = 1.0, 2.0 ** -7, 2.0 ** -6
+    gate, up, down = (torch.zeros(s, device="cuda") for s in ((1, I, H), (1, I, H), (1, H, I)))
+    gate[0, 0, 0] = gate[0, 0, 1] = 2.0 ** 7                       # 2^7 (1 + 2^-7)
+    up[0, 0, 0], up[0, 0, 2] = 2.0 ** 121, -(2.0 ** 120)           # 2^120 (2 - 2^-6)
+    down[0, :4, 0] = 2.0 ** -100
+    down[0, 4, 0] = -(2.0 ** -100)
+    if form == "mx4":
+        w = [lora.mx4_quantize(t) for t in (gate, up, down)]
+        assert all(torch.equal(lora.mx4_dequantize(q, "f32"), t) for q, t in zip(w, (gate, up, down)))
+    else:
+        w = [t.to(torch.bfloat16) for t in (gate, up, down)]
+    ids, one = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones((1, 1), device="cuda")
+    y = lora.moe_experts(x, ids, one, *w)
+    assert y[0].tolist() == [2.0 ** 28] * 4 + [-(2.0 ** 28)] + [0.0] * 3
