@@ -24,7 +24,9 @@ namespace lora {
 // ------------------------------------------------------------------ route --
 // A lane's parts of the 64-bit dot products of one bf16 row with NE others
 // (rows of `stride` elements), in the order of k; CH pieces of every row in
-// flight at once.
+// flight at once. A product of two bf16 is exact in 64 bits; in fp32 it could
+// leave the range (and is no faster but for large calls: 64 tokens x 64 experts
+// of width 4096, 4.8 against 5.1 us).
 template <int NE, int CH>
 __device__ __forceinline__ void dot_rows(const uint16_t* __restrict__ xp, const uint16_t* __restrict__ rp,
                                          int64_t stride, int H, int lane, double (&s)[NE]) {
@@ -44,10 +46,11 @@ __device__ __forceinline__ void dot_rows(const uint16_t* __restrict__ xp, const 
 #pragma unroll
             for (int e = 0; e < NE; ++e)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // a product of two bf16 is exact in fp32
-                    s[e] += (double)(__uint_as_float(a[c][i] << 16) * __uint_as_float(b[e][c][i] << 16));
-                    s[e] += (double)(__uint_as_float(a[c][i] & 0xffff0000u) *
-                                     __uint_as_float(b[e][c][i] & 0xffff0000u));
+                for (int i = 0; i < 4; ++i) {
+                    s[e] = __builtin_fma((double)__uint_as_float(a[c][i] << 16),
+                                         (double)__uint_as_float(b[e][c][i] << 16), s[e]);
+                    s[e] = __builtin_fma((double)__uint_as_float(a[c][i] & 0xffff0000u),
+                                         (double)__uint_as_float(b[e][c][i] & 0xffff0000u), s[e]);
                 }
     }
 }

@@ -329,3 +329,21 @@ def test_inner_value_past_the_largest_bf16(form):
     ids, one = torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.ones((1, 1), device="cuda")
     y = lora.moe_experts(x, ids, one, *w)
     assert y[0].tolist() == [2.0 ** 28] * 4 + [-(2.0 ** 28)] + [0.0] * 3
+
+
+@pytest.mark.parametrize("H", [64, 16384])
+def test_route_products_past_fp32(H):
+    """Logits whose products leave the range of fp32 on either side: one
+    workgroup per token, and (a larger router) one wave per logit."""
+    x = torch.zeros(2, H, dtype=torch.bfloat16, device="cuda")
+    r = torch.zeros(6, H, dtype=torch.bfloat16, device="cuda")
+    x[0, :3] = torch.tensor([2.0 ** 100, 2.0 ** 100, 1.0])
+    r[0, :3] = torch.tensor([2.0 ** 100, -(2.0 ** 100), 5.0])  # 5: the first two cancel
+    r[1, 2], r[2, 2], r[3, 2] = 7.0, 3.0, -1.0
+    x[1, 3] = 2.0 ** -100
+    r[4, 3], r[5, 3] = 2.0 ** -60, 2.0 ** -58  # tiny, and not alike
+    ids, w = lora.moe_route(x, r, 3)
+    assert ids.tolist() == [[1, 0, 2], [5, 4, 0]]
+    want = np.exp(np.array([0.0, -2.0, -4.0]))
+    np.testing.assert_allclose(w[0].cpu().numpy(), want / want.sum(), rtol=2.0 ** -20)
+    np.testing.assert_allclose(w[1].cpu().numpy(), 1 / 3, rtol=2.0 ** -20)
