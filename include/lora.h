@@ -474,8 +474,10 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  *   ids      dev int32 [T][k] out;  weights  dev float [T][k] out
  *   workspace dev, at least lora_moe_route_workspace_bytes(T, H, E) bytes
  *            (0 for a small router: workspace may then be null)
- * A NaN logit ranks below every number; ids stay valid and distinct, and the
- * weights of that token are NaN.
+ * A NaN logit ranks below every number; ids stay valid and distinct. The
+ * weights of a token are NaN where a NaN logit is in the sum they are divided
+ * by (with renorm == 0 any, otherwise a chosen one), or where the largest
+ * logit is infinite.
  *
  * lora_moe_experts:
  *   y[t] = round(sum_j weights[t][j] down_e(silu(gate_e x[t]) * up_e x[t])),

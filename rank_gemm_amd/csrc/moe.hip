@@ -71,7 +71,8 @@ __device__ __forceinline__ int64_t rank_key(double v) {
 // The k largest of the E logits in LDS, by rank: RT threads of the 1024 count
 // for one logit how many come before it (larger, or equal at a lower index);
 // ranks below k are the choices. No round waits on another, whatever k. A NaN
-// ranks last, so the ids stay valid and distinct; its weights are NaN.
+// ranks last, so the ids stay valid and distinct; the weights are NaN where it
+// is in their sum.
 __device__ __forceinline__ void topk_token(const double* logits, int E, int k, int renorm, int32_t* ids,
                                            float* weights, double* sel) {
     const int tid = threadIdx.x;

@@ -347,3 +347,35 @@ def test_route_products_past_fp32(H):
     want = np.exp(np.array([0.0, -2.0, -4.0]))
     np.testing.assert_allclose(w[0].cpu().numpy(), want / want.sum(), rtol=2.0 ** -20)
     np.testing.assert_allclose(w[1].cpu().numpy(), 1 / 3, rtol=2.0 ** -20)
+
+
+def test_route_nan_logit_in_the_sum():
+    """A NaN logit reaches a token's weights through the sum they are divided
+    by: over all experts always, over the chosen ones only when it is chosen."""
+    x = torch.randn(4, 64, device="cuda").to(torch.bfloat16)
+    r = torch.randn(5, 64, device="cuda").to(torch.bfloat16)
+    clean = lora.moe_route(x, r, 2)
+    r[3] = float("nan")
+    ids, w = lora.moe_route(x, r, 2, renorm=False)
+    assert bool(torch.isnan(w).all()) and not bool((ids == 3).any())
+    ids, w = lora.moe_route(x, r, 5)
+    assert bool((ids[:, 4] == 3).all()) and bool(torch.isnan(w).all())
+    ids, w = lora.moe_route(x, r, 2)
+    assert not bool(torch.isnan(w).any())
+    same = (clean[0] != 3).all(dim=1)  # tokens that did not choose it before
+    assert torch.equal(ids[same], clean[0][same]) and torch.equal(w[same], clean[1][same])
+
+
+def test_route_infinite_logit():
+    """The largest logit infinite: exp(l - max) has no value. -inf elsewhere is a weight of 0."""
+    x = torch.ones(2, 64, dtype=torch.bfloat16, device="cuda")
+    x[1, 0] = 0.0
+    r = torch.randn(4, 64, device="cuda").to(torch.bfloat16)
+    r[2, 0] = float("inf")  # token 1: 0 * inf, a NaN
+    ids, w = lora.moe_route(x, r, 4)
+    assert ids[0, 0] == 2 and bool(torch.isnan(w).all()) and ids[1, 3] == 2
+    x[1, 0] = 1.0
+    r[2, 0] = float("-inf")
+    ids, w = lora.moe_route(x, r, 4)
+    assert bool((ids[:, 3] == 2).all()) and bool((w[:, 3] == 0).all())
+    np.testing.assert_allclose(w.sum(dim=1).cpu().numpy(), 1.0, rtol=2.0 ** -20)
