@@ -243,6 +243,10 @@ __device__ __forceinline__ MoeRun moe_find(const int32_t* __restrict__ ids, int 
         }
         left &= ~mine;
     }
+    // the list is read by other lanes than the ones that wrote it (and through
+    // a generic pointer): the writes have landed before any of them
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    __builtin_amdgcn_wave_barrier();
     return r;
 }
 

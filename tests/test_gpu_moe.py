@@ -379,3 +379,27 @@ def test_route_infinite_logit():
     ids, w = lora.moe_route(x, r, 4)
     assert bool((ids[:, 3] == 2).all()) and bool((w[:, 3] == 0).all())
     np.testing.assert_allclose(w.sum(dim=1).cpu().numpy(), 1.0, rtol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("T,k", [(16, 4), (33, 2), (5, 3)])
+def test_lists_of_changing_choices(T, k):
+    """Calls in a row whose choices change (the kernels' lists of an expert's
+    pairs with them), on whole numbers: exact before the rounding of y."""
+    H, I, E = 512, 64, 5
+    g = torch.Generator(device="cuda").manual_seed(T)
+
+    def ints(lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    x = ints(-3, 3, T, H)
+    x[:, 0] = 2.0
+    gate = torch.zeros(E, I, H, dtype=torch.bfloat16, device="cuda")
+    gate[:, :, 0] = 64.0  # silu(128) = 128 to the last bit
+    up, down = ints(-1, 1, E, I, H), ints(-1, 1, E, H, I)
+    out = torch.stack([128.0 * (x.double() @ up[e].double().t()) @ down[e].double().t() for e in range(E)])
+    assert float(out.abs().max()) * k < 2 ** 24
+    one = torch.ones(T, k, device="cuda")
+    for i in range(40):
+        ids = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+        want = sum((ids == e).sum(dim=1, keepdim=True).double() * out[e] for e in range(E))
+        assert torch.equal(lora.moe_experts(x, ids, one, gate, up, down), want.float().to(torch.bfloat16)), i
