@@ -41,6 +41,7 @@ __device__ __forceinline__ void dot_rows(const uint16_t* __restrict__ xp, const 
 #pragma unroll
             for (int e = 0; e < NE; ++e) b[e][c] = *or_zero(ok, rp + e * stride + k0 + 512 * c);
         }
+        issue_fence();
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
