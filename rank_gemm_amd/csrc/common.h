@@ -54,11 +54,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// The value whose bf16 rounding is the hi half of v = hi + lo, two halves that
-// keep 16 bits of its mantissa: v, up to the largest finite bf16. A finite v
-// past that would round to infinity and leave -inf as its remainder, whose
-// products add up to NaN; here hi stays finite and lo holds the rest, also
-// where the rest is infinite (or NaN).
+// The hi half of v = hi + lo, two bf16 that keep 16 bits of its mantissa: v
+// rounded, but never past the largest finite value. There lo = v - hi would be
+// -inf and the products of the halves add up to NaN; so hi stays finite and lo
+// holds the rest, also where v itself is infinite.
+__device__ __forceinline__ uint16_t bf16_hi(float v) {
+    const uint16_t h = f32_to_bf16(v);
+    return h - ((h & 0x7fff) == 0x7f80);
+}
+// the value to round for it, ahead of a conversion of two at once
 __device__ __forceinline__ float hi_half(float v) {
     constexpr float kMax = 0x1.fep127f;
     return __builtin_amdgcn_fmed3f(v, -kMax, kMax);

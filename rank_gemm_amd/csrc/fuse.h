@@ -121,7 +121,7 @@ __device__ __forceinline__ void fused_expand(f32x4 (&acc)[FM][FN], const Fuse& f
                         for (int z = 0; z < f.h_splits; ++z) v += hp[z * f.h_plane];
                         v *= sc;
                     }
-                    hi[e] = bf16_to_f32(f32_to_bf16(hi_half(v)));
+                    hi[e] = bf16_to_f32(bf16_hi(v));
                     lo[e] = v - hi[e];
                 }
                 const u32x2 ahi{pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};

@@ -462,7 +462,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_gate_up_kernel(MoeArgs a, cons
             if (q < hi && i < moe_inner(a.I)) {
                 const float v = i < a.I ? gs / (1.f + expf(-gs)) * us : 0.f;
                 uint16_t* ap = act + (int64_t)run.order[q] * 2 * Ir + moe_at<MX>(i);
-                const uint16_t h = f32_to_bf16(hi_half(v));
+                const uint16_t h = bf16_hi(v);
                 ap[0] = h;
                 ap[Ir] = f32_to_bf16(v - bf16_to_f32(h));
             }

@@ -592,7 +592,7 @@ __global__ __launch_bounds__(256) void mx4_operand_kernel(Mx4Prep a) {
         if (q < r)
             for (int z = 0; z < a.hs; ++z) v += a.h[((int64_t)z * a.M + p) * a.r_max + q];
         v *= sc;
-        const uint16_t hi = f32_to_bf16(hi_half(v));
+        const uint16_t hi = bf16_hi(v);
         a.ext[(p * 2) * rp + q] = hi;
         a.ext[(p * 2 + 1) * rp + q] = f32_to_bf16(v - bf16_to_f32(hi));
     }

@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void shrink_finish_kernel(const float* __restr
         const int64_t p = it.begin + m;
         if (ext) {
             v *= sc;
-            const uint16_t hi = f32_to_bf16(hi_half(v));
+            const uint16_t hi = bf16_hi(v);
             ext[(p * 2) * rp + q] = hi;
             ext[(p * 2 + 1) * rp + q] = f32_to_bf16(v - bf16_to_f32(hi));
         } else {

@@ -109,7 +109,7 @@ __device__ __forceinline__ void shrink_item(const uint16_t* __restrict__ X, cons
                 if (out.ext) {
                     if (q < out.rp) {
                         const float v = s[e] * out.scale;
-                        const uint16_t hi = f32_to_bf16(hi_half(v));
+                        const uint16_t hi = bf16_hi(v);
                         out.ext[(p * 2) * out.rp + q] = hi;
                         out.ext[(p * 2 + 1) * out.rp + q] = f32_to_bf16(v - bf16_to_f32(hi));
                     }
@@ -233,7 +233,7 @@ __device__ __forceinline__ void shrink_item_slices(const uint16_t* __restrict__ 
                 if (m >= it.count || q >= rp) continue;
                 const int64_t p = it.begin + m;
                 const float v = v4[e] * sc;
-                const uint16_t hi = f32_to_bf16(hi_half(v));
+                const uint16_t hi = bf16_hi(v);
                 ext[(p * 2) * rp + q] = hi;
                 ext[(p * 2 + 1) * rp + q] = f32_to_bf16(v - bf16_to_f32(hi));
             }
