@@ -218,18 +218,18 @@ static hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* w
                                 sl.scale, ext);
 }
 
-// One slice on the tiled path split over K: the 256 x 128 kernel writing
-// partials, then the split-K path's kernel 2, which adds them in split order
-// and rounds. The expand runs as extra K steps dealt round the splits; without
-// that form (r_max % 8 != 0, or pools of more than kMetaSlots slots), or when
-// those steps would add more than a fifth to a split, kernel 2 applies it from
-// fp32 h. The base product is split alike in every case, adapters or none, so
-// rows without one keep the bits of a base-only call (and the unsplit tile
-// takes longer: rank 12, 512 x 14336 -> 4096 84 against 166 us, 1024 x 14336 ->
-// 4096 135 against 169; 399 adapters of rank 64, 769 x 8200 -> 1500 225 against
-// 604; 59, 1024 x 14336 -> 4096 222 against 319).
+// One slice on the tiled path split over K: the shrink to the expand operand,
+// the 256 x 128 kernel writing partials (the extra K steps dealt round the
+// splits), then the split-K path's kernel 2 without adapters (adds the
+// partials, rounds).
+// Without the extra-step form of the expand (r_max % 8 != 0, or pools of more
+// than kMetaSlots slots), or when the extra steps would add more than a fifth
+// to a split, the slice runs unsplit.
+static hipError_t tiled_forward(const LinearArgs& L, const SliceArgs& sl, const GemmPlan& g, hipStream_t st,
+                                StageTimer* tm, uint16_t* ext_ready = nullptr);
 static hipError_t split_tiled_forward(const LinearArgs& L, const SliceArgs& sl, const GemmPlan& g, hipStream_t st,
                                       StageTimer* tm) {
+    const bool ext_ok = L.r_max % 8 == 0 && L.S <= kMetaSlots;
     // extra steps per 256-row tile, from the live slots of 256 rows bounded
     // by the work items (16 rows of one slot each) that fall in them (64 /
     // (2 rp) slots share a step when 2 rp divides 64); spread over the splits
@@ -238,27 +238,30 @@ static hipError_t split_tiled_forward(const LinearArgs& L, const SliceArgs& sl, 
     const int64_t slots_per_tile = items_per_tile < L.S ? items_per_tile : (int64_t)L.S;
     const int r2 = 2 * ((L.r_max + 7) & ~7);
     const int64_t est_extra = 64 % r2 == 0 ? (slots_per_tile * r2 + 63) / 64 : slots_per_tile * cdiv(r2, 64);
-    const bool steps = L.r_max % 8 == 0 && L.S <= kMetaSlots && est_extra * 5 <= (int64_t)g.tks * (g.tkc / 64);
+    if (L.adapters && (!ext_ok || est_extra * 5 > (int64_t)g.tks * (g.tkc / 64))) {
+        GemmPlan gu = g;
+        gu.tks = 0;
+        return tiled_forward(L, sl, gu, st, tm);
+    }
     const int M = L.M, N = sl.N, K = L.K;
     const int n_mt = cdiv(M, 64), n_nt = cdiv(N, 64);
     char* ws = static_cast<char*>(L.workspace);
     const size_t py = ((size_t)g.tks * n_mt * n_nt * 16 * 64 * 16 + 255) & ~size_t(255);
     float* part = reinterpret_cast<float*>(ws);
-    float* h = reinterpret_cast<float*>(ws + py);
-    uint16_t* ext = steps ? reinterpret_cast<uint16_t*>(h) : nullptr;
+    uint16_t* ext = reinterpret_cast<uint16_t*>(ws + py);
     if (L.adapters) {
-        const hipError_t e = tiled_shrink(L, sl, ws + py, steps ? nullptr : h, ext, st, tm);
+        const hipError_t e = tiled_shrink(L, sl, ws + py, nullptr, ext, st, tm);
         if (e != hipSuccess) return e;
     }
-    const Fuse f{L.token_order, L.slot_indptr, nullptr, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0,
-                 steps ? L.adapters : 0, ext, (L.r_max + 7) & ~7};
+    const Fuse f{L.token_order, L.slot_indptr, nullptr, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
+                 ext, (L.r_max + 7) & ~7};
     const hipError_t e =
         launch_tile<256, 128, 4, 2, 3, true>(L.X, sl.W, nullptr, M, N, K, f, false, st, tm, SplitOut{part, g.tkc, n_mt, n_nt},
                                      g.tks);
     if (e != hipSuccess) return e;
-    LinearArgs fin = L;
-    if (steps) fin.adapters = 0;
-    return splitk_finish_bf16(fin, sl, part, g.tks, n_mt, h, 1, st, tm);
+    LinearArgs base = L;
+    base.adapters = 0;
+    return splitk_finish_bf16(base, sl, part, g.tks, n_mt, nullptr, 1, st, tm);
 }
 
 // One slice on the tiled path: the shrink to final h, then the tiled GEMM
@@ -266,7 +269,7 @@ static hipError_t split_tiled_forward(const LinearArgs& L, const SliceArgs& sl, 
 // bf16 hi / lo; otherwise in the epilogue from fp32 h). With ext_ready the
 // expand operand was already written there (several slices, one shrink).
 static hipError_t tiled_forward(const LinearArgs& L, const SliceArgs& sl, const GemmPlan& g, hipStream_t st,
-                                StageTimer* tm, uint16_t* ext_ready = nullptr) {
+                                StageTimer* tm, uint16_t* ext_ready) {
     if (g.tks > 1) return split_tiled_forward(L, sl, g, st, tm);
     const int M = L.M, N = sl.N, K = L.K;
     Fuse f{L.token_order, L.slot_indptr, nullptr, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
