@@ -22,6 +22,7 @@
 //  * split-K (decode-sized T, splitk.hip): a K-split GEMM with the shrink in
 //    extra workgroups of the same launch, then a kernel that adds the splits
 //    and applies the expand.
+#include "../../include/lora.h"
 #include "gemm_tile.h"
 #include "shrink.h"
 
@@ -77,10 +78,6 @@ GemmPlan gemm_bf16_plan(int M, int N, int K) {
                 g.tks = kse;
                 g.tkc = kc;
             }
-        }
-        if (g.tks > 1) {
-            g.bm = 256;
-            g.bn = 128;
         }
         return g;
     }
@@ -218,31 +215,33 @@ static hipError_t tiled_shrink(const LinearArgs& L, const SliceArgs& sl, char* w
                                 sl.scale, ext);
 }
 
+// Whether a slice whose plan splits K runs split: where the pool has the
+// extra-step form of the expand (r_max % 8 == 0, at most kMetaSlots slots) and
+// those steps would add at most 3/8 to a split's. By the sizes and the pool
+// alone, not by the batch's plan or adapters: the split is the order in which
+// y's sums are taken, and rows without an adapter keep a base-only call's bits.
+// Split against unsplit, 769 x 8200 -> 1500: 128 slots of rank 16 (0.22) 69
+// against 85 us, 17 of rank 64 (0.26) 74 against 94; 512 x 14336 -> 4096: 64 of
+// rank 32 (0.21) 92 against 95, 256 of rank 16 (0.32) 134 against 121 with all in
+// use, 78 against 85 with 9; 512 of rank 16 (0.61) 172 against 171.
+static bool split_runs(const GemmPlan& g, int M, int S, int r_max) {
+    if (g.tks < 2 || r_max % 8 != 0 || S > kMetaSlots) return false;
+    // extra steps per 256-row tile, from the work items (16 rows of one slot
+    // each) that M rows over S slots can have in 256 rows (64 / (2 rp) slots
+    // share a step when 2 rp divides 64)
+    const int64_t items_per_tile = ((int64_t)lora_plan_max_items(M, S) * 256 + M - 1) / M;
+    const int64_t slots_per_tile = items_per_tile < S ? items_per_tile : S;
+    const int r2 = 2 * r_max;
+    const int64_t est_extra = 64 % r2 == 0 ? (slots_per_tile * r2 + 63) / 64 : slots_per_tile * cdiv(r2, 64);
+    return est_extra * 8 <= (int64_t)g.tks * (g.tkc / 64) * 3;
+}
+
 // One slice on the tiled path split over K: the shrink to the expand operand,
 // the 256 x 128 kernel writing partials (the extra K steps dealt round the
 // splits), then the split-K path's kernel 2 without adapters (adds the
 // partials, rounds).
-// Without the extra-step form of the expand (r_max % 8 != 0, or pools of more
-// than kMetaSlots slots), or when the extra steps would add more than a fifth
-// to a split, the slice runs unsplit.
-static hipError_t tiled_forward(const LinearArgs& L, const SliceArgs& sl, const GemmPlan& g, hipStream_t st,
-                                StageTimer* tm, uint16_t* ext_ready = nullptr);
 static hipError_t split_tiled_forward(const LinearArgs& L, const SliceArgs& sl, const GemmPlan& g, hipStream_t st,
                                       StageTimer* tm) {
-    const bool ext_ok = L.r_max % 8 == 0 && L.S <= kMetaSlots;
-    // extra steps per 256-row tile, from the live slots of 256 rows bounded
-    // by the work items (16 rows of one slot each) that fall in them (64 /
-    // (2 rp) slots share a step when 2 rp divides 64); spread over the splits
-    // they should stay small next to a split's base steps
-    const int64_t items_per_tile = ((int64_t)L.n_items * 256 + L.M - 1) / L.M;
-    const int64_t slots_per_tile = items_per_tile < L.S ? items_per_tile : (int64_t)L.S;
-    const int r2 = 2 * ((L.r_max + 7) & ~7);
-    const int64_t est_extra = 64 % r2 == 0 ? (slots_per_tile * r2 + 63) / 64 : slots_per_tile * cdiv(r2, 64);
-    if (L.adapters && (!ext_ok || est_extra * 5 > (int64_t)g.tks * (g.tkc / 64))) {
-        GemmPlan gu = g;
-        gu.tks = 0;
-        return tiled_forward(L, sl, gu, st, tm);
-    }
     const int M = L.M, N = sl.N, K = L.K;
     const int n_mt = cdiv(M, 64), n_nt = cdiv(N, 64);
     char* ws = static_cast<char*>(L.workspace);
@@ -269,8 +268,8 @@ static hipError_t split_tiled_forward(const LinearArgs& L, const SliceArgs& sl, 
 // bf16 hi / lo; otherwise in the epilogue from fp32 h). With ext_ready the
 // expand operand was already written there (several slices, one shrink).
 static hipError_t tiled_forward(const LinearArgs& L, const SliceArgs& sl, const GemmPlan& g, hipStream_t st,
-                                StageTimer* tm, uint16_t* ext_ready) {
-    if (g.tks > 1) return split_tiled_forward(L, sl, g, st, tm);
+                                StageTimer* tm, uint16_t* ext_ready = nullptr) {
+    if (split_runs(g, L.M, L.S, L.r_max)) return split_tiled_forward(L, sl, g, st, tm);
     const int M = L.M, N = sl.N, K = L.K;
     Fuse f{L.token_order, L.slot_indptr, nullptr, sl.B_pool, sl.rank, sl.scale, L.S, L.r_max, 1, 0, L.adapters,
            nullptr, (L.r_max + 7) & ~7};

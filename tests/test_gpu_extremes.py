@@ -18,7 +18,7 @@ EXPANDS = [
     (9000, 256, 300, 3, 16, "linear"),       # its full K range
     (2100, 256, 1300, 3, 12, "linear"),      # the tile's epilogue
     (512, 14336, 4096, 3, 16, "linear"),     # a tiled split's extra steps
-    (1030, 14336, 1100, 3, 12, "linear"),    # ... and beside them
+    (1030, 14336, 1100, 3, 12, "linear"),    # ... and unsplit, in the epilogue
     (9000, 256, 300, 3, 16, "multi"),        # several slices, one shrink
     (5, 256, 200, 3, 16, "bf16"),            # over a 4-bit base: kernel 2 of the bf16 path
     (64, 256, 14400, 3, 16, "bf16"),         # its own
