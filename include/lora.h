@@ -419,8 +419,9 @@ int lora_linear_noalloc(const lora_pool* pool, const void* x, const void* W, con
  * lora_mx4_pack_scales lays out scale bytes in row order, dev
  * [batch][rows][ceil(K / 32)], as a checkpoint holds them (the codes of such
  * a checkpoint are already in this form).
- * All three are asynchronous on `stream`. Errors: LORA_EINVAL (sizes, null
- * or misaligned pointers, unknown dtype), LORA_EHIP. With rows or batch 0
+ * No output may overlap an input or another output. All three are
+ * asynchronous on `stream`. Errors: LORA_EINVAL (sizes, null, misaligned or
+ * equal pointers, unknown dtype), LORA_EHIP. With rows or batch 0
  * they return LORA_OK and launch nothing.
  */
 #define LORA_MX4_MAX_ROWS 4194240
@@ -488,7 +489,7 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  *   ids, weights  as lora_moe_route writes them, or the caller's own; a
  *            choice whose id is outside [0, E) adds nothing, and a token may
  *            name an expert twice
- *   y        dev bf16 [T][H] out, overwritten completely; must not alias x
+ *   y        dev bf16 [T][H] out, overwritten completely
  *   workspace dev, at least lora_moe_experts_workspace_bytes(T, H, I, k) bytes
  * The terms of a token are added in the order of j: equal inputs give equal
  * bits. Products take bf16 operands with fp32 sums; the inner values
@@ -498,7 +499,8 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  * weights start on 16-byte, y on 8-byte boundaries; 1 <= E <= LORA_MOE_MAX_EXPERTS,
  * 1 <= k <= min(E, LORA_MOE_MAX_K) (lora_moe_experts: k may exceed E),
  * T k <= LORA_MOE_MAX_PAIRS; H and I at most LORA_MX4_MAX_ROWS, one expert's
- * matrix, x and the inner values under 2 GiB each. Asynchronous on `stream`.
+ * matrix, x and the inner values under 2 GiB each. No output may overlap an
+ * input or another output. Asynchronous on `stream`.
  * Errors: LORA_EINVAL, LORA_ESPACE, LORA_EHIP. T == 0 launches nothing.
  */
 #define LORA_MOE_MAX_EXPERTS 512

@@ -579,6 +579,7 @@ int lora_mx4_quantize(int dtype, const void* src, int batch, int rows, int K, vo
     if ((dtype != LORA_F32 && dtype != LORA_BF16) || !mx4_sizes(batch, rows, K)) return LORA_EINVAL;
     if (batch == 0 || rows == 0) return LORA_OK;
     if (!src || !aligned(src, es_of(dtype)) || !mx4_buffers(codes, scales)) return LORA_EINVAL;
+    if (src == codes || src == scales || codes == scales) return LORA_EINVAL;
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
     if (profiler().on) lk.lock();
@@ -593,6 +594,7 @@ int lora_mx4_dequantize(const void* codes, const void* scales, int batch, int ro
     if ((dtype != LORA_F32 && dtype != LORA_BF16) || !mx4_sizes(batch, rows, K)) return LORA_EINVAL;
     if (batch == 0 || rows == 0) return LORA_OK;
     if (!dst || !aligned(dst, es_of(dtype)) || !mx4_buffers(codes, scales)) return LORA_EINVAL;
+    if (dst == codes || dst == scales) return LORA_EINVAL;
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
     if (profiler().on) lk.lock();
@@ -605,7 +607,7 @@ int lora_mx4_dequantize(const void* codes, const void* scales, int batch, int ro
 int lora_mx4_pack_scales(const void* e8m0, int batch, int rows, int K, void* scales, void* stream) {
     if (!mx4_sizes(batch, rows, K)) return LORA_EINVAL;
     if (batch == 0 || rows == 0) return LORA_OK;
-    if (!e8m0 || !scales || !aligned(scales, 8)) return LORA_EINVAL;
+    if (!e8m0 || !scales || !aligned(scales, 8) || e8m0 == scales) return LORA_EINVAL;
     return lora::mx4_pack_scales((const uint8_t*)e8m0, batch, rows, K, (uint8_t*)scales, as_stream(stream)) ==
                    hipSuccess
                ? LORA_OK
@@ -679,6 +681,10 @@ int lora_moe_route(const void* x, const void* router, int T, int H, int E, int k
     if (!x || !router || !ids || !weights || !aligned(x, 16) || !aligned(router, 16)) return LORA_EINVAL;
     const size_t need = lora_moe_route_workspace_bytes(T, H, E);
     if (need > 0 && (!workspace || !aligned(workspace, 8) || workspace_bytes < need)) return LORA_ESPACE;
+    const void* out[2] = {ids, weights};
+    for (const void* o : out)
+        if (o == x || o == router) return LORA_EINVAL;
+    if (out[0] == out[1]) return LORA_EINVAL;
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
     if (profiler().on) lk.lock();
@@ -700,7 +706,8 @@ int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* w
         !moe_fits(form, T, H, I, k))
         return LORA_EINVAL;
     if (T == 0) return LORA_OK;
-    if (!x || !ids || !weights || !y || y == x || !aligned(x, 16) || !aligned(y, 8)) return LORA_EINVAL;
+    if (!x || !ids || !weights || !y || !aligned(x, 16) || !aligned(y, 8)) return LORA_EINVAL;
+    if (y == x || y == ids || y == weights) return LORA_EINVAL;
     const void* data[3] = {w->gate, w->up, w->down};
     const void* scales[3] = {w->gate_scales, w->up_scales, w->down_scales};
     for (int i = 0; i < 3; ++i) {

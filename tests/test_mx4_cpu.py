@@ -137,3 +137,19 @@ def test_experts_refuses_sizes(form, H, I):
     d = lora.MoeWeightsDesc(*[P16] * 6)
     assert lora.lib().lora_moe_experts(form, P16, P16, P16, ctypes.byref(d), 1, H, I, 2, 1, P16 + 4096, P16, 1 << 60,
                                        None) == lora.LORA_EINVAL
+
+
+def test_outputs_alias_nothing():
+    """Buffers that would be read and written, or written twice, in one call."""
+    L, Q = lora.lib(), P16 + 4096
+    for a, b, c in ((P16, P16, Q), (P16, Q, P16), (P16, Q, Q)):
+        assert L.lora_mx4_quantize(*q_args(src=a, codes=b, scales=c)) == lora.LORA_EINVAL
+    for dst in (P16, Q):
+        assert L.lora_mx4_dequantize(P16, Q, 1, 4, 64, lora.LORA_F32, dst, None) == lora.LORA_EINVAL
+    assert L.lora_mx4_pack_scales(P16, 1, 4, 64, P16, None) == lora.LORA_EINVAL
+    for ids, weights in ((P16, Q + 512), (Q, Q + 512), (Q + 512, P16), (Q + 512, Q), (Q + 512, Q + 512)):
+        assert L.lora_moe_route(P16, Q, 4, 64, 8, 2, 1, ids, weights, None, 0, None) == lora.LORA_EINVAL
+    d = lora.MoeWeightsDesc(*[P16 + 8192] * 6)
+    for y in (P16, Q, Q + 512, P16 + 8192):
+        assert L.lora_moe_experts(lora.LORA_MX4, P16, Q, Q + 512, ctypes.byref(d), 4, 64, 64, 8, 2, y, P16 + 16384,
+                                  1 << 20, None) == lora.LORA_EINVAL
