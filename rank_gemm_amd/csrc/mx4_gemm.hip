@@ -1,10 +1,13 @@
 // The tiled GEMM of MXFP4 operands (x rounded to 4 bits in plan order, W in 4
 // bits): gemm_tile.h's pipeline with the scaled 16x16x128 product. 8192 x 4096
-// -> 14336 takes 269 us, 3.6 PFLOP/s: 1.53 us per 256 k of a 256 x 256 tile, for
-// 0.97 us of matrix time (2048 cycles at 2.1 GHz; the matrix cores are busy 49%
-// of the kernel's cycles), as the bf16 tile takes for 64 k: two stages fill the
-// LDS, so a step's loads have one step to land. Without its stores it would take
-// 46 us less, without adapters 27 less.
+// -> 14336 takes 255 to 290 us by box and clock (median of event times 262, 3.7
+// PFLOP/s), base-only 230 to 240. A step of 256 k takes 1.55 to 1.60 us (slopes of
+// 8192 x 4096 .. 16384 -> 14336) for 0.97 us of matrix time (2048 cycles at 2.1
+// GHz; the matrix cores are busy 49% of the kernel's cycles). It is not memory: a
+// step that loads the same lines again and again takes 1.51. With every load
+// answered by zeros it takes 1.03, but zeros also spare the matrix cores power;
+// what the rest is has not been established. The stores are 8 us of the kernel,
+// 16 base-only.
 #include "gemm_tile.h"
 #include "mx4_linear.h"
 

@@ -186,9 +186,12 @@ __global__ __launch_bounds__(256) void mx4_split_kernel(Mx4Split a) {
 // lane group with rows 4 - 11 of its neighbour, whose chunk differs in bit 2:
 // the two sets of slots are then disjoint (with c ^ (r % 16) they are equal,
 // and conflicts take 48% of the LDS cycles). 64 rows,
-// 4096 -> 14336: 15 us (the 64-column kernel 27), bound by what a CU takes in:
-// twice as many bytes of x as of W; 2, 3 or 4 units in flight, one wave per
-// SIMD or two, and a rotated order of units per tile take the same time.
+// 4096 -> 14336: 15 us (the 64-column kernel 27), 5.9 and 1.10 a unit of 48 KB
+// (44 GB/s a CU, under half of what its feed reaches). No one resource bounds a
+// unit: with x's loads answered by zeros it takes 0.92 us, with W's 0.79, without
+// the products 0.80, the conversions 1.00, the fragment reads 1.00; they partly
+// follow one another. 2, 3 or 4 units in flight, one wave per SIMD or two, and a
+// rotated order of units per tile take the same time.
 constexpr int kWideCols = 128;
 __device__ __forceinline__ int wide_swizzle(int row) { return (row + 4) & 15; }
 
@@ -694,6 +697,12 @@ static bool finish_few(int M, int N) { return (int64_t)cdiv(N, 64) * cdiv(M, 16)
 // against 48), and at most 128 of its tiles (1024 x 4096 -> 1024 25 against 33;
 // 192 tiles 38 against 33), unless a pool that mx4_finish does not take would
 // leave many blocks to the bf16 path's kernel 2.
+// 4-bit activations: split K while its 64 x 64 tiles are few (kernels, split
+// against the 4-bit tile: 64 x 4096 -> 4096 15.5 against 22 us, 128 x 4096 ->
+// 4096 21 against 22, 256 x 4096 -> 2048 21 against 22, 512 x 4096 -> 1024 equal
+// at 22, 128 x 14336 -> 4096 39 against 35; past 128 tiles 65 x 4096 -> 8200 31
+// against 23, 96 x 4096 -> 14336 35 against 24), and for one tile of rows at any
+// width (64 x 4096 -> 14336 25 against 24).
 enum class Mx4Path { kSplit, kTile4, kDequant };
 static Mx4Path mx4_path(int M, int N, int K, int S, int r_max, bool act4) {
     if (act4) return M <= 64 || (int64_t)cdiv(M, 64) * cdiv(N, 64) <= 128 ? Mx4Path::kSplit : Mx4Path::kTile4;
@@ -710,8 +719,11 @@ static bool mx4_wide(int M, bool act4) { return !act4 && M > 16; }
 // item moves about the bytes of a unit per 256 k. The wide kernel takes the
 // splits of the least estimated time: 1.5 us per unit and workgroup of a CU
 // (two on one CU take about twice as long), and each split's partials,
-// written and read at 5 TB/s. The shrink takes K ranges of a
-// split's length, 8 at most.
+// written and read at 5 TB/s. The 64-column kernel goes for 512 workgroups (4-bit
+// x, kernels at 256 / 512 / 1024: 48 x 4096 -> 4096 18.5 / 15 / 15 us, 64 x 14336
+// -> 4096 32 / 28 / 26, 64 x 4096 -> 14336 29 / 25 / 28; 16-bit x: 1 x 4096 ->
+// 4096 9.6 / 8.7 / 8.7, 16 x 14336 -> 4096 18.9 / 16.7 / 18.2). The shrink takes
+// K ranges of a split's length, 8 at most.
 struct Mx4SplitPlan {
     int n_mt, n_nt, ks, upb, hs, hkc;
 };
