@@ -441,6 +441,8 @@ int lora_mx4_pack_scales(const void* e8m0, int batch, int rows, int K, void* sca
  *                  LORA_MX4: act(x) = each row of x rounded to MXFP4 by
  *                  lora_mx4_quantize's rule, the base product on the scaled
  *                  4-bit matrix instruction
+ * With 16-bit activations What is what lora_mx4_dequantize gives in bf16: values
+ * of 2^128 and up (scale bytes 253 and 254) are infinite.
  * The adapter correction reads x itself in both forms. Sums are fp32, y is
  * rounded once. bf16 pools only, of any d_in (rows of x, and the pool's A,
  * are copied to padded rows in the workspace when d_in is not a multiple of
@@ -485,7 +487,7 @@ int lora_linear_mx4_device_plan(const lora_pool* pool, const void* x, const void
  *   e = ids[t][j]
  *   form     LORA_BF16: gate, up dev bf16 [E][I][H], down dev bf16 [E][H][I],
  *            scale pointers ignored; LORA_MX4: the same shapes as batches of E
- *            MXFP4 matrices
+ *            MXFP4 matrices, taken as lora_mx4_dequantize gives them in bf16
  *   ids, weights  as lora_moe_route writes them, or the caller's own; a
  *            choice whose id is outside [0, E) adds nothing, and a token may
  *            name an expert twice

@@ -138,6 +138,28 @@ def test_scales_at_the_ends_of_their_range(T, d_in, d_out, act):
     assert not bad.any(), f"{bad.sum()} of {fine.sum()}, scale bytes {sorted(set(byte[bad.any(axis=0), 0].tolist()))}"
 
 
+@pytest.mark.parametrize("T,d_in,d_out", PATHS)
+def test_weights_past_the_largest_bf16(T, d_in, d_out):
+    """Scale bytes 252 .. 254 with every code: with 16-bit activations a value
+    past bf16's range is the infinity that dequantising gives, with 4-bit ones
+    the product is of the value itself."""
+    byte = np.full((d_out, -(-d_in // 32)), 127, np.uint8)
+    byte[:, 0] = 254 - np.arange(d_out) // 16 % 3
+    codes = np.zeros((d_out, byte.shape[1] * 16), np.uint8)
+    codes[:, 0] = np.arange(d_out) % 16  # the first value of each row
+    q = lora.mx4_pack(torch.from_numpy(codes).cuda(), torch.from_numpy(byte).cuda(), d_in)
+    x = torch.zeros(T, d_in, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 2.0 ** -100
+    pool = lora.Pool(2, 4, d_in, d_out, "bf16")
+    plan = lora.plan(np.zeros(T, np.int32), 2)
+    exact = mx4_ref.values(codes, byte, d_in)[:, 0]
+    as_bf16 = lora.mx4_dequantize(q, "bf16")[:, 0].double().cpu().numpy()
+    np.testing.assert_array_equal(as_bf16, np.where(np.abs(exact) < 2.0 ** 128, exact, np.copysign(np.inf, exact)))
+    for act, w in (("bf16", as_bf16), ("mx4", exact)):
+        y = lora.linear_mx4(x, q, pool, plan, act=act).double().cpu().numpy()
+        np.testing.assert_array_equal(y, np.broadcast_to(w * 2.0 ** -100, y.shape))
+
+
 @pytest.mark.parametrize("act", ["bf16", "mx4"])
 @pytest.mark.parametrize("T,d_in,d_out", PATHS)
 def test_nan_stays_in_its_row_and_column(T, d_in, d_out, act):
