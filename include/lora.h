@@ -523,10 +523,145 @@ int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* w
                      void* stream);
 
 /*
+ * lora_moe_route with the choice made by scores, a bias and groups:
+ *   s_e = sigmoid(l_e) (LORA_SCORE_SIGMOID) or softmax(l)_e over all E experts
+ *   (LORA_SCORE_SOFTMAX), l = x R^T as in lora_moe_route;  c_e = s_e + bias_e
+ *   With groups > 1 the experts form `groups` groups of E / groups
+ *   neighbours; a group's value is the sum of its group_best (1 or 2) largest
+ *   c, and only the experts of the top_groups groups of the largest values are
+ *   left. ids[t][0..k) are the k largest c of the experts left, falling;
+ *   weights[t][j] = scale * s, divided by the sum of the k chosen s if renorm.
+ *   bias     dev float [E], or null: it moves the choice, not the weights
+ * Equal values (c, or a group's) go to the lower index; a NaN ranks below every
+ * number, ids stay valid and distinct. Logits, scores and sums are held in 64
+ * bits, weights rounded to fp32 once. The softmax's scores are NaN if a logit
+ * is, or if the largest is infinite. Sizes, buffers, workspace and errors are
+ * lora_moe_route's; LORA_EINVAL also for an unknown score, groups < 1 or E not
+ * a multiple of it, top_groups outside [1, groups], k > top_groups * E /
+ * groups, group_best other than 1 and 2, a scale that is not finite, and an
+ * output that is the bias.
+ */
+#define LORA_SCORE_SOFTMAX 0
+#define LORA_SCORE_SIGMOID 1
+typedef struct lora_route_scores {
+    const float* bias;
+    int32_t score, groups, top_groups, group_best, renorm;
+    float scale;
+} lora_route_scores;
+int lora_moe_route_scored(const void* x, const void* router, int T, int H, int E, int k, const lora_route_scores* r,
+                          int32_t* ids, float* weights, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged key-value cache: position j of a request lies in row j % page_rows
+ * of page table[j / page_rows], the table a row of page numbers per request.
+ *   k, v   dev, caller-owned: element (page, row, head, d) of each at
+ *          page * page_stride + row * row_stride + head * head_stride + d
+ *          (strides in elements, above 0, alike for k and v; rows do not
+ *          overlap), so [page][row][head][dim] and [page][head][row][dim] both fit
+ *   form   LORA_BF16, or LORA_F8: 8-bit E4M3 values (4 bits of mantissa, at
+ *          most 448, no infinities), each standing for itself times its head's
+ *          k_scale or v_scale, dev float [kv_heads]
+ * dim is a multiple of 8 (LORA_F8: of 16) up to LORA_ATTN_MAX_DIM; k, v and
+ * every stride times the element size are multiples of 16 bytes. Offsets are
+ * computed in 64 bits.
+ */
+#define LORA_F8 3 /* a form of a cache, not of a pool */
+#define LORA_ATTN_MAX_DIM 256
+#define LORA_ATTN_MAX_BATCH 65535
+typedef struct lora_kv_cache {
+    void *k, *v;
+    const float *k_scale, *v_scale; /* LORA_F8 only */
+    int64_t page_stride, row_stride, head_stride;
+    int32_t form, n_pages, page_rows, kv_heads, dim;
+} lora_kv_cache;
+
+/*
+ * Store the keys and values of T tokens: cache row rows[t] (page * page_rows +
+ * row in the page) of every head takes k[t] and v[t]. LORA_F8 stores the
+ * nearest E4M3 value, ties to the even mantissa, of the fp32 quotient
+ * k / k_scale[head], values past 448 as 448; NaN stays NaN.
+ *   k, v   dev bf16 [T][kv_heads][dim], tokens k_stride and v_stride elements
+ *          apart (as views of merged q/k/v rows are); on 16-byte boundaries
+ *   rows   dev int64 [T]; a token whose row is outside the cache (-1, for a
+ *          padded place of the batch) is not stored. Rows that are named twice
+ *          hold pieces of either token.
+ * Every other row of the cache is left as it was. Asynchronous on `stream`.
+ * Errors: LORA_EINVAL (sizes, null, misaligned or equal pointers), LORA_EHIP.
+ * T == 0 launches nothing.
+ */
+int lora_kv_append(const lora_kv_cache* cache, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                   const int64_t* rows, int T, void* stream);
+
+/*
+ * Attention of one new token a request over its cached positions:
+ *   out[b][h] = round(sum_j p_j v_j),  p = softmax_j(scale q[b][h] . k_j),
+ *   j from max(0, n_b - window) (window 0: from 0) to n_b - 1
+ * where k_j and v_j are those of kv head h / (heads / kv_heads).
+ *   q        dev bf16 [B][heads][dim], requests q_stride elements apart; on
+ *            16-byte boundaries
+ *   table    dev int32 [B][width], rows table_stride elements apart; entries
+ *            past a request's last page are not read
+ *   lengths  dev int32 [B]: n_b, the new token's own position included; below
+ *            0 taken as 0, past width * page_rows as that
+ *   out      dev bf16 [B][heads][dim] out, overwritten completely, on 16-byte
+ *            boundaries
+ *   lse      dev float [B][heads] out, or null: log sum_j exp(scale q . k_j)
+ *   workspace dev, at least lora_attn_decode_workspace_bytes(...) bytes (0 for
+ *            some sizes: it may then be null)
+ * Positions whose page number is outside [0, n_pages) are left out. A request
+ * without a position (length 0, or all left out) gets zeros and an lse of
+ * -infinity. Scores, sums and outputs are held in fp32, out is rounded once;
+ * a cache row that holds a NaN at an attended position gives NaN. The order of
+ * sums depends on the lengths of the whole batch, not on time: equal inputs
+ * give equal bits. No output may overlap an input, the workspace or another
+ * output. Asynchronous on `stream`. Errors: LORA_EINVAL (sizes, a heads that
+ * is no multiple of kv_heads, width * page_rows past 2^30, a scale that is not
+ * finite, null, misaligned or equal pointers), LORA_ESPACE, LORA_EHIP. B == 0
+ * launches nothing.
+ */
+size_t lora_attn_decode_workspace_bytes(int B, int heads, int kv_heads, int dim, int width, int page_rows);
+int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride, int heads, const int32_t* table,
+                     int64_t table_stride, int width, const int32_t* lengths, int B, float scale, int window,
+                     void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The next token of each request from its logits l and a random number u:
+ *   w_i = exp((l_i - max l) / temperature);  in the order of falling l, equal
+ *   logits by index: the first top_k tokens, of these the shortest prefix
+ *   whose sum of w is at least top_p of theirs, of these the ones with
+ *   w_i >= min_p (the first token in the order always stays); then ids[b] =
+ *   the lowest index at which the running sum, by index, of the kept w passes
+ *   u times their whole sum, and probs[b] = its w over that sum.
+ *   logits   dev LORA_F32 or LORA_BF16 [B][V], requests `stride` elements apart
+ *   u        dev double [B] in [0, 1)
+ *   temperature, top_p, min_p dev float [B], top_k dev int32 [B]: each request's
+ *            own, or null for temperature 1 and no filter. A temperature that is
+ *            not above 0 takes the first token in the order, with probability 1.
+ *            top_k < 1, top_p >= 1 and min_p <= 0 (or NaN) filter nothing;
+ *            top_p <= 0 leaves the first token.
+ *   ids      dev int32 [B] out;  probs  dev float [B] out
+ *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes
+ * Tokens whose logit is NaN or -infinity are never drawn; where there is no
+ * other, ids[b] = -1 and probs[b] = 0. Among logits of +infinity all weigh the
+ * same, and nothing else does. Weights are 64-bit exponentials, rounded to
+ * whole numbers of 2^-shift (shift = 46 up to 65536 tokens, then 62 less the
+ * bits of V - 1); their sums are exact, so equal inputs give equal bits.
+ * 1 <= V <= LORA_SAMPLE_MAX_VOCAB, B <= LORA_SAMPLE_MAX_BATCH. Asynchronous on
+ * `stream`. Errors: LORA_EINVAL (sizes, unknown dtype, null, misaligned or
+ * equal pointers), LORA_ESPACE, LORA_EHIP. B == 0 launches nothing.
+ */
+#define LORA_SAMPLE_MAX_VOCAB 4194304
+#define LORA_SAMPLE_MAX_BATCH 65535
+size_t lora_sample_workspace_bytes(int B, int V);
+int lora_sample(int dtype, const void* logits, int64_t stride, int B, int V, const double* u,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* ids,
+                float* probs, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Per-kernel timing, for diagnostics and the benchmark's roofline figures.
  * Between lora_profile_begin and lora_profile_end, lora_linear,
  * lora_linear_multi, lora_shrink, lora_mx4_quantize, lora_mx4_dequantize,
- * lora_linear_mx4 and lora_moe_* record a HIP event pair around every kernel
+ * lora_linear_mx4, lora_moe_*, lora_kv_append, lora_attn_decode and lora_sample record a HIP event pair around every kernel
  * they launch, on the stream it is launched on (not while that stream is being
  * captured into a graph, and at most max_records kernels).
  * lora_profile_end waits for the recorded events and writes one entry per

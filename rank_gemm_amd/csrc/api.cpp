@@ -182,6 +182,33 @@ inline bool moe_sizes(int T, int H, int E, int k) {
            T <= LORA_MOE_MAX_PAIRS / k;
 }
 
+static_assert(LORA_ATTN_MAX_DIM == lora::kAttnMaxDim, "head dimension of the interface and the kernels");
+
+// A cache the kernels can address; its buffers only where they are used.
+int check_cache(const lora_kv_cache* c) {
+    if (!c || (c->form != LORA_BF16 && c->form != LORA_F8)) return LORA_EINVAL;
+    const int unit = c->form == LORA_F8 ? 16 : 8;  // elements of 16 bytes
+    if (c->n_pages < 1 || c->page_rows < 1 || c->kv_heads < 1 || c->dim < 1 || c->dim > LORA_ATTN_MAX_DIM ||
+        c->dim % unit != 0)
+        return LORA_EINVAL;
+    for (int64_t s : {c->page_stride, c->row_stride, c->head_stride})
+        if (s < c->dim || s % unit != 0) return LORA_EINVAL;
+    if (!c->k || !c->v || c->k == c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return LORA_EINVAL;
+    if (c->form == LORA_F8 &&
+        (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+        return LORA_EINVAL;
+    return LORA_OK;
+}
+inline lora::KvCache kernel_cache(const lora_kv_cache& c) {
+    return {c.k, c.v, c.k_scale, c.v_scale, c.page_stride, c.row_stride, c.head_stride,
+            c.n_pages, c.page_rows, c.kv_heads, c.dim};
+}
+inline bool attn_sizes(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
+    return B >= 0 && B <= LORA_ATTN_MAX_BATCH && kv_heads >= 1 && heads >= kv_heads && heads <= 65535 &&
+           heads % kv_heads == 0 && dim >= 1 && dim <= LORA_ATTN_MAX_DIM && width >= 1 && page_rows >= 1 &&
+           width <= (1 << 30) / page_rows;
+}
+
 // The experts' kernels address one matrix, x and the inner values through
 // buffer resources: each under 2 GiB.
 inline bool moe_fits(int form, int T, int H, int I, int k) {
@@ -723,6 +750,115 @@ int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* w
                           {data[1], (const uint8_t*)scales[1]}, {data[2], (const uint8_t*)scales[2]},
                           (uint16_t*)y, T, H, I, E, k, workspace};
     return lora::moe_experts(a, form == LORA_MX4, st, timer_for(st)) == hipSuccess ? LORA_OK : LORA_EHIP;
+}
+
+int lora_moe_route_scored(const void* x, const void* router, int T, int H, int E, int k, const lora_route_scores* r,
+                          int32_t* ids, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!moe_sizes(T, H, E, k) || !r || (r->score != LORA_SCORE_SOFTMAX && r->score != LORA_SCORE_SIGMOID))
+        return LORA_EINVAL;
+    if (r->groups < 1 || E % r->groups != 0 || r->top_groups < 1 || r->top_groups > r->groups ||
+        k > r->top_groups * (E / r->groups) || r->group_best < 1 || r->group_best > 2 || !std::isfinite(r->scale))
+        return LORA_EINVAL;
+    if (T == 0) return LORA_OK;
+    if (!x || !router || !ids || !weights || !aligned(x, 16) || !aligned(router, 16)) return LORA_EINVAL;
+    const size_t need = lora_moe_route_workspace_bytes(T, H, E);
+    if (need > 0 && (!workspace || !aligned(workspace, 8) || workspace_bytes < need)) return LORA_ESPACE;
+    const void* out[2] = {ids, weights};
+    for (const void* o : out)
+        if (o == x || o == router || o == r->bias) return LORA_EINVAL;
+    if (out[0] == out[1]) return LORA_EINVAL;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    const lora::RouteScored rs{r->score == LORA_SCORE_SIGMOID, r->bias, r->groups, r->top_groups, r->group_best,
+                               r->renorm, r->scale};
+    return lora::moe_route_scored((const uint16_t*)x, (const uint16_t*)router, T, H, E, k, rs, ids, weights, workspace,
+                                  st, timer_for(st)) == hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+int lora_kv_append(const lora_kv_cache* c, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                   const int64_t* rows, int T, void* stream) {
+    int rc = check_cache(c);
+    if (rc != LORA_OK) return rc;
+    const int64_t row = (int64_t)c->kv_heads * c->dim;
+    // a workgroup per 256 pieces of 8 values
+    if (T < 0 || row / 8 > INT32_MAX || (int64_t)T * (row / 8) > (int64_t)INT32_MAX * 256) return LORA_EINVAL;
+    for (int64_t s : {k_stride, v_stride})
+        if (s < row || s % 8 != 0) return LORA_EINVAL;
+    if (T == 0) return LORA_OK;
+    if (!k || !v || !rows || !aligned(k, 16) || !aligned(v, 16) || !aligned(rows, 8)) return LORA_EINVAL;
+    for (const void* in : {k, v, (const void*)rows, (const void*)c->k_scale, (const void*)c->v_scale})
+        if (in == c->k || in == c->v) return LORA_EINVAL;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    return lora::kv_append(kernel_cache(*c), c->form == LORA_F8, (const uint16_t*)k, (const uint16_t*)v, k_stride,
+                           v_stride, rows, T, st, timer_for(st)) == hipSuccess
+               ? LORA_OK
+               : LORA_EHIP;
+}
+
+size_t lora_attn_decode_workspace_bytes(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
+    return attn_sizes(B, heads, kv_heads, dim, width, page_rows)
+               ? lora::attn_decode_workspace(B, heads, kv_heads, dim, width, page_rows)
+               : 0;
+}
+
+int lora_attn_decode(const lora_kv_cache* c, const void* q, int64_t q_stride, int heads, const int32_t* table,
+                     int64_t table_stride, int width, const int32_t* lengths, int B, float scale, int window,
+                     void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_cache(c);
+    if (rc != LORA_OK) return rc;
+    if (!attn_sizes(B, heads, c->kv_heads, c->dim, width, c->page_rows) || !std::isfinite(scale) || window < 0 ||
+        q_stride < (int64_t)heads * c->dim || q_stride % 8 != 0 || table_stride < width)
+        return LORA_EINVAL;
+    if (B == 0) return LORA_OK;
+    if (!q || !table || !lengths || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) ||
+        !aligned(lengths, 4) || !aligned(lse, 4))
+        return LORA_EINVAL;
+    const size_t need = lora_attn_decode_workspace_bytes(B, heads, c->kv_heads, c->dim, width, c->page_rows);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LORA_ESPACE;
+    for (const void* o : {(const void*)out, (const void*)lse})
+        for (const void* in : {q, (const void*)table, (const void*)lengths, (const void*)c->k, (const void*)c->v,
+                               (const void*)c->k_scale, (const void*)c->v_scale, (const void*)(need > 0 ? workspace : nullptr)})
+            if (o && o == in) return LORA_EINVAL;
+    if (out == lse) return LORA_EINVAL;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    const lora::AttnArgs a{kernel_cache(*c), (const uint16_t*)q, q_stride, heads, B, table, table_stride, width, lengths,
+                           (float)((double)scale * 1.4426950408889634), window, (uint16_t*)out, lse, workspace};
+    return lora::attn_decode(a, c->form == LORA_F8, st, timer_for(st)) == hipSuccess ? LORA_OK : LORA_EHIP;
+}
+
+size_t lora_sample_workspace_bytes(int B, int V) {
+    return B < 0 || B > LORA_SAMPLE_MAX_BATCH || V < 1 || V > LORA_SAMPLE_MAX_VOCAB ? 0 : lora::sample_workspace(B, V);
+}
+
+int lora_sample(int dtype, const void* logits, int64_t stride, int B, int V, const double* u,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* ids,
+                float* probs, void* workspace, size_t workspace_bytes, void* stream) {
+    if ((dtype != LORA_F32 && dtype != LORA_BF16) || B < 0 || B > LORA_SAMPLE_MAX_BATCH || V < 1 ||
+        V > LORA_SAMPLE_MAX_VOCAB || stride < V)
+        return LORA_EINVAL;
+    if (B == 0) return LORA_OK;
+    if (!logits || !u || !ids || !probs || !aligned(logits, es_of(dtype)) || !aligned(u, 8) || !aligned(ids, 4) ||
+        !aligned(probs, 4))
+        return LORA_EINVAL;
+    const size_t need = lora_sample_workspace_bytes(B, V);
+    if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LORA_ESPACE;
+    for (const void* o : {(const void*)ids, (const void*)probs})
+        for (const void* in : {logits, (const void*)u, (const void*)temperature, (const void*)top_k,
+                               (const void*)top_p, (const void*)min_p, (const void*)(need > 0 ? workspace : nullptr)})
+            if (o == in) return LORA_EINVAL;
+    if ((const void*)ids == (const void*)probs) return LORA_EINVAL;
+    hipStream_t st = as_stream(stream);
+    std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
+    if (profiler().on) lk.lock();
+    const lora::SampleArgs a{logits, stride, B, V, u, temperature, top_k, top_p, min_p, ids, probs, workspace};
+    return lora::sample(a, dtype == LORA_BF16, st, timer_for(st)) == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 
 int lora_profile_begin(int max_records) {

@@ -181,6 +181,63 @@ hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, in
 size_t moe_experts_workspace(int T, int H, int I, int k);
 hipError_t moe_experts(const MoeArgs& a, bool mx4, hipStream_t st, StageTimer* tm);
 
+// The same with scores in place of logits, a bias and groups.
+struct RouteScored {
+    int sigmoid;       // scores: sigmoid of each logit, or the softmax of all
+    const float* bias; // [E] added to the scores for the choice alone, or null
+    int groups, top_groups, group_best;
+    int renorm;
+    float scale;
+};
+hipError_t moe_route_scored(const uint16_t* X, const uint16_t* router, int T, int H, int E, int k,
+                            const RouteScored& r, int32_t* ids, float* weights, void* workspace, hipStream_t st,
+                            StageTimer* tm);
+
+// ---- paged key-value cache and decode attention -----------------------------------
+struct KvCache {  // strides in elements: bf16, or 8-bit E4M3 values
+    void *k, *v;
+    const float *k_scale, *v_scale;  // [kv_heads], 8-bit caches
+    int64_t page_stride, row_stride, head_stride;
+    int n_pages, page_rows, kv_heads, dim;
+};
+hipError_t kv_append(const KvCache& c, bool f8, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                     int64_t v_stride, const int64_t* rows, int T, hipStream_t st, StageTimer* tm);
+
+constexpr int kAttnMaxDim = 256;
+struct AttnArgs {
+    KvCache c;
+    const uint16_t* q;  // [B] rows q_stride apart, each [heads][dim]
+    int64_t q_stride;
+    int heads, B;
+    const int32_t* table;  // [B] rows table_stride apart, each [width]
+    int64_t table_stride;
+    int width;
+    const int32_t* lengths;  // [B]
+    float scale_log2;        // softmax scale times log2(e)
+    int window;              // 0: none
+    uint16_t* out;           // [B][heads][dim]
+    float* lse;              // [B][heads] or null
+    void* workspace;
+};
+size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width, int page_rows);
+hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* tm);
+
+// ---- sampling ----------------------------------------------------------------------
+struct SampleArgs {
+    const void* logits;  // [B] rows stride apart, each [V]
+    int64_t stride;
+    int B, V;
+    const double* u;           // [B]
+    const float* temperature;  // [B], or null: 1
+    const int32_t* top_k;      // [B], or null: all
+    const float *top_p, *min_p;
+    int32_t* ids;
+    float* probs;
+    void* workspace;
+};
+size_t sample_workspace(int B, int V);
+hipError_t sample(const SampleArgs& a, bool bf16, hipStream_t st, StageTimer* tm);
+
 // ---- slot pool ------------------------------------------------------------
 hipError_t pool_check_finite(int dtype, const void* p, int64_t n, int* flag, hipStream_t st);
 hipError_t pool_write_slot(int dtype, void* A_pool, void* B_pool, int32_t* rank, float* scale, int slot,

@@ -107,15 +107,11 @@ __device__ __forceinline__ void topk_token(const double* logits, int E, int k, i
     if (tid < k) weights[tid] = p / den;
 }
 
-// One workgroup per token: its 16 waves take four experts at a time.
-__global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t* __restrict__ X,
-                                                         const uint16_t* __restrict__ R, int H, int E, int k,
-                                                         int renorm, int32_t* __restrict__ ids,
-                                                         float* __restrict__ weights) {
-    __shared__ double logits[kMoeMaxExperts];
-    __shared__ double sel[kMoeMaxK];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x;
-    const uint16_t* xp = X + (int64_t)t * H;
+// The logits of a token into LDS: the workgroup's 16 waves take four experts
+// at a time.
+__device__ __forceinline__ void token_logits(const uint16_t* __restrict__ xp, const uint16_t* __restrict__ R, int H,
+                                             int E, double* logits) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int e0 = wave * 4; e0 < E; e0 += 64) {
         double s[4];
         if (e0 + 4 <= E) {  // uniform
@@ -133,6 +129,16 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t* __restr
             logits[e0 + lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
     }
     __syncthreads();
+}
+
+__global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t* __restrict__ X,
+                                                         const uint16_t* __restrict__ R, int H, int E, int k,
+                                                         int renorm, int32_t* __restrict__ ids,
+                                                         float* __restrict__ weights) {
+    __shared__ double logits[kMoeMaxExperts];
+    __shared__ double sel[kMoeMaxK];
+    const int t = blockIdx.x;
+    token_logits(X + (int64_t)t * H, R, H, E, logits);
     topk_token(logits, E, k, renorm, ids + t * k, weights + t * k, sel);
 }
 
@@ -158,6 +164,112 @@ __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict
     for (int i = threadIdx.x; i < E; i += 1024) lds[i] = logits[(int64_t)t * E + i];
     __syncthreads();
     topk_token(lds, E, k, renorm, ids + t * k, weights + t * k, sel);
+}
+
+// ----------------------------------------------------------- route by scores --
+// s_e = sigmoid(l_e), or the softmax of all logits; c_e = s_e + bias_e. With
+// groups of n = E / groups neighbours, a group's value is the sum of its
+// group_best largest c, and the experts of the top_groups groups of the
+// largest values are left. Of these the k largest c are chosen; their weights
+// are their s, divided by its sum where renorm, times scale. Everything is
+// held in 64 bits, and every choice is by rank, as in topk_token: equal values
+// to the lower index, NaN below every number.
+struct ScoredLds {
+    double logits[kMoeMaxExperts];  // then the scores
+    int64_t key[kMoeMaxExperts];    // of c
+    double best[kMoeMaxExperts];    // [groups][group_best] largest c
+    int left[kMoeMaxExperts];       // is this group left?
+    double sel[kMoeMaxK];
+};
+__device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const RouteScored& r, int32_t* ids,
+                                             float* weights) {
+    const int tid = threadIdx.x, lane = tid & 63, n = E / r.groups;
+    // every wave that holds a score takes the softmax's maximum and sum for itself
+    double top = -INFINITY, den = 0.0;
+    if (!r.sigmoid && tid - lane < E) {
+        for (int i = lane; i < E; i += 64) top = fmax(top, L.logits[i]);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o));
+        for (int i = lane; i < E; i += 64) den += exp(L.logits[i] - top);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) den += __shfl_xor(den, o);
+    }
+    double s = 0.0, c = 0.0;
+    if (tid < E) {
+        const double l = L.logits[tid];
+        s = r.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / den;
+        c = r.bias ? s + (double)r.bias[tid] : s;
+        L.key[tid] = rank_key(c);
+    }
+    __syncthreads();
+    if (tid < E) L.logits[tid] = s;
+    const int best = min(r.group_best, n);
+    if (r.groups > 1) {
+        if (tid < E) {
+            const int g0 = tid / n * n;
+            const int64_t mine = L.key[tid];
+            int before = 0;
+            for (int j = g0; j < g0 + n; ++j) before += L.key[j] > mine || (L.key[j] == mine && j < tid);
+            if (before < best) L.best[tid / n * best + before] = c;
+        }
+        __syncthreads();
+        if (tid < r.groups) {
+            auto value = [&](int g) { return rank_key(best == 2 ? L.best[2 * g] + L.best[2 * g + 1] : L.best[g]); };
+            const int64_t mine = value(tid);
+            int before = 0;
+            for (int g = 0; g < r.groups; ++g) {
+                const int64_t other = value(g);
+                before += other > mine || (other == mine && g < tid);
+            }
+            L.left[tid] = before < r.top_groups;
+        }
+    } else if (tid == 0) {
+        L.left[0] = 1;
+    }
+    __syncthreads();
+    const int rt = E <= 64 ? 16 : E <= 128 ? 8 : E <= 256 ? 4 : 2;  // threads per expert, neighbours in a wave
+    const int e = tid / rt, part = tid % rt;
+    const bool on = e < E && L.left[e / n];
+    int before = 0;
+    if (on) {
+        const int64_t mine = L.key[e];
+        for (int j = part; j < E; j += rt)
+            before += L.left[j / n] && (L.key[j] > mine || (L.key[j] == mine && j < e));
+    }
+    for (int o = 1; o < rt; o <<= 1) before += __shfl_xor(before, o);
+    if (on && part == 0 && before < k) {
+        ids[before] = e;
+        L.sel[before] = L.logits[e];
+    }
+    __syncthreads();
+    if (tid < k) {
+        double sum = 1.0;
+        if (r.renorm) {
+            sum = 0.0;
+            for (int j = 0; j < k; ++j) sum += L.sel[j];
+        }
+        weights[tid] = (float)(L.sel[tid] / sum * (double)r.scale);
+    }
+}
+
+__global__ __launch_bounds__(1024) void moe_scored_kernel(const uint16_t* __restrict__ X,
+                                                          const uint16_t* __restrict__ R, int H, int E, int k,
+                                                          RouteScored r, int32_t* __restrict__ ids,
+                                                          float* __restrict__ weights) {
+    __shared__ ScoredLds L;
+    const int t = blockIdx.x;
+    token_logits(X + (int64_t)t * H, R, H, E, L.logits);
+    scored_token(L, E, k, r, ids + t * k, weights + t * k);
+}
+
+__global__ __launch_bounds__(1024) void moe_scored_topk_kernel(const double* __restrict__ logits, int E, int k,
+                                                               RouteScored r, int32_t* __restrict__ ids,
+                                                               float* __restrict__ weights) {
+    __shared__ ScoredLds L;
+    const int t = blockIdx.x;
+    for (int i = threadIdx.x; i < E; i += 1024) L.logits[i] = logits[(int64_t)t * E + i];
+    __syncthreads();
+    scored_token(L, E, k, r, ids + t * k, weights + t * k);
 }
 
 // ---------------------------------------------------------------- experts --
@@ -599,6 +711,20 @@ hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, in
     if (e != hipSuccess) return e;
     return launch(tm, "moe_topk", moe_topk_kernel, dim3(T), dim3(1024), st, (const double*)logits, E, k, renorm, ids,
                   weights);
+}
+
+hipError_t moe_route_scored(const uint16_t* X, const uint16_t* router, int T, int H, int E, int k,
+                            const RouteScored& r, int32_t* ids, float* weights, void* workspace, hipStream_t st,
+                            StageTimer* tm) {
+    if ((int64_t)E * H <= kMoeRouteOne)
+        return launch(tm, "moe_scored", moe_scored_kernel, dim3(T), dim3(1024), st, X, router, H, E, k, r, ids,
+                      weights);
+    double* logits = static_cast<double*>(workspace);
+    hipError_t e = launch(tm, "moe_logits", moe_logits_kernel, dim3((E + 3) / 4, T), dim3(256), st, X, router, H, E,
+                          logits);
+    if (e != hipSuccess) return e;
+    return launch(tm, "moe_scored_topk", moe_scored_topk_kernel, dim3(T), dim3(1024), st, (const double*)logits, E, k,
+                  r, ids, weights);
 }
 
 // the inner values of every pair, its down products, then the plan

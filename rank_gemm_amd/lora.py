@@ -9,7 +9,9 @@ fallback of any kind: if it is missing, or no GPU is present, calls raise.
 Names follow the C ABI: ``Pool.install`` -> lora_pool_install, ``plan`` ->
 lora_plan, ``linear`` -> lora_linear, ``shrink`` -> lora_shrink,
 ``mx4_quantize`` -> lora_mx4_quantize, ``linear_mx4`` -> lora_linear_mx4,
-``moe_route`` -> lora_moe_route, ``moe_experts`` -> lora_moe_experts.
+``moe_route`` -> lora_moe_route, ``moe_experts`` -> lora_moe_experts,
+``moe_route_scored`` -> lora_moe_route_scored, ``kv_append`` -> lora_kv_append,
+``attn_decode`` -> lora_attn_decode, ``sample`` -> lora_sample.
 """
 from __future__ import annotations
 
@@ -24,7 +26,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora.so")
 
 LORA_OK, LORA_EINVAL, LORA_ESLOT, LORA_ERANK, LORA_ENONFINITE, LORA_EHIP, LORA_ESPACE = 0, -1, -2, -3, -4, -5, -6
-LORA_F32, LORA_BF16, LORA_MX4 = 0, 1, 2
+LORA_F32, LORA_BF16, LORA_MX4, LORA_F8 = 0, 1, 2, 3
+LORA_SCORE_SOFTMAX, LORA_SCORE_SIGMOID = 0, 1
 LORA_PLAN_ROWS = 16
 
 EXPORTS = (
@@ -36,12 +39,15 @@ EXPORTS = (
     "lora_linear_noalloc", "lora_plan_upload", "lora_mx4_row_bytes", "lora_mx4_scale_bytes", "lora_mx4_quantize",
     "lora_mx4_dequantize", "lora_mx4_pack_scales", "lora_workspace_bytes_mx4", "lora_linear_mx4",
     "lora_linear_mx4_device_plan", "lora_moe_route_workspace_bytes", "lora_moe_route",
-    "lora_moe_experts_workspace_bytes", "lora_moe_experts",
+    "lora_moe_experts_workspace_bytes", "lora_moe_experts", "lora_moe_route_scored", "lora_kv_append",
+    "lora_attn_decode_workspace_bytes", "lora_attn_decode", "lora_sample_workspace_bytes", "lora_sample",
 )
 LORA_DEVICE_PLAN_MAX_SLOTS = 4096
 LORA_NOALLOC_MAX_WORKSPACE = 32 << 20
 LORA_MAX_SLICES = 4
 LORA_MOE_MAX_EXPERTS, LORA_MOE_MAX_K, LORA_MOE_MAX_PAIRS = 512, 16, 512
+LORA_ATTN_MAX_DIM, LORA_ATTN_MAX_BATCH = 256, 65535
+LORA_SAMPLE_MAX_VOCAB, LORA_SAMPLE_MAX_BATCH = 4194304, 65535
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
 _CODE = {"bf16": LORA_BF16, "f32": LORA_F32}
@@ -69,6 +75,20 @@ class MoeWeightsDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scales", "up_scales", "down_scales")]
 
 
+class RouteScoresDesc(ctypes.Structure):
+    """lora_route_scores: how lora_moe_route_scored chooses."""
+    _fields_ = [("bias", ctypes.c_void_p), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """lora_kv_cache: a paged key-value cache."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "row_stride", "head_stride")] + [
+        (n, ctypes.c_int32) for n in ("form", "n_pages", "page_rows", "kv_heads", "dim")]
+
+
 class KernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("count", ctypes.c_int32), ("mean_ms", ctypes.c_double),
                 ("min_ms", ctypes.c_double), ("max_ms", ctypes.c_double), ("median_ms", ctypes.c_double)]
@@ -76,7 +96,7 @@ class KernelStat(ctypes.Structure):
 
 _lib = None
 _lock = threading.Lock()
-_P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _SZ, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
 
 
 def lib():
@@ -130,6 +150,16 @@ def lib():
             L.lora_moe_experts_workspace_bytes.argtypes = [_I, _I, _I, _I]
             L.lora_moe_experts.argtypes = [_I, _P, _P, _P, ctypes.POINTER(MoeWeightsDesc), _I, _I, _I, _I, _I, _P, _P,
                                            _SZ, _P]
+            L.lora_moe_route_scored.argtypes = [_P, _P, _I, _I, _I, _I, ctypes.POINTER(RouteScoresDesc), _P, _P, _P,
+                                                _SZ, _P]
+            cache = ctypes.POINTER(KvCacheDesc)
+            L.lora_kv_append.argtypes = [cache, _P, _P, _L, _L, _P, _I, _P]
+            L.lora_attn_decode_workspace_bytes.argtypes = [_I] * 6
+            L.lora_attn_decode_workspace_bytes.restype = _SZ
+            L.lora_attn_decode.argtypes = [cache, _P, _L, _I, _P, _L, _I, _P, _I, _F, _I, _P, _P, _P, _SZ, _P]
+            L.lora_sample_workspace_bytes.argtypes = [_I, _I]
+            L.lora_sample_workspace_bytes.restype = _SZ
+            L.lora_sample.argtypes = [_I, _P, _L, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
             L.lora_profile_begin.argtypes = [_I]
             L.lora_profile_end.argtypes = [ctypes.POINTER(KernelStat), _I, ctypes.POINTER(_I)]
             L.lora_status_string.argtypes = [_I]
@@ -768,6 +798,174 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate,
     _call(dev, L.lora_moe_experts, "lora_moe_experts", LORA_MX4 if mx4 else LORA_BF16, x.data_ptr(), ids.data_ptr(),
           weights.data_ptr(), ctypes.byref(d), T, H, I, E, k, y.data_ptr(), ws, nb)
     return y
+
+
+_SCORE = {"softmax": LORA_SCORE_SOFTMAX, "sigmoid": LORA_SCORE_SIGMOID}
+
+
+def moe_route_scored(x: torch.Tensor, router: torch.Tensor, k: int, score: str = "sigmoid",
+                     bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1, group_best: int = 2,
+                     renorm: bool = True, scale: float = 1.0):
+    """lora_moe_route_scored: (ids int32 [T, k], weights fp32 [T, k]) of the k
+    experts with the largest score + bias (fp32 [E]) among those of the
+    ``top_groups`` of ``groups`` groups with the largest sum of their
+    ``group_best`` largest; the weights are ``scale`` times the scores, divided
+    by their sum with ``renorm``. ``score``: "sigmoid" or "softmax" of the
+    logits x router^T. x [T, H], router [E, H], bf16."""
+    code = _SCORE.get(score)
+    if code is None:
+        raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
+    _dev_tensor(x, torch.bfloat16, "x")
+    _dev_tensor(router, torch.bfloat16, "router")
+    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and router {tuple(router.shape)} must be [T, H] and [E, H]")
+    (T, H), E, k = x.shape, router.shape[0], int(k)
+    dev = _same_device(("x", x), ("router", router))
+    if bias is not None:
+        _dev_tensor(bias, torch.float32, "bias", (E,))
+        _same_device(("x", x), ("bias", bias))
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    L = lib()
+    n = L.lora_moe_route_workspace_bytes(T, H, E)
+    keep, ws, nb = _space(None, n, dev) if n else (None, None, 0)
+    d = RouteScoresDesc(bias.data_ptr() if bias is not None else None, code, int(groups), int(top_groups),
+                        int(group_best), int(bool(renorm)), float(scale))
+    _call(dev, L.lora_moe_route_scored, "lora_moe_route_scored", x.data_ptr(), router.data_ptr(), T, H, E, k,
+          ctypes.byref(d), ids.data_ptr(), weights.data_ptr(), ws, nb)
+    return ids, weights
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCacheDesc:
+    """The descriptor of a cache given as tensors [pages, page_rows, kv_heads,
+    dim] of any strides (the last dimension contiguous, alike for both)."""
+    dt = getattr(k_cache, "dtype", None)
+    f8 = dt == torch.float8_e4m3fn
+    if not f8 and dt != torch.bfloat16:
+        raise ValueError(f"k_cache must be bf16 or float8_e4m3fn, got {dt}")
+    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype != dt:
+        raise ValueError("k_cache and v_cache must be device tensors of one type")
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides:
+        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} must be [pages, page_rows, "
+                         "kv_heads, dim] with the same strides")
+    pages, rows, heads, dim = shape
+    if pages < 1 or rows < 1 or heads < 1 or dim < 1 or strides[3] != 1:
+        raise ValueError("a cache needs a page, a row and a head, and a contiguous last dimension")
+    # a dimension of one element has any stride
+    s = [n if m > 1 else dim for n, m in zip(strides, shape)]
+    extent = 0
+    for st, m in sorted((n, m) for n, m in zip(s, shape[:3]) if m > 1):
+        if st < max(extent, dim):
+            raise ValueError(f"rows of the cache overlap (shape {tuple(shape)}, strides {tuple(strides)})")
+        extent = st * m
+    if not f8:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to an 8-bit cache")
+        return KvCacheDesc(k_cache.data_ptr(), v_cache.data_ptr(), None, None, s[0], s[1], s[2], LORA_BF16, pages,
+                           rows, heads, dim)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _dev_tensor(t, torch.float32, name, (heads,))
+        _same_device(("k_cache", k_cache), (name, t))
+    return KvCacheDesc(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), s[0], s[1],
+                       s[2], LORA_F8, pages, rows, heads, dim)
+
+
+def _head_rows(t, name: str, heads: int, dim: int) -> int:
+    """The stride between tokens of bf16 rows [tokens, heads, dim] whose heads
+    are contiguous (a view of merged q/k/v rows is)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 device tensor")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (tokens, {heads}, {dim})")
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return st[0] if shape[0] > 1 else heads * dim
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, rows: torch.Tensor,
+              k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None) -> None:
+    """lora_kv_append: cache row rows[t] (page * page_rows + row in the page,
+    int64; -1 stores nothing) takes k[t] and v[t]. k, v [T, kv_heads, dim]
+    bf16, views of merged rows included; k_cache, v_cache [pages, page_rows,
+    kv_heads, dim] in bf16, or float8_e4m3fn with an fp32 scale per head."""
+    d = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    sk, sv = _head_rows(k, "k", d.kv_heads, d.dim), _head_rows(v, "v", d.kv_heads, d.dim)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
+    _dev_tensor(rows, torch.int64, "rows", (T,))
+    dev = _same_device(("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("rows", rows))
+    _call(dev, lib().lora_kv_append, "lora_kv_append", ctypes.byref(d), k.data_ptr(), v.data_ptr(), sk, sv,
+          rows.data_ptr(), T)
+
+
+def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                lengths: torch.Tensor, scale: float | None = None, window: int = 0,
+                k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, lse: bool = False, workspace: torch.Tensor | None = None):
+    """lora_attn_decode: attention of one new token a request, q [B, heads,
+    dim] bf16, over its first lengths[b] (int32) positions in the paged cache,
+    or the last ``window`` of them; table [B, width] int32 names a request's
+    pages in order. ``scale`` defaults to dim ** -0.5. Returns out [B, heads,
+    dim] bf16, with ``lse`` also the fp32 [B, heads] log of the sum of exp."""
+    d = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (B, heads, dim)")
+    B, heads, dim = q.shape
+    sq = _head_rows(q, "q", heads, d.dim)
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
+            table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be int32 of shape ({B}, width) with contiguous rows")
+    width = table.shape[1]
+    _dev_tensor(lengths, torch.int32, "lengths", (B,))
+    if out is None:
+        out = torch.empty((B, heads, dim), dtype=torch.bfloat16, device=q.device)
+    _dev_tensor(out, torch.bfloat16, "out", (B, heads, dim))
+    sums = torch.empty((B, heads), dtype=torch.float32, device=q.device) if lse else None
+    dev = _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("table", table), ("lengths", lengths),
+                       ("out", out))
+    L = lib()
+    n = L.lora_attn_decode_workspace_bytes(B, heads, d.kv_heads, d.dim, width, d.page_rows)
+    keep, ws, nb = _space(workspace, n, dev) if n else (None, None, 0)
+    _call(dev, L.lora_attn_decode, "lora_attn_decode", ctypes.byref(d), q.data_ptr(), sq, heads, table.data_ptr(),
+          table.stride(0) if B > 1 else width, width, lengths.data_ptr(), B,
+          d.dim ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(),
+          sums.data_ptr() if lse else None, ws, nb)
+    return (out, sums) if lse else out
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+           top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None):
+    """lora_sample: (ids int32 [B], probs fp32 [B]) of the tokens drawn from
+    logits [B, V] (bf16 or fp32, rows of any stride) with the random numbers u
+    (fp64 [B], in [0, 1)); temperature, top_p, min_p (fp32 [B]) and top_k
+    (int32 [B]) are each request's own, None for temperature 1 and no filter.
+    A temperature of 0 takes the likeliest token; -1 where a row has none."""
+    dt = _DTYPE_NAME.get(getattr(logits, "dtype", None))
+    if dt is None or not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a bf16 or fp32 device tensor [B, V]")
+    B, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a request must be contiguous")
+    _dev_tensor(u, torch.float64, "u", (B,))
+    dev = _same_device(("logits", logits), ("u", u))
+    own = []
+    for name, t, kind in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                          ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is not None:
+            _dev_tensor(t, kind, name, (B,))
+            _same_device(("logits", logits), (name, t))
+        own.append(t.data_ptr() if t is not None else None)
+    ids = torch.empty(B, dtype=torch.int32, device=dev)
+    probs = torch.empty(B, dtype=torch.float32, device=dev)
+    L = lib()
+    n = L.lora_sample_workspace_bytes(B, V)
+    keep, ws, nb = _space(None, n, dev) if n else (None, None, 0)
+    _call(dev, L.lora_sample, "lora_sample", _CODE[dt], logits.data_ptr(), logits.stride(0) if B > 1 else V, B, V,
+          u.data_ptr(), *own, ids.data_ptr(), probs.data_ptr(), ws, nb)
+    return ids, probs
 
 
 def profile_begin(max_records: int = 100000):
