@@ -632,7 +632,9 @@ int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride
  *   w_i >= min_p (the first token in the order always stays); then ids[b] =
  *   the lowest index at which the running sum, by index, of the kept w passes
  *   u times their whole sum, and probs[b] = its w over that sum.
- *   logits   dev LORA_F32 or LORA_BF16 [B][V], requests `stride` elements apart
+ *   logits   dev LORA_F32 or LORA_BF16 [B][V], requests `stride` elements apart,
+ *            beginning anywhere (the aligned 16-byte pieces of memory that hold a
+ *            row are read whole)
  *   u        dev double [B] in [0, 1)
  *   temperature, top_p, min_p dev float [B], top_k dev int32 [B]: each request's
  *            own, or null for temperature 1 and no filter. A temperature that is

@@ -5,14 +5,20 @@
 //   first token, by index, at which the running sum of the kept w passes u
 //   times their whole sum.
 //
-// Nothing is sorted. A first kernel reads every logit once and leaves, for each
-// tile of 512, the largest and (where the request draws from all of them, or
-// by top_p alone) the sum of the weights. A second one, a workgroup a request,
-// finds the border of each prefix: a histogram over the tokens that can lie
-// above it says in which bin it is, the tokens of that bin are ranked. Tiles
-// whose largest logit is below the border found so far are not read again, so
-// that a few likely tokens cost a few tiles. The draw goes by the tiles' sums
-// and then through one tile.
+// Nothing is sorted. The border of a prefix is found by a histogram of the
+// tokens over bins of equal width below the largest logit, and by ranking the
+// tokens of the one bin that holds it; the draw goes by sums over tiles of 512
+// tokens and then through one tile. Every pass over whole rows is spread over
+// the chip, tile by tile, whatever the batch:
+//   tops     the largest logit of each tile
+//   bins     the histogram (top_p, or a top_k past the number of tiles); rows
+//            without those filters: the tiles' sums at once
+//   gather   the tokens of the border's bin
+//   border   a workgroup a request: ranks that bin. A top_k up to the number of
+//            tiles is done here from first to last: its tokens are in tiles
+//            whose largest logit is among the k largest, few of which are read
+//   sums     the tiles' sums of the kept tokens
+//   draw     a workgroup a request
 //
 // Weights are 64-bit exponentials held as whole numbers of 2^-shift, so that
 // sums do not depend on the order in which they are made: equal inputs give
@@ -24,20 +30,15 @@
 
 namespace lora {
 
-// Keys: 0 for NaN, otherwise rising with the value; -0 counts as 0.
-constexpr uint32_t kKeyNone = 0x007fffffu;  // of -infinity: never drawn, like NaN
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);
-    return v != v ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k); }
-
-// 2^y for y <= 0 (0 below -1000): y = n + r, |r| <= 1/2, and the series of
-// 2^r = e^(r ln 2) to the eleventh power (the next term is under 1e-14).
+// ------------------------------------------------------------------ weights --
+// 2^y for y <= 0 (2^-1000 below that, and for NaN): y = n + r, |r| <= 1/2, and
+// the series of 2^r = e^(r ln 2) to the eleventh power (the next term is under
+// 1e-14).
 __device__ __forceinline__ double exp2_neg(double y) {
     constexpr double L = 0.693147180559945309417;
     constexpr double c2 = L * L / 2, c3 = c2 * L / 3, c4 = c3 * L / 4, c5 = c4 * L / 5, c6 = c5 * L / 6,
                      c7 = c6 * L / 7, c8 = c7 * L / 8, c9 = c8 * L / 9, c10 = c9 * L / 10, c11 = c10 * L / 11;
+    y = __builtin_fmax(y, -1000.0);
     const double n = __builtin_rint(y), r = y - n;
     double s = c11;
     s = __builtin_fma(s, r, c10);
@@ -51,25 +52,45 @@ __device__ __forceinline__ double exp2_neg(double y) {
     s = __builtin_fma(s, r, c2);
     s = __builtin_fma(s, r, L);
     s = __builtin_fma(s, r, 1.0);
-    return y < -1000.0 ? 0.0 : __builtin_ldexp(s, (int)n);
+    return __builtin_ldexp(s, (int)n);
 }
 
-// Weights relative to a largest logit: w of a key, and w as a whole number of
-// 2^-shift: w + 2^(52 - shift) has 2^-shift as the last place of its mantissa.
+// The weights of a request: w of a logit (-infinity and NaN: nothing that
+// counts), and w as a whole number of 2^-shift: w + 2^(52 - shift) has 2^-shift
+// as the last place of its mantissa.
 struct Weights {
-    float top;
-    double per;  // log2(e) / temperature
+    float top;    // the largest logit
+    double per;   // log2(e) / temperature
     double lift;  // 2^(52 - shift)
-    __device__ __forceinline__ double of(uint32_t key) const {
-        const float v = of_key(key);
-        const double w = exp2_neg(((double)v - (double)top) * per);
-        // among infinite logits all weigh the same; -infinity and NaN nothing
-        return key <= kKeyNone ? 0.0 : top == INFINITY ? (v == top ? 1.0 : 0.0) : w;
+    __device__ __forceinline__ double of(float v) const {
+        if (top == INFINITY) return v == top ? 1.0 : 0.0;  // among infinite logits all weigh the same
+        return exp2_neg(((double)v - (double)top) * per);
     }
     __device__ __forceinline__ uint64_t whole(double w) const {
         return __builtin_bit_cast(uint64_t, w + lift) - __builtin_bit_cast(uint64_t, lift);
     }
 };
+
+// A token as a number that rises with its place in the order: its logit's bits
+// made to rise with the value (-0 counts as 0), then its index inverted.
+__device__ __forceinline__ uint64_t token(float v, int i) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return (uint64_t)(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ float token_logit(uint64_t t) {
+    const uint32_t k = (uint32_t)(t >> 32);
+    return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ int token_index(uint64_t t) { return (int)~(uint32_t)t; }
+
+// A prefix of a request's tokens in the order: all logits above v, and of the
+// equal ones those at an index up to `last`. NaN is in none.
+struct Prefix {
+    float v;
+    int last;
+    __device__ __forceinline__ bool holds(float x, int i) const { return x > v || (x == v && i <= last); }
+};
+__device__ __forceinline__ Prefix up_to(uint64_t t) { return Prefix{token_logit(t), token_index(t)}; }
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int src) {
     return (uint64_t)(uint32_t)__shfl((int)(uint32_t)v, src) |
@@ -84,11 +105,6 @@ __device__ __forceinline__ uint64_t wave_total(uint64_t v) {
     for (int o = 32; o > 0; o >>= 1) v += shfl64_xor(v, o);
     return v;
 }
-__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-    return v;
-}
 __device__ __forceinline__ uint64_t wave_scan(uint64_t v, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -98,11 +114,10 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v, int lane) {  // inclus
     return v;
 }
 
-// ------------------------------------------------------------------- tiles --
+// -------------------------------------------------------------------- rows --
 // A request's logits in tiles of 512, 8 a lane, read in the 16-byte pieces that
 // hold them: rows may begin anywhere, values before and behind the row count
-// as NaN. Element e of a lane's piece i of tile t has index
-// 512 t + 512 i / pieces + 16 / size lane + e - skip.
+// as NaN. Value j of a lane of tile t has index(t, j, lane).
 constexpr int kTile = 512;
 template <bool BF16>
 struct Row {
@@ -126,99 +141,137 @@ struct Row {
     __device__ __forceinline__ int index(int t, int j, int lane) const {
         return t * kTile + (j / E) * 64 * E + lane * E + j % E - skip;
     }
-    __device__ __forceinline__ uint32_t key(const u32x4 (&x)[P], int t, int j, int lane) const {
-        const int i = index(t, j, lane);
-        float v;
-        if constexpr (BF16) {
-            const uint32_t w = x[0][j >> 1];
-            v = __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
-        } else {
-            v = __uint_as_float(x[j >> 2][j & 3]);
+    __device__ __forceinline__ void values(float (&v)[8], const u32x4 (&x)[P], int t, int lane) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (BF16) {
+                const uint32_t w = x[0][j >> 1];
+                v[j] = __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+            } else {
+                v[j] = __uint_as_float(x[j >> 2][j & 3]);
+            }
         }
-        return (uint32_t)i < (uint32_t)V ? key_of(v) : 0u;
+        if (t == 0 || t == tiles - 1) {  // uniform
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if ((uint32_t)index(t, j, lane) >= (uint32_t)V) v[j] = __builtin_nanf("");
+        }
     }
 };
 
-// Tiles of a row at most, whatever its alignment; the workspace's layout.
+// Tiles of a row at most, whatever its alignment.
 __host__ __device__ inline int sample_tiles(int V) { return (V + 7 + kTile - 1) / kTile; }
 
-// What a request asks for.
-struct Ask {
-    bool greedy;
-    int k;        // 0: all
-    float p;      // 1: all
-    float least;  // 0: all
-};
-__device__ __forceinline__ Ask ask_of(const SampleArgs& a, int b, float* t) {
-    Ask r;
-    *t = a.temperature ? a.temperature[b] : 1.f;
-    const int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f;
-    r.greedy = !(*t > 0.f);
-    r.k = k > 0 && k < a.V ? k : 0;
-    r.p = p < 1.f ? p : 1.f;
-    r.least = least > 0.f ? least : 0.f;
-    return r;
-}
-// Whether the tiles' sums over all tokens are used: the draw is from all of
-// them, or top_p is the first filter.
-__device__ __forceinline__ bool needs_sums(const Ask& r) {
-    return !r.greedy && r.k == 0 && (r.p < 1.f || r.least == 0.f);
-}
+constexpr int kBins = 2048;
+constexpr int kList = 1024;  // tokens of a border's bin that are ranked
 
-// The largest key of each tile, and the sum of its weights relative to that. A
-// wave takes 4 tiles.
-template <bool BF16>
-__global__ __launch_bounds__(256) void sample_tiles_kernel(SampleArgs a, double lift, uint32_t* __restrict__ tops,
-                                                           uint64_t* __restrict__ sums) {
-    const int lane = threadIdx.x & 63, b = blockIdx.y, nt = sample_tiles(a.V);
-    const int t0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 4;
-    const Row<BF16> row(a, b);
-    u32x4 x[4][Row<BF16>::P];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) row.load(x[j], t0 + j, true, lane);
-    float t;
-    const Ask ask = ask_of(a, b, &t);
-    const bool sum = needs_sums(ask);
-    issue_fence();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (t0 + j >= nt) break;  // uniform
-        uint32_t k[8], top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            k[e] = row.key(x[j], t0 + j, e, lane);
-            top = max(top, k[e]);
-        }
-        top = wave_top(top);
-        uint64_t s = 0;
-        if (sum) {
-            const Weights W{of_key(top), 1.4426950408889634 / (double)t, lift};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += W.whole(W.of(k[e]));
-            s = wave_total(s);
-        }
-        if (lane == 0) {
-            tops[(int64_t)b * nt + t0 + j] = top;
-            sums[(int64_t)b * nt + t0 + j] = s;
+// What the kernels leave for one another, in the workspace.
+struct RowState {
+    uint32_t count;  // tokens gathered
+    Prefix kept;
+};
+struct SampleSpace {
+    SampleArgs a;
+    double lift;
+    int nt, per_wg;    // tiles of a row, of a workgroup
+    uint64_t* bins;    // [B][kBins]
+    uint64_t* sums;    // [B][nt]
+    uint64_t* list;    // [B][kList]
+    float* tops;       // [B][nt]
+    RowState* state;   // [B]
+};
+
+// What a request asks for, and the way it takes.
+enum Way { kDone, kSums, kFew, kCount, kMass };
+struct Ask {
+    float t, p, least;  // p 1, least 0: all
+    int k;              // 0: all
+    Way way;
+    float top;   // the largest logit, the least of the tiles' largest
+    float under;
+    int live;    // tiles with a token that can be drawn
+};
+template <int NT>
+struct BlockLds {
+    uint64_t part[NT / 64];
+    float part_top[NT / 64], part_under[NT / 64];
+    int part_live[NT / 64];
+    uint64_t found[4];
+    uint32_t count;
+};
+template <int NT>
+__device__ __forceinline__ Ask ask_of(const SampleSpace& s, int b, BlockLds<NT>& L) {
+    const SampleArgs& a = s.a;
+    Ask r;
+    float top = -INFINITY, under = INFINITY;
+    int live = 0;
+    for (int i = threadIdx.x; i < s.nt; i += NT) {
+        const float v = s.tops[(int64_t)b * s.nt + i];
+        if (v > -INFINITY) {
+            top = fmaxf(top, v);
+            under = fminf(under, v);
+            ++live;
         }
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor(top, o));
+        under = fminf(under, __shfl_xor(under, o));
+        live += __shfl_xor(live, o);
+    }
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        L.part_top[wave] = top;
+        L.part_under[wave] = under;
+        L.part_live[wave] = live;
+    }
+    __syncthreads();
+    r.top = top, r.under = under, r.live = 0;
+    for (int w = 0; w < NT / 64; ++w) {
+        r.top = fmaxf(r.top, L.part_top[w]);
+        r.under = fminf(r.under, L.part_under[w]);
+        r.live += L.part_live[w];
+    }
+    r.top = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(r.top)));
+    r.t = a.temperature ? a.temperature[b] : 1.f;
+    const int k = a.top_k ? a.top_k[b] : 0;
+    const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f;
+    r.k = k > 0 && k < a.V ? k : 0;
+    r.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
+    r.least = least > 0.f ? least : 0.f;
+    r.way = !(r.t > 0.f) || r.top == -INFINITY ? kDone
+            : r.k                              ? (r.k <= r.live ? kFew : kCount)
+            : r.p < 1.f                        ? kMass
+                                               : kSums;
+    return r;
+}
+__device__ __forceinline__ Weights weights_of(const SampleSpace& s, const Ask& r) {
+    return Weights{r.top, 1.4426950408889634 / (double)r.t, s.lift};
 }
 
-// ------------------------------------------------------------------ borders --
-constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
-constexpr int kBins = 2048, kList = kSampleThreads;
-struct SampleLds {
-    uint64_t bin[kBins];
-    uint64_t list[kList];   // tokens of the border's bin: key, then ~index
-    uint64_t part[kSampleWaves];
-    uint64_t found[4];
-    uint32_t count, low, high;
+// Bins of equal width below the largest logit, monotone in it (each step of
+// the arithmetic is); what lies past the last, and NaN, is in the last.
+struct Scale {
+    float top, per;
+    __device__ __forceinline__ int bin(float v) const { return (int)fminf((top - v) * per, (float)(kBins - 1)); }
 };
-__device__ __forceinline__ uint64_t token(uint32_t key, int i) { return (uint64_t)key << 32 | (uint32_t)~i; }
+// Of top_k: down to the lowest tile's largest logit, which the border is not
+// below where there are at least k tiles, otherwise twice as far.
+__device__ __forceinline__ Scale scale_of_count(const Ask& r) {
+    const float reach = (r.top - r.under) * (r.k <= r.live ? 1.f : 2.f);
+    return Scale{r.top, r.top == INFINITY ? 0.f : fminf((kBins - 2) / fmaxf(reach, 1e-30f), 1e30f)};
+}
+// Of top_p: the tokens behind the border weigh at least 1 - p of the whole,
+// which is at least 1, with the border's own; fewer than V of them, so that one
+// weighs at least (1 - p) / V.
+__device__ __forceinline__ Scale scale_of_mass(const Ask& r, const Weights& W, int V) {
+    const double reach = log2((double)V / (1.0 - (double)r.p)) + 1.0;
+    return Scale{r.top, r.top == INFINITY ? 0.f : (float)fmin(W.per * (kBins - 2) / reach, 1e30)};
+}
 
 // the sum of a value over the threads before this one; *all: over all of them
-__device__ __forceinline__ uint64_t block_before(uint64_t v, SampleLds& L, uint64_t* all) {
+template <int NT>
+__device__ __forceinline__ uint64_t block_before(uint64_t v, BlockLds<NT>& L, uint64_t* all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t in = wave_scan(v, lane);
     __syncthreads();
@@ -226,7 +279,7 @@ __device__ __forceinline__ uint64_t block_before(uint64_t v, SampleLds& L, uint6
     __syncthreads();
     uint64_t before = in - v, sum = 0;
 #pragma unroll
-    for (int w = 0; w < kSampleWaves; ++w) {
+    for (int w = 0; w < NT / 64; ++w) {
         const uint64_t x = L.part[w];
         if (w < wave) before += x;
         sum += x;
@@ -234,95 +287,238 @@ __device__ __forceinline__ uint64_t block_before(uint64_t v, SampleLds& L, uint6
     *all = sum;
     return before;
 }
+// The bin at which above + the sum of the bins from the first on reaches what
+// is wanted (found[0], kBins if none), and the sum before it (found[1]).
+// want_of(sum of all bins) says what that is, and is its result.
+template <int NT, class Want>
+__device__ __forceinline__ uint64_t find_bin(const uint64_t* bins, uint64_t above, Want want_of, BlockLds<NT>& L) {
+    constexpr int N = kBins / NT;
+    uint64_t x[N], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += x[i] = bins[N * threadIdx.x + i];
+    uint64_t before = above + block_before<NT>(sum, L, &all);
+    const uint64_t want = want_of(all);
+    if (threadIdx.x == 0) L.found[0] = kBins;
+    __syncthreads();
+    if (before < want && want <= before + sum) {
+        int i = 0;
+#pragma unroll
+        for (int j = 0; j < N - 1; ++j)
+            if (i == j && before + x[j] < want) {
+                before += x[j];
+                ++i;
+            }
+        L.found[0] = N * threadIdx.x + i;
+        L.found[1] = before;
+    }
+    __syncthreads();
+    return want;
+}
+// at least one unit: the first token stays
+__device__ __forceinline__ uint64_t share(float p, uint64_t all) {
+    const double x = __builtin_ceil((double)p * (double)all);
+    return x < 1.0 ? 1 : x >= (double)all ? all : (uint64_t)x;
+}
+__device__ __forceinline__ void add(uint64_t* at, uint64_t v) {
+    atomicAdd((unsigned long long*)at, (unsigned long long)v);
+}
 
-// A prefix of a request's tokens in falling order: all up to token `last`
-// (tokens compare as their order: a larger key, then a lower index).
-typedef uint64_t Prefix;
-__device__ __forceinline__ bool holds(Prefix p, uint64_t t) { return t >= p; }
-constexpr Prefix kAll = (uint64_t)(kKeyNone + 1) << 32;  // every token but NaN and -infinity
-
-// Whole rows, tile by tile: f(tile, logits) for the tiles that on(tile) says, 4
-// of a wave's in flight.
-template <bool BF16, class On, class F>
-__device__ __forceinline__ void each_tile(const Row<BF16>& row, On on, F f) {
+// Tiles [t0, t1) of a row, a wave 4 at a time: f(tile, values) for those that
+// on(tile) says.
+template <int NT, bool BF16, class On, class F>
+__device__ __forceinline__ void each_tile(const Row<BF16>& row, int t0, int t1, On on, F f) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int t0 = wave * 4; t0 < row.tiles; t0 += kSampleWaves * 4) {
+    t1 = min(t1, row.tiles);
+    for (int t = t0 + wave * 4; t < t1; t += NT / 64 * 4) {
         u32x4 x[4][Row<BF16>::P];
         uint32_t is = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (t0 + j < row.tiles && __builtin_amdgcn_readfirstlane(on(t0 + j))) is |= 1u << j;
+            if (t + j < t1 && __builtin_amdgcn_readfirstlane(on(t + j))) is |= 1u << j;
         if (!is) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) row.load(x[j], t0 + j, (is >> j) & 1, lane);
+        for (int j = 0; j < 4; ++j) row.load(x[j], t + j, (is >> j) & 1, lane);
         issue_fence();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if ((is >> j) & 1) f(t0 + j, x[j]);
+            if ((is >> j) & 1) {
+                float v[8];
+                row.values(v, x[j], t + j, lane);
+                f(t + j, v);
+            }
     }
 }
 
-// The bin at which the sum of the bins from the first on reaches `want`
-// (found[0], kBins if none), and the sum before it (found[1]). *all: the whole.
-__device__ __forceinline__ void find_bin(uint64_t above, uint64_t want, SampleLds& L, uint64_t* all) {
-    const int tid = threadIdx.x;
-    const uint64_t x = L.bin[2 * tid], y = L.bin[2 * tid + 1];
-    const uint64_t before = above + block_before(x + y, L, all);
-    if (tid == 0) L.found[0] = kBins;
-    __syncthreads();
-    if (before < want && want <= before + x + y) {
-        const bool first = want <= before + x;
-        L.found[0] = first ? 2 * tid : 2 * tid + 1;
-        L.found[1] = first ? before : before + x;
-    }
-    __syncthreads();
-}
-__device__ __forceinline__ void clear_bins(SampleLds& L) {
-    L.bin[threadIdx.x] = 0;
-    L.bin[threadIdx.x + kSampleThreads] = 0;
-    __syncthreads();
-}
+// ------------------------------------------------------------- row by tiles --
+constexpr int kTilesNT = 256;
 
-// The n-th (from 1) of the tokens with this key that `in` holds; there are at
-// least n.
 template <bool BF16>
-__device__ __forceinline__ Prefix nth_equal(const Row<BF16>& row, const uint32_t* tops, uint32_t key, uint64_t n,
-                                            SampleLds& L) {
-    const int lane = threadIdx.x & 63;
-    // tokens of each stretch of tiles, a bin each; then the tile by tile and lane by lane walk of one wave
-    int sh = 0;
-    while (((row.tiles - 1) >> sh) >= kBins) ++sh;
-    clear_bins(L);
-    auto same = [&](int t) { return tops[t] >= key; };
-    each_tile(row, same, [&](int t, const u32x4(&x)[Row<BF16>::P]) {
-        int c = 0;
+__global__ __launch_bounds__(kTilesNT) void sample_tops_kernel(SampleSpace s) {
+    const int b = blockIdx.y, lane = threadIdx.x & 63, t0 = blockIdx.x * s.per_wg;
+    const Row<BF16> row(s.a, b);
+    each_tile<kTilesNT>(
+        row, t0, t0 + s.per_wg, [](int) { return true; },
+        [&](int t, const float(&v)[8]) {
+            float m = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c += __popcll(__ballot(row.key(x, t, e, lane) == key));
-        if (lane == 0 && c) atomicAdd((unsigned long long*)&L.bin[t >> sh], (unsigned long long)c);
-    });
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j]);  // of a number and NaN the number
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+            if (lane == 0) s.tops[(int64_t)b * s.nt + t] = m;
+        });
+    // what the others add to
+    for (int i = blockIdx.x * kTilesNT + threadIdx.x; i < kBins; i += gridDim.x * kTilesNT)
+        s.bins[(int64_t)b * kBins + i] = 0;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) s.state[b].count = 0;
+        // the tile that only rows of another alignment have
+        for (int t = row.tiles + threadIdx.x; t < s.nt; t += kTilesNT) s.tops[(int64_t)b * s.nt + t] = -INFINITY;
+    }
+}
+
+// The tiles' sums of the tokens that a prefix and min_p leave.
+template <int NT, bool BF16>
+__device__ __forceinline__ void tile_sums(const SampleSpace& s, const Row<BF16>& row, int b, int t0, int t1,
+                                          const Ask& r, const Weights& W, Prefix kept, uint64_t* sums) {
+    const int lane = threadIdx.x & 63;
+    const float* tops = s.tops + (int64_t)b * s.nt;
+    const double least = (double)r.least;
+    for (int t = t0 + threadIdx.x; t < min(t1, s.nt); t += NT) sums[t] = 0;
     __syncthreads();
-    uint64_t all;
-    find_bin(0, n, L, &all);
-    const int t0 = (int)L.found[0] << sh;
-    uint64_t left = n - L.found[1];
+    each_tile<NT>(
+        row, t0, t1, [&](int t) { return tops[t] >= kept.v && W.of(tops[t]) >= least; },
+        [&](int t, const float(&v)[8]) {
+            uint64_t x = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (kept.holds(v[j], row.index(t, j, lane))) {
+                    const double w = W.of(v[j]);
+                    x += w < least ? 0 : W.whole(w);
+                }
+            x = wave_total(x);
+            if (lane == 0) sums[t] = x;
+        });
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
+    __shared__ uint64_t bins[kBins];
+    __shared__ BlockLds<kTilesNT> L;
+    const int b = blockIdx.y, t0 = blockIdx.x * s.per_wg;
+    const Ask r = ask_of<kTilesNT>(s, b, L);
+    if (r.way == kDone || r.way == kFew) return;
+    const Row<BF16> row(s.a, b);
+    const Weights W = weights_of(s, r);
+    if (r.way == kSums) {
+        tile_sums<kTilesNT>(s, row, b, t0, t0 + s.per_wg, r, W, Prefix{-INFINITY, -1}, s.sums + (int64_t)b * s.nt);
+        return;
+    }
+    const bool mass = r.way == kMass;
+    const Scale S = mass ? scale_of_mass(r, W, s.a.V) : scale_of_count(r);
+    for (int i = threadIdx.x; i < kBins; i += kTilesNT) bins[i] = 0;
+    __syncthreads();
+    if (mass)
+        each_tile<kTilesNT>(
+            row, t0, t0 + s.per_wg, [](int) { return true; },
+            [&](int, const float(&v)[8]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t q = W.whole(W.of(v[j]));
+                    if (q) add(&bins[S.bin(v[j])], q);
+                }
+            });
+    else
+        each_tile<kTilesNT>(
+            row, t0, t0 + s.per_wg, [](int) { return true; },
+            [&](int, const float(&v)[8]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (v[j] > -INFINITY) add(&bins[S.bin(v[j])], 1);
+            });
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kTilesNT)
+        if (bins[i]) add(&s.bins[(int64_t)b * kBins + i], bins[i]);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kTilesNT) void sample_gather_kernel(SampleSpace s) {
+    __shared__ BlockLds<kTilesNT> L;
+    const int b = blockIdx.y, lane = threadIdx.x & 63, t0 = blockIdx.x * s.per_wg;
+    const Ask r = ask_of<kTilesNT>(s, b, L);
+    if (r.way != kCount && r.way != kMass) return;
+    const Row<BF16> row(s.a, b);
+    const Weights W = weights_of(s, r);
+    const bool mass = r.way == kMass;
+    const Scale S = mass ? scale_of_mass(r, W, s.a.V) : scale_of_count(r);
+    find_bin<kTilesNT>(
+        s.bins + (int64_t)b * kBins, 0, [&](uint64_t all) { return mass ? share(r.p, all) : (uint64_t)r.k; }, L);
+    const int bin = (int)L.found[0];
+    if (bin == kBins) return;
+    RowState* st = s.state + b;
+    const float* tops = s.tops + (int64_t)b * s.nt;
+    each_tile<kTilesNT>(
+        row, t0, t0 + s.per_wg, [&](int t) { return S.bin(tops[t]) <= bin; },
+        [&](int t, const float(&v)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool is = v[j] > -INFINITY && S.bin(v[j]) == bin;
+                const uint64_t m = __ballot(is);
+                if (!m) continue;
+                uint32_t at = 0;
+                if (lane == __builtin_ctzll(m)) at = atomicAdd(&st->count, (uint32_t)__popcll(m));
+                at = __shfl((int)at, __builtin_ctzll(m)) + __popcll(m & ((1ull << lane) - 1));
+                if (is && at < kList) s.list[(int64_t)b * kList + at] = token(v[j], row.index(t, j, lane));
+            }
+        });
+}
+
+// ------------------------------------------------------------------ borders --
+constexpr int kBorderNT = 1024;
+struct BorderLds {
+    uint64_t bins[kBins];
+    uint64_t list[kList];
+    BlockLds<kBorderNT> block;
+};
+
+// The n-th (from 1) of the tokens with this logit; there are at least n.
+template <bool BF16>
+__device__ __forceinline__ Prefix nth_equal(const Row<BF16>& row, const float* tops, float v0, uint64_t n,
+                                            BorderLds& L) {
+    const int lane = threadIdx.x & 63;
+    int sh = 0;  // tiles of a bin, then of one wave's walk
+    while (((row.tiles - 1) >> sh) >= kBins) ++sh;
+    for (int i = threadIdx.x; i < kBins; i += kBorderNT) L.bins[i] = 0;
+    __syncthreads();
+    each_tile<kBorderNT>(
+        row, 0, row.tiles, [&](int t) { return tops[t] >= v0; },
+        [&](int t, const float(&v)[8]) {
+            int c = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c += __popcll(__ballot(v[j] == v0));
+            if (lane == 0 && c) add(&L.bins[t >> sh], c);
+        });
+    __syncthreads();
+    find_bin<kBorderNT>(L.bins, 0, [&](uint64_t) { return n; }, L.block);
+    const int t0 = (int)L.block.found[0] << sh;
+    uint64_t left = n - L.block.found[1];
     if (threadIdx.x < 64)
         for (int t = t0; t < min(t0 + (1 << sh), row.tiles); ++t) {
             u32x4 x[Row<BF16>::P];
+            float v[8];
             row.load(x, t, true, lane);
+            row.values(v, x, t, lane);
             uint64_t done = 0;
 #pragma unroll
             for (int i = 0; i < Row<BF16>::P; ++i) {
                 uint32_t c = 0;
 #pragma unroll
-                for (int e = 0; e < Row<BF16>::E; ++e) c += row.key(x, t, i * Row<BF16>::E + e, lane) == key;
+                for (int e = 0; e < Row<BF16>::E; ++e) c += v[i * Row<BF16>::E + e] == v0;
                 const uint64_t in = wave_scan(c, lane);
-                if (left > done + in - c && left <= done + in) {
-                    uint64_t at = done + in - c;
+                uint64_t at = done + in - c;
 #pragma unroll
-                    for (int e = 0; e < Row<BF16>::E; ++e) {
-                        const int j = i * Row<BF16>::E + e;
-                        if (row.key(x, t, j, lane) == key && ++at == left) L.found[2] = token(key, row.index(t, j, lane));
-                    }
+                for (int e = 0; e < Row<BF16>::E; ++e) {
+                    const int j = i * Row<BF16>::E + e;
+                    if (v[j] == v0 && ++at == left) L.block.found[2] = row.index(t, j, lane);
                 }
                 done += shfl64(in, 63);
             }
@@ -330,335 +526,264 @@ __device__ __forceinline__ Prefix nth_equal(const Row<BF16>& row, const uint32_t
             left -= done;
         }
     __syncthreads();
-    return L.found[2];
+    const Prefix p{v0, (int)L.block.found[2]};
+    __syncthreads();
+    return p;
 }
 
-// Where a token falls: bins of equal width below the largest logit, monotone
-// in the key (each step of the arithmetic is).
-struct Scale {
-    float top, per;
-    __device__ __forceinline__ int bin(uint32_t key) const {
-        return (int)fminf((top - of_key(key)) * per, (float)(kBins - 1));
-    }
-};
-
-// The shortest prefix of `in` with at least `want` of its tokens (MASS false)
-// or of its whole weights (MASS true); in where even that has less. `last` is
-// a bin that no border lies behind; tokens behind it are not looked at.
-template <bool BF16, bool MASS>
-__device__ __forceinline__ Prefix border(const Row<BF16>& row, const uint32_t* tops, const Weights& W, Prefix in,
-                                         uint64_t want, double part, const Scale& S, int last, SampleLds& L) {
+// Of the n <= kList tokens in L.list: the one at which above + the sum of the
+// weights from the largest token on reaches `want`. The tokens' range is cut by
+// histograms until few are left, which are ranked.
+template <class Weight>
+__device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want, Weight weight, BorderLds& L) {
     const int tid = threadIdx.x, lane = tid & 63;
-    const uint32_t floor_key = (uint32_t)(in >> 32);
-    auto weight = [&](uint32_t k) -> uint64_t { return MASS ? W.whole(W.of(k)) : 1; };
-    clear_bins(L);
-    each_tile(
-        row, [&](int t) { return tops[t] >= floor_key && S.bin(tops[t]) <= last; },
-        [&](int t, const u32x4(&x)[Row<BF16>::P]) {
+    const uint64_t mine = tid < n ? L.list[tid] : 0;
+    const uint64_t w = tid < n ? weight(token_logit(mine)) : 0;
+    uint64_t low = 0, high = ~0ull;  // the border is in [low, high]
+    for (;;) {
+        const bool in = tid < n && mine >= low && mine <= high;
+        // how many are left, and their range
+        uint64_t lo = in ? mine : ~0ull, hi = in ? mine : 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t k = row.key(x, t, e, lane);
-                if (holds(in, token(k, row.index(t, e, lane)))) {
-                    const int n = S.bin(k);
-                    if (n <= last) atomicAdd((unsigned long long*)&L.bin[n], (unsigned long long)weight(k));
-                }
-            }
-        });
-    __syncthreads();
-    uint64_t all;
-    if (MASS && want == 0) {  // the share of what the bins hold
-        block_before(L.bin[2 * tid] + L.bin[2 * tid + 1], L, &all);
-        const double x = __builtin_ceil(part * (double)all);
-        want = x < 1.0 ? 1 : x >= (double)all ? all : (uint64_t)x;
-    }
-    find_bin(0, want, L, &all);
-    const int b = (int)L.found[0];
-    if (b == kBins) return in;
-    uint64_t above = L.found[1];
-    // the tokens of the border's bin
-    if (tid == 0) {
-        L.count = 0;
-        L.low = ~0u;
-        L.high = 0;
-    }
-    __syncthreads();
-    each_tile(
-        row, [&](int t) { return tops[t] >= floor_key && S.bin(tops[t]) <= b; },
-        [&](int t, const u32x4(&x)[Row<BF16>::P]) {
-            uint32_t low = ~0u, high = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t k = row.key(x, t, e, lane);
-                const uint64_t tk = token(k, row.index(t, e, lane));
-                if (holds(in, tk) && S.bin(k) == b) {
-                    const uint32_t at = atomicAdd(&L.count, 1u);
-                    if (at < kList) L.list[at] = tk;
-                    low = min(low, k);
-                    high = max(high, k);
-                }
-            }
-            if (high) {
-                atomicMin(&L.low, low);
-                atomicMax(&L.high, high);
-            }
-        });
-    __syncthreads();
-    const int n = (int)L.count;
-    uint32_t low = L.low, high = L.high;
-    if (low != high && n <= kList) {
-        // ranks: what of the bin comes before each token
-        const uint64_t mine = tid < n ? L.list[tid] : 0;
-        const uint64_t w = tid < n ? weight((uint32_t)(mine >> 32)) : 0;
+        for (int o = 32; o > 0; o >>= 1) {
+            lo = min(lo, shfl64_xor(lo, o));
+            hi = max(hi, shfl64_xor(hi, o));
+        }
+        const uint64_t m = __ballot(in);
+        for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
         __syncthreads();
-        if (MASS) L.bin[tid] = w;
-        __syncthreads();
-        if (tid < n) {
-            uint64_t before = above;
-            for (int j = 0; j < n; ++j)
-                if (L.list[j] > mine) before += MASS ? L.bin[j] : 1;
-            if (before < want && want <= before + w) L.found[2] = mine;
+        if (tid == 0) {
+            L.block.found[0] = ~0ull;
+            L.block.found[1] = 0;
+            L.block.count = 0;
         }
         __syncthreads();
-        return L.found[2];
-    }
-    while (low != high) {  // more tokens than the list holds: by the digits of their keys
-        int sh = 0;
-        while ((high - low) >> sh >= kBins) ++sh;
-        clear_bins(L);
-        each_tile(
-            row, [&](int t) { return tops[t] >= low; },
-            [&](int t, const u32x4(&x)[Row<BF16>::P]) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t k = row.key(x, t, e, lane);
-                    if (k >= low && k <= high && holds(in, token(k, row.index(t, e, lane))))
-                        atomicAdd((unsigned long long*)&L.bin[(high - k) >> sh], (unsigned long long)weight(k));
-                }
-            });
+        if (lane == 0 && m) {
+            atomicMin((unsigned long long*)&L.block.found[0], (unsigned long long)lo);
+            atomicMax((unsigned long long*)&L.block.found[1], (unsigned long long)hi);
+            atomicAdd(&L.block.count, (uint32_t)__popcll(m));
+        }
         __syncthreads();
-        find_bin(above, want, L, &all);
-        const uint32_t at = (uint32_t)L.found[0];
-        above = L.found[1];
-        const uint32_t top = high - (at << sh);
-        low = max(low, top - ((1u << sh) - 1));
+        low = L.block.found[0];
+        high = L.block.found[1];
+        if (L.block.count <= 64) break;
+        const int sh = max(0, 64 - __builtin_clzll(high - low) - 11);  // (high - low) >> sh < 2048
+        if (in) add(&L.bins[(high - mine) >> sh], w);
+        __syncthreads();
+        find_bin<kBorderNT>(L.bins, above, [&](uint64_t) { return want; }, L.block);
+        const uint64_t at = L.block.found[0];
+        above = L.block.found[1];
+        const uint64_t top = high - (at << sh), width = (1ull << sh) - 1;
+        low = top - low > width ? top - width : low;
         high = top;
         __syncthreads();
     }
-    const uint64_t one = weight(high);
-    return nth_equal(row, tops, high, (want - above + one - 1) / one, L);
+    // at most 64: compacted, then each against the others
+    __syncthreads();
+    if (tid == 0) L.block.count = 0;
+    __syncthreads();
+    if (tid < n && mine >= low && mine <= high) {
+        const uint32_t at = atomicAdd(&L.block.count, 1u);
+        L.list[at] = mine;
+        L.bins[at] = w;
+    }
+    __syncthreads();
+    const int c = (int)L.block.count;
+    if (tid < c) {
+        const uint64_t me = L.list[tid], mw = L.bins[tid];
+        uint64_t before = above;
+        for (int j = 0; j < c; ++j)
+            if (L.list[j] > me) before += L.bins[j];
+        if (before < want && want <= before + mw) L.block.found[2] = me;
+    }
+    __syncthreads();
+    const Prefix p = up_to(L.block.found[2]);
+    __syncthreads();
+    return p;
 }
 
-// One workgroup a request, over what the first kernel left.
-template <bool BF16>
-__global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a, double lift,
-                                                                const uint32_t* __restrict__ all_tops,
-                                                                const uint64_t* __restrict__ all_sums) {
-    extern __shared__ uint64_t tile_sum[];  // [tiles], then the largest keys
-    __shared__ SampleLds L;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x, nt = sample_tiles(a.V);
-    uint32_t* tops = reinterpret_cast<uint32_t*>(tile_sum + nt);
-    const Row<BF16> row(a, b);
-    float t;
-    const Ask ask = ask_of(a, b, &t);
-    // the largest key, and the first tile that has it
-    uint64_t best = 0;
-    uint32_t least_top = ~0u;  // of the tiles with a token that can be drawn
-    int live = 0;              // their number
-    for (int i = tid; i < nt; i += kSampleThreads) {
-        const uint32_t k = all_tops[(int64_t)b * nt + i];
-        tops[i] = k;
-        best = max(best, token(k, i));
-        if (k > kKeyNone) {
-            least_top = min(least_top, k);
-            ++live;
-        }
-    }
+// The shortest prefix of `in` with at least k of its tokens (MASS false) or p
+// of its weights (MASS true), by this workgroup alone; `in` where it has less.
+// No border lies behind bin `last`; tokens behind it are not looked at (of MASS
+// it is the last there is).
+template <bool BF16, bool MASS>
+__device__ __forceinline__ Prefix border(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r,
+                                         const Weights& W, Prefix in, const Scale& S, int last, BorderLds& L) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const float* tops = s.tops + (int64_t)b * s.nt;
+    auto weight = [&](float v) -> uint64_t { return MASS ? W.whole(W.of(v)) : 1; };
+    for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
+    __syncthreads();
+    each_tile<kBorderNT>(
+        row, 0, row.tiles, [&](int t) { return tops[t] >= in.v && S.bin(tops[t]) <= last; },
+        [&](int t, const float(&v)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (in.holds(v[j], row.index(t, j, lane))) {
+                    const int n = S.bin(v[j]);
+                    if (n <= last) add(&L.bins[n], weight(v[j]));
+                }
+        });
+    __syncthreads();
+    const uint64_t want = find_bin<kBorderNT>(
+        L.bins, 0, [&](uint64_t all) { return MASS ? share(r.p, all) : (uint64_t)r.k; }, L.block);
+    const int bin = (int)L.block.found[0];
+    uint64_t above = L.block.found[1];
+    __syncthreads();
+    if (bin == kBins) return in;
+    // the tokens of the border's bin
+    float low = INFINITY, high = -INFINITY;
+    if (tid == 0) L.block.count = 0;
+    __syncthreads();
+    each_tile<kBorderNT>(
+        row, 0, row.tiles, [&](int t) { return tops[t] >= in.v && S.bin(tops[t]) <= bin; },
+        [&](int t, const float(&v)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (in.holds(v[j], row.index(t, j, lane)) && S.bin(v[j]) == bin) {
+                    const uint32_t at = atomicAdd(&L.block.count, 1u);
+                    if (at < kList) L.list[at] = token(v[j], row.index(t, j, lane));
+                    low = fminf(low, v[j]);
+                    high = fmaxf(high, v[j]);
+                }
+        });
+    __syncthreads();
+    const int n = (int)L.block.count;
+    __syncthreads();
+    if (n <= kList) return rank_list(n, above, want, weight, L);
+    // more tokens than the list holds: by the digits of their logits' order
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
-        best = max(best, shfl64_xor(best, o));
-        least_top = min(least_top, (uint32_t)__shfl_xor((int)least_top, o));
-        live += __shfl_xor(live, o);
+        low = fminf(low, __shfl_xor(low, o));
+        high = fmaxf(high, __shfl_xor(high, o));
     }
     if (lane == 0) {
-        L.part[wave] = best;
-        L.list[wave] = (uint64_t)least_top << 32 | (uint32_t)live;
+        L.block.part_top[tid >> 6] = high;
+        L.block.part_under[tid >> 6] = low;
     }
     __syncthreads();
-    live = 0;
-    least_top = ~0u;
-    for (int w = 0; w < kSampleWaves; ++w) {
-        best = max(best, L.part[w]);
-        least_top = min(least_top, (uint32_t)(L.list[w] >> 32));
-        live += (int)(uint32_t)L.list[w];
+    for (int w = 0; w < kBorderNT / 64; ++w) {
+        low = fminf(low, L.block.part_under[w]);
+        high = fmaxf(high, L.block.part_top[w]);
     }
-    const uint32_t top = (uint32_t)(best >> 32);
-    if (top <= kKeyNone) {
-        if (tid == 0) {
-            a.ids[b] = -1;
-            a.probs[b] = 0.f;
-        }
-        return;
-    }
-    // the first token in the order
-    if (tid < 64) {
-        const int at = (int)~(uint32_t)best;
-        u32x4 x[Row<BF16>::P];
-        row.load(x, at, true, lane);
-        uint64_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, token(row.key(x, at, e, lane), row.index(at, e, lane)));
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) m = max(m, shfl64_xor(m, o));
-        if (lane == 0) L.found[3] = m;
-    }
-    __syncthreads();
-    const uint64_t first = L.found[3];
-    if (ask.greedy) {
-        if (tid == 0) {
-            a.ids[b] = (int)~(uint32_t)first;
-            a.probs[b] = 1.f;
-        }
-        return;
-    }
-    const Weights W{of_key(top), 1.4426950408889634 / (double)t, lift};
-    Prefix kept = kAll;
-    uint64_t all;
-    bool filtered = false;
-    if (ask.k) {
-        // at least k tokens lie at or above the k-th largest tile's top: bins down
-        // to the lowest one hold the border then, otherwise twice as far
-        const bool sure = ask.k <= live;
-        const float reach = (W.top - of_key(least_top)) * (sure ? 1.f : 2.f);
-        const Scale S{W.top, W.top == INFINITY ? 0.f : fminf((kBins - 2) / fmaxf(reach, 1e-30f), 1e30f)};
-        int last = kBins - 1;
-        if (sure) {
-            clear_bins(L);
-            for (int i = tid; i < nt; i += kSampleThreads)
-                if (tops[i] > kKeyNone) atomicAdd((unsigned long long*)&L.bin[S.bin(tops[i])], 1ull);
-            __syncthreads();
-            find_bin(0, (uint64_t)ask.k, L, &all);
-            last = min((int)L.found[0], kBins - 1);
-            __syncthreads();
-        }
-        kept = border<BF16, false>(row, tops, W, kept, (uint64_t)ask.k, 0.0, S, last, L);
-        filtered = true;
-    }
-    if (ask.p < 1.f) {
-        // the tokens behind the border weigh at most (1 - p) of the whole, which is
-        // at least 1, and are fewer than V: the first of them weighs at least ...
-        const double reach = log2((double)a.V / (1.0 - (double)fmaxf(ask.p, 0.f))) + 1.0;
-        const double per = W.per * (kBins - 2) / reach;
-        const Scale S{W.top, W.top == INFINITY ? 0.f : (float)fmin(per, 1e30)};
-        uint64_t want = 0;
-        int last = kBins - 1;
-        if (!filtered) {
-            // where the largest tokens of the tiles alone make up the share, the border is among them
-            clear_bins(L);
-            uint64_t sum = 0;
-            for (int i = tid; i < nt; i += kSampleThreads) {
-                const double f = W.of(tops[i]);
-                sum += (uint64_t)((double)all_sums[(int64_t)b * nt + i] * f);
-                if (tops[i] > kKeyNone)
-                    atomicAdd((unsigned long long*)&L.bin[S.bin(tops[i])], (unsigned long long)W.whole(f));
-            }
-            block_before(sum, L, &all);
-            const double x = __builtin_ceil((double)ask.p * (double)all);
-            const uint64_t share = x < 1.0 ? 1 : (uint64_t)x;
-            uint64_t of_tops;
-            find_bin(0, share, L, &of_tops);
-            if ((int)L.found[0] < kBins) {
-                last = (int)L.found[0];
-                want = share;
-            }
-            __syncthreads();
-        }
-        kept = border<BF16, true>(row, tops, W, kept, want, (double)ask.p, S, last, L);
-        filtered = true;
-    }
-    // the sums of the kept tokens, tile by tile
-    const double least = (double)ask.least;
-    auto weight = [&](uint32_t k, int i) -> uint64_t {
-        const uint64_t tk = token(k, i);
-        if (!holds(kept, tk)) return 0;
-        const double w = W.of(k);
-        return w < least && tk != first ? 0 : W.whole(w);
-    };
-    const bool whole = !filtered && ask.least == 0.f;
-    const uint32_t floor_key = (uint32_t)(kept >> 32);
-    __syncthreads();
-    if (whole) {
-        for (int i = tid; i < nt; i += kSampleThreads)
-            tile_sum[i] = (uint64_t)((double)all_sums[(int64_t)b * nt + i] * W.of(tops[i]));
-    } else {
-        for (int i = tid; i < nt; i += kSampleThreads) tile_sum[i] = 0;
+    auto key = [](float v) { return (uint32_t)(token(v, 0) >> 32); };
+    uint32_t k0 = key(low), k1 = key(high);
+    while (k0 != k1) {
+        int sh = 0;
+        while (((k1 - k0) >> sh) >= kBins) ++sh;
+        for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
         __syncthreads();
-        each_tile(
-            row, [&](int i) { return tops[i] >= floor_key && (W.of(tops[i]) >= least || tops[i] == top); },
-            [&](int i, const u32x4(&x)[Row<BF16>::P]) {
-                uint64_t s = 0;
+        each_tile<kBorderNT>(
+            row, 0, row.tiles, [&](int t) { return key(tops[t]) >= k0; },
+            [&](int t, const float(&v)[8]) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += weight(row.key(x, i, e, lane), row.index(i, e, lane));
-                s = wave_total(s);
-                if (lane == 0) tile_sum[i] = s;
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t k = key(v[j]);
+                    if (k >= k0 && k <= k1 && in.holds(v[j], row.index(t, j, lane)))
+                        add(&L.bins[(k1 - k) >> sh], weight(v[j]));
+                }
             });
+        __syncthreads();
+        find_bin<kBorderNT>(L.bins, above, [&](uint64_t) { return want; }, L.block);
+        const uint32_t top = k1 - ((uint32_t)L.block.found[0] << sh), width = (1u << sh) - 1;
+        above = L.block.found[1];
+        k0 = top - k0 > width ? top - width : k0;
+        k1 = top;
+        __syncthreads();
     }
+    const float v0 = token_logit((uint64_t)k1 << 32);
+    const uint64_t one = weight(v0);
+    return nth_equal(row, tops, v0, (want - above + one - 1) / one, L);
+}
+
+// The first token in the order: of the largest logits the one at the lowest
+// index.
+template <int NT, bool BF16>
+__device__ __forceinline__ void first_token(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r,
+                                            BlockLds<NT>& L) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const float* tops = s.tops + (int64_t)b * s.nt;
+    if (tid == 0) L.found[0] = ~0ull;
     __syncthreads();
-    // the tile with the border of u: a stretch of tiles a thread
-    const int per = (nt + kSampleThreads - 1) / kSampleThreads, t0 = min(tid * per, nt), t1 = min(t0 + per, nt);
-    uint64_t mine = 0;
-    for (int i = t0; i < t1; ++i) mine += tile_sum[i];
-    uint64_t before = block_before(mine, L, &all);
-    const double u = fmin(fmax(a.u[b], 0.0), 1.0);
+    for (int i = tid; i < s.nt; i += NT)
+        if (tops[i] == r.top) atomicMin((unsigned long long*)&L.found[0], (unsigned long long)i);
+    __syncthreads();
+    if (tid >= 64) return;
+    const int t = (int)L.found[0];
+    u32x4 x[Row<BF16>::P];
+    float v[8];
+    row.load(x, t, true, lane);
+    row.values(v, x, t, lane);
+    int first = 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (v[j] == r.top) first = min(first, row.index(t, j, lane));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) first = min(first, __shfl_xor(first, o));
+    if (lane == 0) {
+        s.a.ids[b] = first;
+        s.a.probs[b] = 1.f;
+    }
+}
+
+// The draw, from the tiles' sums.
+template <int NT, bool BF16>
+__device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r, const Weights& W,
+                                     Prefix kept, const uint64_t* sums, BlockLds<NT>& L) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const double least = (double)r.least;
+    const int per = (s.nt + NT - 1) / NT, t0 = min(tid * per, s.nt), t1 = min(t0 + per, s.nt);
+    uint64_t mine = 0, all;
+    for (int i = t0; i < t1; ++i) mine += sums[i];
+    uint64_t before = block_before<NT>(mine, L, &all);
+    if (all == 0) {  // min_p above every weight
+        first_token<NT>(s, row, b, r, L);
+        return;
+    }
+    const double u = fmin(fmax(s.a.u[b], 0.0), 1.0);
     // the first running sum above u * all: a whole number, so above its floor, and at most all
     const uint64_t pass = min((uint64_t)(u * (double)all), all - 1);
     if (before <= pass && pass < before + mine) {
         int i = t0;
-        for (; before + tile_sum[i] <= pass; ++i) before += tile_sum[i];
+        for (; before + sums[i] <= pass; ++i) before += sums[i];
         L.found[0] = i;
         L.found[1] = pass - before;
     }
     __syncthreads();
     if (tid >= 64) return;
-    const int at = (int)L.found[0];
+    const int t = (int)L.found[0];
     const uint64_t left = L.found[1];
     u32x4 x[Row<BF16>::P];
-    row.load(x, at, true, lane);
-    // sums of all tokens are relative to the tile's own largest: f takes them to
-    // the row's as tile_sum has it, a step that keeps their order
-    const double f = whole ? W.of(tops[at]) : 1.0;
-    const Weights T{of_key(tops[at]), W.per, lift};
+    float v[8];
+    row.load(x, t, true, lane);
+    row.values(v, x, t, lane);
     uint64_t run = 0;
 #pragma unroll
     for (int i = 0; i < Row<BF16>::P; ++i) {
-        uint64_t w[Row<BF16>::E], s = 0;
+        uint64_t w[Row<BF16>::E], sum = 0;
 #pragma unroll
         for (int e = 0; e < Row<BF16>::E; ++e) {
             const int j = i * Row<BF16>::E + e;
-            const uint32_t k = row.key(x, at, j, lane);
-            w[e] = whole ? T.whole(T.of(k)) : weight(k, row.index(at, j, lane));
-            s += w[e];
+            const double wj = W.of(v[j]);
+            w[e] = kept.holds(v[j], row.index(t, j, lane)) && !(wj < least) ? W.whole(wj) : 0;
+            sum += w[e];
         }
-        const uint64_t in = run + wave_scan(s, lane);
-        auto passes = [&](uint64_t v) { return (whole ? (uint64_t)((double)v * f) : v) > left; };
-        const uint64_t m = __ballot(passes(in));
+        const uint64_t in = run + wave_scan(sum, lane);
+        const uint64_t m = __ballot(in > left);
         if (m) {
             if (lane == __builtin_ctzll(m)) {
-                uint64_t v = in - s;
-                int e = 0;
+                uint64_t at = in - sum;
+                bool done = false;
 #pragma unroll
-                for (int n = 0; n < Row<BF16>::E; ++n) {
-                    if (!passes(v + w[n]) && e == n) {
-                        v += w[n];
-                        e = n + 1;
+                for (int e = 0; e < Row<BF16>::E; ++e) {
+                    at += w[e];
+                    if (!done && at > left) {
+                        const int j = i * Row<BF16>::E + e;
+                        s.a.ids[b] = row.index(t, j, lane);
+                        s.a.probs[b] = (float)(W.of(v[j]) * (4503599627370496.0 / s.lift) / (double)all);
+                        done = true;
                     }
                 }
-#pragma unroll
-                for (int n = 0; n < Row<BF16>::E; ++n)
-                    if (n == e) {
-                        const int j = i * Row<BF16>::E + n;
-                        a.ids[b] = row.index(at, j, lane);
-                        a.probs[b] = (float)(W.of(row.key(x, at, j, lane)) * (4503599627370496.0 / lift) / (double)all);
-                    }
             }
             return;
         }
@@ -666,27 +791,137 @@ __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a, do
     }
 }
 
+template <bool BF16>
+__global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s) {
+    __shared__ BorderLds L;
+    const int tid = threadIdx.x, b = blockIdx.x;
+    const Ask r = ask_of<kBorderNT>(s, b, L.block);
+    if (r.way == kSums || r.way == kDone) return;
+    const Row<BF16> row(s.a, b);
+    const Weights W = weights_of(s, r);
+    const float* tops = s.tops + (int64_t)b * s.nt;
+    const Prefix every{-INFINITY, -1};
+    Prefix kept = every;
+    if (r.way == kFew) {
+        // at least k tokens lie at or above the k-th largest of the tiles' tops
+        const Scale S = scale_of_count(r);
+        for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < s.nt; i += kBorderNT)
+            if (tops[i] > -INFINITY) add(&L.bins[S.bin(tops[i])], 1);
+        __syncthreads();
+        find_bin<kBorderNT>(L.bins, 0, [&](uint64_t) { return (uint64_t)r.k; }, L.block);
+        const int last = min((int)L.block.found[0], kBins - 1);
+        __syncthreads();
+        kept = border<BF16, false>(s, row, b, r, W, every, S, last, L);
+    } else {
+        const bool mass = r.way == kMass;
+        const uint64_t want = find_bin<kBorderNT>(
+            s.bins + (int64_t)b * kBins, 0, [&](uint64_t all) { return mass ? share(r.p, all) : (uint64_t)r.k; },
+            L.block);
+        const int bin = (int)L.block.found[0], n = (int)s.state[b].count;
+        const uint64_t above = L.block.found[1];
+        __syncthreads();
+        if (bin < kBins && n <= kList) {
+            if (tid < n) L.list[tid] = s.list[(int64_t)b * kList + tid];
+            __syncthreads();
+            kept = rank_list(n, above, want, [&](float v) -> uint64_t { return mass ? W.whole(W.of(v)) : 1; }, L);
+        } else if (bin < kBins) {
+            kept = mass ? border<BF16, true>(s, row, b, r, W, every, scale_of_mass(r, W, s.a.V), kBins - 1, L)
+                        : border<BF16, false>(s, row, b, r, W, every, scale_of_count(r), kBins - 1, L);
+        }
+    }
+    if (r.k && r.p < 1.f)
+        kept = border<BF16, true>(s, row, b, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L);
+    if (r.way != kFew) {
+        if (tid == 0) s.state[b].kept = kept;
+        return;
+    }
+    uint64_t* sums = s.sums + (int64_t)b * s.nt;
+    tile_sums<kBorderNT>(s, row, b, 0, s.nt, r, W, kept, sums);
+    __syncthreads();
+    draw<kBorderNT>(s, row, b, r, W, kept, sums, L.block);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kTilesNT) void sample_sums_kernel(SampleSpace s) {
+    __shared__ BlockLds<kTilesNT> L;
+    const int b = blockIdx.y, t0 = blockIdx.x * s.per_wg;
+    const Ask r = ask_of<kTilesNT>(s, b, L);
+    if (r.way != kCount && r.way != kMass) return;
+    const Row<BF16> row(s.a, b);
+    tile_sums<kTilesNT>(s, row, b, t0, t0 + s.per_wg, r, weights_of(s, r), s.state[b].kept,
+                        s.sums + (int64_t)b * s.nt);
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kTilesNT) void sample_draw_kernel(SampleSpace s) {
+    __shared__ BlockLds<kTilesNT> L;
+    const int b = blockIdx.x;
+    const Ask r = ask_of<kTilesNT>(s, b, L);
+    if (r.way == kFew) return;  // drawn
+    if (r.top == -INFINITY) {
+        if (threadIdx.x == 0) {
+            s.a.ids[b] = -1;
+            s.a.probs[b] = 0.f;
+        }
+        return;
+    }
+    const Row<BF16> row(s.a, b);
+    if (r.way == kDone) {
+        first_token<kTilesNT>(s, row, b, r, L);
+        return;
+    }
+    const Prefix kept = r.way == kSums ? Prefix{-INFINITY, -1} : s.state[b].kept;
+    draw<kTilesNT>(s, row, b, r, weights_of(s, r), kept, s.sums + (int64_t)b * s.nt, L);
+}
+
 // -------------------------------------------------------------------- host --
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t sample_workspace(int B, int V) {
-    const size_t n = (size_t)B * sample_tiles(V);
-    return align256(n * sizeof(uint64_t)) + align256(n * sizeof(uint32_t));
+    const size_t tiles = (size_t)B * sample_tiles(V);
+    return align256((size_t)B * kBins * 8) + align256(tiles * 8) + align256((size_t)B * kList * 8) +
+           align256(tiles * 4) + align256((size_t)B * sizeof(RowState));
+}
+
+template <bool BF16>
+static hipError_t run(const SampleSpace& s, hipStream_t st, StageTimer* tm) {
+    const dim3 tiles((s.nt + s.per_wg - 1) / s.per_wg, s.a.B), rows(s.a.B);
+    const bool filters = s.a.top_k || s.a.top_p;
+    hipError_t e = launch(tm, "sample_tops", sample_tops_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
+    if (e == hipSuccess) e = launch(tm, "sample_bins", sample_bins_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
+    if (e == hipSuccess && filters) {
+        e = launch(tm, "sample_gather", sample_gather_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
+        if (e == hipSuccess) e = launch(tm, "sample_border", sample_border_kernel<BF16>, rows, dim3(kBorderNT), st, s);
+        if (e == hipSuccess) e = launch(tm, "sample_sums", sample_sums_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
+    }
+    if (e == hipSuccess) e = launch(tm, "sample_draw", sample_draw_kernel<BF16>, rows, dim3(kTilesNT), st, s);
+    return e;
 }
 
 hipError_t sample(const SampleArgs& a, bool bf16, hipStream_t st, StageTimer* tm) {
+    SampleSpace s{};
+    s.a = a;
     // V weights of at most 2^shift add up to less than 2^63
     int bits = 0;
     while ((int64_t)1 << bits < a.V) ++bits;
-    const double lift = (double)((int64_t)1 << (52 - std::min(46, 62 - bits)));
-    const int nt = sample_tiles(a.V);
-    uint64_t* sums = static_cast<uint64_t*>(a.workspace);
-    uint32_t* tops = reinterpret_cast<uint32_t*>(static_cast<char*>(a.workspace) + align256((size_t)a.B * nt * 8));
-    hipError_t e = launch(tm, "sample_tiles", bf16 ? sample_tiles_kernel<true> : sample_tiles_kernel<false>,
-                          dim3((nt + 15) / 16, a.B), dim3(256), st, a, lift, tops, sums);
-    if (e != hipSuccess) return e;
-    return launch_shm(tm, "sample", bf16 ? sample_kernel<true> : sample_kernel<false>, dim3(a.B), dim3(kSampleThreads),
-                      nt * 12, st, a, lift, (const uint32_t*)tops, (const uint64_t*)sums);
+    s.lift = (double)((int64_t)1 << (52 - std::min(46, 62 - bits)));
+    s.nt = sample_tiles(a.V);
+    // 4 tiles a wave, more where that gives far more workgroups than the chip holds
+    s.per_wg = 16 * (int)std::max<int64_t>(1, (int64_t)a.B * s.nt / (16 * 2048));
+    const size_t tiles = (size_t)a.B * s.nt;
+    char* ws = static_cast<char*>(a.workspace);
+    s.bins = reinterpret_cast<uint64_t*>(ws);
+    ws += align256((size_t)a.B * kBins * 8);
+    s.sums = reinterpret_cast<uint64_t*>(ws);
+    ws += align256(tiles * 8);
+    s.list = reinterpret_cast<uint64_t*>(ws);
+    ws += align256((size_t)a.B * kList * 8);
+    s.tops = reinterpret_cast<float*>(ws);
+    ws += align256(tiles * 4);
+    s.state = reinterpret_cast<RowState*>(ws);
+    return bf16 ? run<true>(s, st, tm) : run<false>(s, st, tm);
 }
 
 }  // namespace lora
