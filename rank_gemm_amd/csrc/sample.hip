@@ -5,7 +5,7 @@
 //   first token, by index, at which the running sum of the kept w passes u
 //   times their whole sum.
 //
-// Nothing is sorted. The border of a prefix is found by a histogram of the
+// No row is sorted. The border of a prefix is found by a histogram of the
 // tokens over bins of equal width below the largest logit, and by ranking the
 // tokens of the one bin that holds it; the draw goes by sums over tiles of 512
 // tokens and then through one tile. Every pass over whole rows is spread over
@@ -13,10 +13,13 @@
 //   tops     the largest logit of each tile
 //   bins     the histogram (top_p, or a top_k past the number of tiles); rows
 //            without those filters: the tiles' sums at once
-//   gather   the tokens of the border's bin
-//   border   a workgroup a request: ranks that bin. A top_k up to the number of
-//            tiles is done here from first to last: its tokens are in tiles
-//            whose largest logit is among the k largest, few of which are read
+//   gather   the tokens of the border's bin; where there are few down to there
+//            for sure, all of them
+//   border   a workgroup a request: ranks that bin; or, where all tokens that
+//            can be kept are at hand, sorts them and draws. A top_k up to the
+//            number of tiles is done here from first to last: its tokens are in
+//            tiles whose largest logit is among the k largest, few of which are
+//            read
 //   sums     the tiles' sums of the kept tokens
 //   draw     a workgroup a request
 //
@@ -168,6 +171,7 @@ constexpr int kList = 1024;  // tokens of a border's bin that are ranked
 // What the kernels leave for one another, in the workspace.
 struct RowState {
     uint32_t count;  // tokens gathered
+    int drawn;       // the border kernel did it
     Prefix kept;
 };
 struct SampleSpace {
@@ -314,6 +318,15 @@ __device__ __forceinline__ uint64_t find_bin(const uint64_t* bins, uint64_t abov
     __syncthreads();
     return want;
 }
+// What a draw from sums of `all` looks for: the first running sum above u all,
+// a whole number, so above its floor, and at most all.
+__device__ __forceinline__ uint64_t draw_at(const SampleSpace& s, int b, uint64_t all) {
+    const double u = fmin(fmax(s.a.u[b], 0.0), 1.0);
+    return min((uint64_t)(u * (double)all), all - 1);
+}
+__device__ __forceinline__ float probability(const SampleSpace& s, const Weights& W, float v, uint64_t all) {
+    return (float)(W.of(v) * (4503599627370496.0 / s.lift) / (double)all);  // 2^52 / lift: units of 1
+}
 // at least one unit: the first token stays
 __device__ __forceinline__ uint64_t share(float p, uint64_t all) {
     const double x = __builtin_ceil((double)p * (double)all);
@@ -321,6 +334,19 @@ __device__ __forceinline__ uint64_t share(float p, uint64_t all) {
 }
 __device__ __forceinline__ void add(uint64_t* at, uint64_t v) {
     atomicAdd((unsigned long long*)at, (unsigned long long)v);
+}
+// To a bin, but what falls in the last one (often most of a row, and adds to
+// one address take turns) is summed by each lane for itself: 61 -> 35 us for
+// 256 rows of 128k with mixed filters. add_rest brings it there in the end.
+__device__ __forceinline__ void add_bin(uint64_t* bins, int n, uint64_t v, uint64_t& rest) {
+    if (n == kBins - 1)
+        rest += v;
+    else
+        add(&bins[n], v);
+}
+__device__ __forceinline__ void add_rest(uint64_t* bins, uint64_t rest) {
+    rest = wave_total(rest);
+    if ((threadIdx.x & 63) == 0 && rest) add(&bins[kBins - 1], rest);
 }
 
 // Tiles [t0, t1) of a row, a wave 4 at a time: f(tile, values) for those that
@@ -370,7 +396,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_tops_kernel(SampleSpace s) {
     for (int i = blockIdx.x * kTilesNT + threadIdx.x; i < kBins; i += gridDim.x * kTilesNT)
         s.bins[(int64_t)b * kBins + i] = 0;
     if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) s.state[b].count = 0;
+        if (threadIdx.x == 0) s.state[b].count = 0, s.state[b].drawn = 0;
         // the tile that only rows of another alignment have
         for (int t = row.tiles + threadIdx.x; t < s.nt; t += kTilesNT) s.tops[(int64_t)b * s.nt + t] = -INFINITY;
     }
@@ -417,6 +443,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
     const Scale S = mass ? scale_of_mass(r, W, s.a.V) : scale_of_count(r);
     for (int i = threadIdx.x; i < kBins; i += kTilesNT) bins[i] = 0;
     __syncthreads();
+    uint64_t rest = 0;
     if (mass)
         each_tile<kTilesNT>(
             row, t0, t0 + s.per_wg, [](int) { return true; },
@@ -424,7 +451,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const uint64_t q = W.whole(W.of(v[j]));
-                    if (q) add(&bins[S.bin(v[j])], q);
+                    if (q) add_bin(bins, S.bin(v[j]), q, rest);
                 }
             });
     else
@@ -433,11 +460,24 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
             [&](int, const float(&v)[8]) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (v[j] > -INFINITY) add(&bins[S.bin(v[j])], 1);
+                    if (v[j] > -INFINITY) add_bin(bins, S.bin(v[j]), 1, rest);
             });
+    add_rest(bins, rest);
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kTilesNT)
         if (bins[i]) add(&s.bins[(int64_t)b * kBins + i], bins[i]);
+}
+
+// Whether the tokens down to the border's bin are at most kList for sure: then
+// all of them are gathered, and the border kernel has what it needs to draw.
+// Of top_p: none of them weighs less than the bin's far edge.
+__device__ __forceinline__ bool short_list(const SampleSpace& s, int b, bool mass, const Weights& W, const Scale& S,
+                                           int bin, uint64_t above) {
+    const uint64_t through = above + s.bins[(int64_t)b * kBins + bin];
+    if (!mass) return through <= kList;
+    if (bin == kBins - 1 || !(S.per > 0.f)) return false;
+    const uint64_t edge = W.whole(W.of(S.top - (float)(bin + 2) / S.per));
+    return edge > 0 && through / edge <= kList;
 }
 
 template <bool BF16>
@@ -454,6 +494,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_gather_kernel(SampleSpace s) 
         s.bins + (int64_t)b * kBins, 0, [&](uint64_t all) { return mass ? share(r.p, all) : (uint64_t)r.k; }, L);
     const int bin = (int)L.found[0];
     if (bin == kBins) return;
+    const bool all = short_list(s, b, mass, W, S, bin, L.found[1]);  // uniform
     RowState* st = s.state + b;
     const float* tops = s.tops + (int64_t)b * s.nt;
     each_tile<kTilesNT>(
@@ -461,7 +502,8 @@ __global__ __launch_bounds__(kTilesNT) void sample_gather_kernel(SampleSpace s) 
         [&](int t, const float(&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool is = v[j] > -INFINITY && S.bin(v[j]) == bin;
+                const int n = S.bin(v[j]);
+                const bool is = v[j] > -INFINITY && (n == bin || (all && n < bin));
                 const uint64_t m = __ballot(is);
                 if (!m) continue;
                 uint32_t at = 0;
@@ -602,6 +644,61 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
     return p;
 }
 
+// The numbers of a workgroup's threads in falling order.
+__device__ __forceinline__ uint64_t sort_falling(uint64_t x, uint64_t* space) {
+    const int tid = threadIdx.x;
+    for (int size = 2; size <= kBorderNT; size *= 2)
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            uint64_t y;
+            if (stride >= 64) {
+                __syncthreads();
+                space[tid] = x;
+                __syncthreads();
+                y = space[tid ^ stride];
+            } else {
+                y = shfl64_xor(x, stride);
+            }
+            // the lower of the two places takes the larger number in a falling run
+            const bool larger = ((tid & stride) == 0) == ((tid & size) == 0);
+            x = larger ? max(x, y) : min(x, y);
+        }
+    __syncthreads();
+    return x;
+}
+
+// From the n <= kList tokens in L.list, which hold every one that can be kept,
+// to the draw: in their order, where the filters are prefixes, then by index.
+// want: what top_p asks for, where it is the first filter.
+__device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const Ask& r, const Weights& W, int n,
+                                            uint64_t want, BorderLds& L) {
+    const int tid = threadIdx.x;
+    const uint64_t me = sort_falling(tid < n ? L.list[tid] : 0, L.bins);
+    const double w = W.of(token_logit(me)), least = (double)r.least;
+    bool kept = me != 0 && (r.k == 0 || tid < r.k);
+    uint64_t q = kept ? W.whole(w) : 0, all;
+    if (r.p < 1.f) {
+        const uint64_t before = block_before<kBorderNT>(q, L.block, &all);
+        kept = kept && before < (r.k ? share(r.p, all) : want);
+    }
+    kept = kept && (!(w < least) || tid == 0);
+    q = kept ? W.whole(w) : 0;
+    __syncthreads();
+    L.list[tid] = me;
+    L.bins[kBorderNT + tid] = q;
+    // the index, inverted, and the place above: 0 where nothing is kept
+    const uint64_t by = sort_falling(kept ? me << 32 | (uint32_t)tid : 0, L.bins);
+    const int from = (int)(uint32_t)by;
+    q = by ? L.bins[kBorderNT + from] : 0;
+    const uint64_t before = block_before<kBorderNT>(q, L.block, &all);
+    const uint64_t pass = draw_at(s, b, all);
+    if (before <= pass && pass < before + q) {
+        const uint64_t t = L.list[from];
+        s.a.ids[b] = token_index(t);
+        s.a.probs[b] = probability(s, W, token_logit(t), all);
+    }
+    if (tid == 0) s.state[b].drawn = 1;
+}
+
 // The shortest prefix of `in` with at least k of its tokens (MASS false) or p
 // of its weights (MASS true), by this workgroup alone; `in` where it has less.
 // No border lies behind bin `last`; tokens behind it are not looked at (of MASS
@@ -614,6 +711,7 @@ __device__ __forceinline__ Prefix border(const SampleSpace& s, const Row<BF16>& 
     auto weight = [&](float v) -> uint64_t { return MASS ? W.whole(W.of(v)) : 1; };
     for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
     __syncthreads();
+    uint64_t rest = 0;
     each_tile<kBorderNT>(
         row, 0, row.tiles, [&](int t) { return tops[t] >= in.v && S.bin(tops[t]) <= last; },
         [&](int t, const float(&v)[8]) {
@@ -621,9 +719,10 @@ __device__ __forceinline__ Prefix border(const SampleSpace& s, const Row<BF16>& 
             for (int j = 0; j < 8; ++j)
                 if (in.holds(v[j], row.index(t, j, lane))) {
                     const int n = S.bin(v[j]);
-                    if (n <= last) add(&L.bins[n], weight(v[j]));
+                    if (n <= last) add_bin(L.bins, n, weight(v[j]), rest);
                 }
         });
+    add_rest(L.bins, rest);
     __syncthreads();
     const uint64_t want = find_bin<kBorderNT>(
         L.bins, 0, [&](uint64_t all) { return MASS ? share(r.p, all) : (uint64_t)r.k; }, L.block);
@@ -740,9 +839,7 @@ __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row,
         first_token<NT>(s, row, b, r, L);
         return;
     }
-    const double u = fmin(fmax(s.a.u[b], 0.0), 1.0);
-    // the first running sum above u * all: a whole number, so above its floor, and at most all
-    const uint64_t pass = min((uint64_t)(u * (double)all), all - 1);
+    const uint64_t pass = draw_at(s, b, all);
     if (before <= pass && pass < before + mine) {
         int i = t0;
         for (; before + sums[i] <= pass; ++i) before += sums[i];
@@ -780,7 +877,7 @@ __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row,
                     if (!done && at > left) {
                         const int j = i * Row<BF16>::E + e;
                         s.a.ids[b] = row.index(t, j, lane);
-                        s.a.probs[b] = (float)(W.of(v[j]) * (4503599627370496.0 / s.lift) / (double)all);
+                        s.a.probs[b] = probability(s, W, v[j], all);
                         done = true;
                     }
                 }
@@ -811,8 +908,25 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
             if (tops[i] > -INFINITY) add(&L.bins[S.bin(tops[i])], 1);
         __syncthreads();
         find_bin<kBorderNT>(L.bins, 0, [&](uint64_t) { return (uint64_t)r.k; }, L.block);
-        const int last = min((int)L.block.found[0], kBins - 1);
+        const int last = min((int)L.block.found[0], kBins - 1), lane = tid & 63;
+        if (tid == 0) L.block.count = 0;
         __syncthreads();
+        each_tile<kBorderNT>(
+            row, 0, row.tiles, [&](int t) { return S.bin(tops[t]) <= last; },
+            [&](int t, const float(&v)[8]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (v[j] > -INFINITY && S.bin(v[j]) <= last) {
+                        const uint32_t at = atomicAdd(&L.block.count, 1u);
+                        if (at < kList) L.list[at] = token(v[j], row.index(t, j, lane));
+                    }
+            });
+        __syncthreads();
+        const int n = (int)L.block.count;
+        if (n <= kList) {
+            finish_list(s, b, r, W, n, 0, L);
+            return;
+        }
         kept = border<BF16, false>(s, row, b, r, W, every, S, last, L);
     } else {
         const bool mass = r.way == kMass;
@@ -821,34 +935,33 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
             L.block);
         const int bin = (int)L.block.found[0], n = (int)s.state[b].count;
         const uint64_t above = L.block.found[1];
+        const Scale S = mass ? scale_of_mass(r, W, s.a.V) : scale_of_count(r);
         __syncthreads();
         if (bin < kBins && n <= kList) {
             if (tid < n) L.list[tid] = s.list[(int64_t)b * kList + tid];
             __syncthreads();
+            if (short_list(s, b, mass, W, S, bin, above)) {
+                finish_list(s, b, r, W, n, want, L);
+                return;
+            }
             kept = rank_list(n, above, want, [&](float v) -> uint64_t { return mass ? W.whole(W.of(v)) : 1; }, L);
         } else if (bin < kBins) {
-            kept = mass ? border<BF16, true>(s, row, b, r, W, every, scale_of_mass(r, W, s.a.V), kBins - 1, L)
-                        : border<BF16, false>(s, row, b, r, W, every, scale_of_count(r), kBins - 1, L);
+            kept = mass ? border<BF16, true>(s, row, b, r, W, every, S, kBins - 1, L)
+                        : border<BF16, false>(s, row, b, r, W, every, S, kBins - 1, L);
         }
     }
     if (r.k && r.p < 1.f)
         kept = border<BF16, true>(s, row, b, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L);
-    if (r.way != kFew) {
-        if (tid == 0) s.state[b].kept = kept;
-        return;
-    }
-    uint64_t* sums = s.sums + (int64_t)b * s.nt;
-    tile_sums<kBorderNT>(s, row, b, 0, s.nt, r, W, kept, sums);
-    __syncthreads();
-    draw<kBorderNT>(s, row, b, r, W, kept, sums, L.block);
+    if (tid == 0) s.state[b].kept = kept;
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(kTilesNT) void sample_sums_kernel(SampleSpace s) {
     __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.y, t0 = blockIdx.x * s.per_wg;
+    if (s.state[b].drawn) return;
     const Ask r = ask_of<kTilesNT>(s, b, L);
-    if (r.way != kCount && r.way != kMass) return;
+    if (r.way == kDone || r.way == kSums) return;
     const Row<BF16> row(s.a, b);
     tile_sums<kTilesNT>(s, row, b, t0, t0 + s.per_wg, r, weights_of(s, r), s.state[b].kept,
                         s.sums + (int64_t)b * s.nt);
@@ -858,8 +971,8 @@ template <bool BF16>
 __global__ __launch_bounds__(kTilesNT) void sample_draw_kernel(SampleSpace s) {
     __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.x;
+    if (s.state[b].drawn) return;
     const Ask r = ask_of<kTilesNT>(s, b, L);
-    if (r.way == kFew) return;  // drawn
     if (r.top == -INFINITY) {
         if (threadIdx.x == 0) {
             s.a.ids[b] = -1;
