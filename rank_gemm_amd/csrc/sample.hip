@@ -173,6 +173,8 @@ struct RowState {
     uint32_t count;  // tokens gathered
     int drawn;       // the border kernel did it
     Prefix kept;
+    int way, live;  // what the bins kernel found (Ask)
+    float top, under;
 };
 struct SampleSpace {
     SampleArgs a;
@@ -203,10 +205,20 @@ struct BlockLds {
     uint64_t found[4];
     uint32_t count;
 };
-template <int NT>
-__device__ __forceinline__ Ask ask_of(const SampleSpace& s, int b, BlockLds<NT>& L) {
-    const SampleArgs& a = s.a;
+__device__ __forceinline__ Ask asked(const SampleArgs& a, int b) {
     Ask r;
+    r.t = a.temperature ? a.temperature[b] : 1.f;
+    const int k = a.top_k ? a.top_k[b] : 0;
+    const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f;
+    r.k = k > 0 && k < a.V ? k : 0;
+    r.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
+    r.least = least > 0.f ? least : 0.f;
+    return r;
+}
+// From the tiles' largest logits, by a workgroup.
+template <int NT>
+__device__ __forceinline__ Ask find_way(const SampleSpace& s, int b, BlockLds<NT>& L) {
+    Ask r = asked(s.a, b);
     float top = -INFINITY, under = INFINITY;
     int live = 0;
     for (int i = threadIdx.x; i < s.nt; i += NT) {
@@ -237,16 +249,17 @@ __device__ __forceinline__ Ask ask_of(const SampleSpace& s, int b, BlockLds<NT>&
         r.live += L.part_live[w];
     }
     r.top = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(r.top)));
-    r.t = a.temperature ? a.temperature[b] : 1.f;
-    const int k = a.top_k ? a.top_k[b] : 0;
-    const float p = a.top_p ? a.top_p[b] : 1.f, least = a.min_p ? a.min_p[b] : 0.f;
-    r.k = k > 0 && k < a.V ? k : 0;
-    r.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
-    r.least = least > 0.f ? least : 0.f;
     r.way = !(r.t > 0.f) || r.top == -INFINITY ? kDone
             : r.k                              ? (r.k <= r.live ? kFew : kCount)
             : r.p < 1.f                        ? kMass
                                                : kSums;
+    return r;
+}
+// As the bins kernel left it.
+__device__ __forceinline__ Ask known_way(const SampleSpace& s, int b) {
+    Ask r = asked(s.a, b);
+    const RowState& st = s.state[b];
+    r.way = (Way)st.way, r.live = st.live, r.top = st.top, r.under = st.under;
     return r;
 }
 __device__ __forceinline__ Weights weights_of(const SampleSpace& s, const Ask& r) {
@@ -350,9 +363,12 @@ __device__ __forceinline__ void add_rest(uint64_t* bins, uint64_t rest) {
 }
 
 // Tiles [t0, t1) of a row, a wave 4 at a time: f(tile, values) for those that
-// on(tile) says.
-template <int NT, bool BF16, class On, class F>
-__device__ __forceinline__ void each_tile(const Row<BF16>& row, int t0, int t1, On on, F f) {
+// on(tile) says, then end(first of the 4, which of them).
+struct Nothing {
+    __device__ __forceinline__ void operator()(int, uint32_t) const {}
+};
+template <int NT, bool BF16, class On, class F, class End = Nothing>
+__device__ __forceinline__ void each_tile(const Row<BF16>& row, int t0, int t1, On on, F f, End end = End()) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     t1 = min(t1, row.tiles);
     for (int t = t0 + wave * 4; t < t1; t += NT / 64 * 4) {
@@ -372,7 +388,39 @@ __device__ __forceinline__ void each_tile(const Row<BF16>& row, int t0, int t1, 
                 row.values(v, x[j], t + j, lane);
                 f(t + j, v);
             }
+        end(t, is);
     }
+}
+// The same for the tiles of a list.
+template <int NT, bool BF16, class F>
+__device__ __forceinline__ void each_listed(const Row<BF16>& row, const int* tiles, int n, F f) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int i = wave * 4; i < n; i += NT / 64 * 4) {
+        u32x4 x[4][Row<BF16>::P];
+        int t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t[j] = __builtin_amdgcn_readfirstlane(tiles[min(i + j, n - 1)]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) row.load(x[j], t[j], true, lane);
+        issue_fence();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < n) {
+                float v[8];
+                row.values(v, x[j], t[j], lane);
+                f(t[j], v);
+            }
+    }
+}
+// The sums of 4 values over a wave: of value i in the lanes 16 i to 16 i + 15.
+__device__ __forceinline__ uint64_t wave_totals(const uint64_t (&x)[4], int lane) {
+    const bool h = lane & 32, q = lane & 16;
+    const uint64_t a = (h ? x[2] : x[0]) + shfl64_xor(h ? x[0] : x[2], 32);
+    const uint64_t b = (h ? x[3] : x[1]) + shfl64_xor(h ? x[1] : x[3], 32);
+    uint64_t v = (q ? b : a) + shfl64_xor(q ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += shfl64_xor(v, o);
+    return v;
 }
 
 // ------------------------------------------------------------- row by tiles --
@@ -411,18 +459,22 @@ __device__ __forceinline__ void tile_sums(const SampleSpace& s, const Row<BF16>&
     const double least = (double)r.least;
     for (int t = t0 + threadIdx.x; t < min(t1, s.nt); t += NT) sums[t] = 0;
     __syncthreads();
+    uint64_t x[4];
     each_tile<NT>(
         row, t0, t1, [&](int t) { return tops[t] >= kept.v && W.of(tops[t]) >= least; },
         [&](int t, const float(&v)[8]) {
-            uint64_t x = 0;
+            uint64_t y = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (kept.holds(v[j], row.index(t, j, lane))) {
                     const double w = W.of(v[j]);
-                    x += w < least ? 0 : W.whole(w);
+                    y += w < least ? 0 : W.whole(w);
                 }
-            x = wave_total(x);
-            if (lane == 0) sums[t] = x;
+            x[t & 3] = y;  // t0 is a multiple of 4: a constant place
+        },
+        [&](int t, uint32_t is) {
+            const uint64_t y = wave_totals(x, lane);
+            if ((lane & 15) == 0 && (is >> (lane >> 4)) & 1) sums[t + (lane >> 4)] = y;
         });
 }
 
@@ -431,7 +483,11 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
     __shared__ uint64_t bins[kBins];
     __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.y, t0 = blockIdx.x * s.per_wg;
-    const Ask r = ask_of<kTilesNT>(s, b, L);
+    const Ask r = find_way<kTilesNT>(s, b, L);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        RowState& st = s.state[b];
+        st.way = r.way, st.live = r.live, st.top = r.top, st.under = r.under;
+    }
     if (r.way == kDone || r.way == kFew) return;
     const Row<BF16> row(s.a, b);
     const Weights W = weights_of(s, r);
@@ -483,8 +539,9 @@ __device__ __forceinline__ bool short_list(const SampleSpace& s, int b, bool mas
 template <bool BF16>
 __global__ __launch_bounds__(kTilesNT) void sample_gather_kernel(SampleSpace s) {
     __shared__ BlockLds<kTilesNT> L;
-    const int b = blockIdx.y, lane = threadIdx.x & 63, t0 = blockIdx.x * s.per_wg;
-    const Ask r = ask_of<kTilesNT>(s, b, L);
+    __shared__ uint64_t list[kList];
+    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 63, t0 = blockIdx.x * s.per_wg;
+    const Ask r = known_way(s, b);
     if (r.way != kCount && r.way != kMass) return;
     const Row<BF16> row(s.a, b);
     const Weights W = weights_of(s, r);
@@ -495,23 +552,29 @@ __global__ __launch_bounds__(kTilesNT) void sample_gather_kernel(SampleSpace s) 
     const int bin = (int)L.found[0];
     if (bin == kBins) return;
     const bool all = short_list(s, b, mass, W, S, bin, L.found[1]);  // uniform
-    RowState* st = s.state + b;
     const float* tops = s.tops + (int64_t)b * s.nt;
+    if (tid == 0) L.count = 0;
+    __syncthreads();
     each_tile<kTilesNT>(
         row, t0, t0 + s.per_wg, [&](int t) { return S.bin(tops[t]) <= bin; },
         [&](int t, const float(&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int n = S.bin(v[j]);
-                const bool is = v[j] > -INFINITY && (n == bin || (all && n < bin));
-                const uint64_t m = __ballot(is);
-                if (!m) continue;
-                uint32_t at = 0;
-                if (lane == __builtin_ctzll(m)) at = atomicAdd(&st->count, (uint32_t)__popcll(m));
-                at = __shfl((int)at, __builtin_ctzll(m)) + __popcll(m & ((1ull << lane) - 1));
-                if (is && at < kList) s.list[(int64_t)b * kList + at] = token(v[j], row.index(t, j, lane));
+                if (v[j] > -INFINITY && (n == bin || (all && n < bin))) {
+                    const uint32_t at = atomicAdd(&L.count, 1u);
+                    if (at < kList) list[at] = token(v[j], row.index(t, j, lane));
+                }
             }
         });
+    __syncthreads();
+    const uint32_t n = L.count;
+    __syncthreads();
+    if (n == 0) return;
+    if (tid == 0) L.count = atomicAdd(&s.state[b].count, n);
+    __syncthreads();
+    for (uint32_t i = tid, at = L.count; i < n && at + i < kList; i += kTilesNT)
+        s.list[(int64_t)b * kList + at + i] = list[i];
 }
 
 // ------------------------------------------------------------------ borders --
@@ -644,18 +707,20 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
     return p;
 }
 
-// The numbers of a workgroup's threads in falling order.
-__device__ __forceinline__ uint64_t sort_falling(uint64_t x, uint64_t* space) {
+// The numbers of the first n threads (a power of 2 from 64 on) in falling order.
+__device__ __forceinline__ uint64_t sort_falling(uint64_t x, int n, uint64_t* space) {
     const int tid = threadIdx.x;
-    for (int size = 2; size <= kBorderNT; size *= 2)
+    for (int size = 2; size <= n; size *= 2)
         for (int stride = size / 2; stride > 0; stride /= 2) {
             uint64_t y;
             if (stride >= 64) {
                 __syncthreads();
                 space[tid] = x;
                 __syncthreads();
+                if (tid >= n) continue;  // whole waves
                 y = space[tid ^ stride];
             } else {
+                if (tid >= n) continue;
                 y = shfl64_xor(x, stride);
             }
             // the lower of the two places takes the larger number in a falling run
@@ -672,7 +737,9 @@ __device__ __forceinline__ uint64_t sort_falling(uint64_t x, uint64_t* space) {
 __device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const Ask& r, const Weights& W, int n,
                                             uint64_t want, BorderLds& L) {
     const int tid = threadIdx.x;
-    const uint64_t me = sort_falling(tid < n ? L.list[tid] : 0, L.bins);
+    int size = 64;
+    while (size < n) size *= 2;
+    const uint64_t me = sort_falling(tid < n ? L.list[tid] : 0, size, L.bins);
     const double w = W.of(token_logit(me)), least = (double)r.least;
     bool kept = me != 0 && (r.k == 0 || tid < r.k);
     uint64_t q = kept ? W.whole(w) : 0, all;
@@ -686,7 +753,7 @@ __device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const A
     L.list[tid] = me;
     L.bins[kBorderNT + tid] = q;
     // the index, inverted, and the place above: 0 where nothing is kept
-    const uint64_t by = sort_falling(kept ? me << 32 | (uint32_t)tid : 0, L.bins);
+    const uint64_t by = sort_falling(kept ? me << 32 | (uint32_t)tid : 0, size, L.bins);
     const int from = (int)(uint32_t)by;
     q = by ? L.bins[kBorderNT + from] : 0;
     const uint64_t before = block_before<kBorderNT>(q, L.block, &all);
@@ -704,10 +771,9 @@ __device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const A
 // No border lies behind bin `last`; tokens behind it are not looked at (of MASS
 // it is the last there is).
 template <bool BF16, bool MASS>
-__device__ __forceinline__ Prefix border(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r,
-                                         const Weights& W, Prefix in, const Scale& S, int last, BorderLds& L) {
+__device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops, const Ask& r, const Weights& W, Prefix in,
+                                         const Scale& S, int last, BorderLds& L) {
     const int tid = threadIdx.x, lane = tid & 63;
-    const float* tops = s.tops + (int64_t)b * s.nt;
     auto weight = [&](float v) -> uint64_t { return MASS ? W.whole(W.of(v)) : 1; };
     for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
     __syncthreads();
@@ -890,13 +956,16 @@ __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row,
 
 template <bool BF16>
 __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s) {
+    extern __shared__ float lds_tops[];  // [nt], then a list of tiles
     __shared__ BorderLds L;
     const int tid = threadIdx.x, b = blockIdx.x;
-    const Ask r = ask_of<kBorderNT>(s, b, L.block);
+    const Ask r = known_way(s, b);
     if (r.way == kSums || r.way == kDone) return;
     const Row<BF16> row(s.a, b);
     const Weights W = weights_of(s, r);
-    const float* tops = s.tops + (int64_t)b * s.nt;
+    const float* tops = lds_tops;
+    int* tiles = reinterpret_cast<int*>(lds_tops + s.nt);
+    for (int i = tid; i < s.nt; i += kBorderNT) lds_tops[i] = s.tops[(int64_t)b * s.nt + i];
     const Prefix every{-INFINITY, -1};
     Prefix kept = every;
     if (r.way == kFew) {
@@ -911,9 +980,15 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
         const int last = min((int)L.block.found[0], kBins - 1), lane = tid & 63;
         if (tid == 0) L.block.count = 0;
         __syncthreads();
-        each_tile<kBorderNT>(
-            row, 0, row.tiles, [&](int t) { return S.bin(tops[t]) <= last; },
-            [&](int t, const float(&v)[8]) {
+        for (int i = tid; i < row.tiles; i += kBorderNT)
+            if (tops[i] > -INFINITY && S.bin(tops[i]) <= last) tiles[atomicAdd(&L.block.count, 1u)] = i;
+        __syncthreads();
+        const int live = (int)L.block.count;
+        __syncthreads();
+        if (tid == 0) L.block.count = 0;
+        __syncthreads();
+        each_listed<kBorderNT>(
+            row, tiles, live, [&](int t, const float(&v)[8]) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (v[j] > -INFINITY && S.bin(v[j]) <= last) {
@@ -927,7 +1002,7 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
             finish_list(s, b, r, W, n, 0, L);
             return;
         }
-        kept = border<BF16, false>(s, row, b, r, W, every, S, last, L);
+        kept = border<BF16, false>(row, tops, r, W, every, S, last, L);
     } else {
         const bool mass = r.way == kMass;
         const uint64_t want = find_bin<kBorderNT>(
@@ -946,22 +1021,20 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
             }
             kept = rank_list(n, above, want, [&](float v) -> uint64_t { return mass ? W.whole(W.of(v)) : 1; }, L);
         } else if (bin < kBins) {
-            kept = mass ? border<BF16, true>(s, row, b, r, W, every, S, kBins - 1, L)
-                        : border<BF16, false>(s, row, b, r, W, every, S, kBins - 1, L);
+            kept = mass ? border<BF16, true>(row, tops, r, W, every, S, kBins - 1, L)
+                        : border<BF16, false>(row, tops, r, W, every, S, kBins - 1, L);
         }
     }
     if (r.k && r.p < 1.f)
-        kept = border<BF16, true>(s, row, b, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L);
+        kept = border<BF16, true>(row, tops, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L);
     if (tid == 0) s.state[b].kept = kept;
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(kTilesNT) void sample_sums_kernel(SampleSpace s) {
-    __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.y, t0 = blockIdx.x * s.per_wg;
-    if (s.state[b].drawn) return;
-    const Ask r = ask_of<kTilesNT>(s, b, L);
-    if (r.way == kDone || r.way == kSums) return;
+    const Ask r = known_way(s, b);
+    if (s.state[b].drawn || r.way == kDone || r.way == kSums) return;
     const Row<BF16> row(s.a, b);
     tile_sums<kTilesNT>(s, row, b, t0, t0 + s.per_wg, r, weights_of(s, r), s.state[b].kept,
                         s.sums + (int64_t)b * s.nt);
@@ -971,8 +1044,8 @@ template <bool BF16>
 __global__ __launch_bounds__(kTilesNT) void sample_draw_kernel(SampleSpace s) {
     __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.x;
+    const Ask r = known_way(s, b);
     if (s.state[b].drawn) return;
-    const Ask r = ask_of<kTilesNT>(s, b, L);
     if (r.top == -INFINITY) {
         if (threadIdx.x == 0) {
             s.a.ids[b] = -1;
@@ -1006,7 +1079,7 @@ static hipError_t run(const SampleSpace& s, hipStream_t st, StageTimer* tm) {
     if (e == hipSuccess) e = launch(tm, "sample_bins", sample_bins_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
     if (e == hipSuccess && filters) {
         e = launch(tm, "sample_gather", sample_gather_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
-        if (e == hipSuccess) e = launch(tm, "sample_border", sample_border_kernel<BF16>, rows, dim3(kBorderNT), st, s);
+        if (e == hipSuccess) e = launch_shm(tm, "sample_border", sample_border_kernel<BF16>, rows, dim3(kBorderNT), s.nt * 8, st, s);
         if (e == hipSuccess) e = launch(tm, "sample_sums", sample_sums_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
     }
     if (e == hipSuccess) e = launch(tm, "sample_draw", sample_draw_kernel<BF16>, rows, dim3(kTilesNT), st, s);
@@ -1021,8 +1094,7 @@ hipError_t sample(const SampleArgs& a, bool bf16, hipStream_t st, StageTimer* tm
     while ((int64_t)1 << bits < a.V) ++bits;
     s.lift = (double)((int64_t)1 << (52 - std::min(46, 62 - bits)));
     s.nt = sample_tiles(a.V);
-    // 4 tiles a wave, more where that gives far more workgroups than the chip holds
-    s.per_wg = 16 * (int)std::max<int64_t>(1, (int64_t)a.B * s.nt / (16 * 2048));
+    s.per_wg = 16;  // 4 a wave, whose loads are in flight at once
     const size_t tiles = (size_t)a.B * s.nt;
     char* ws = static_cast<char*>(a.workspace);
     s.bins = reinterpret_cast<uint64_t*>(ws);
