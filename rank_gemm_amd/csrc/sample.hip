@@ -34,15 +34,15 @@
 namespace lora {
 
 // ------------------------------------------------------------------ weights --
-// 2^y for y <= 0 (2^-1000 below that, and for NaN): y = n + r, |r| <= 1/2, and
-// the series of 2^r = e^(r ln 2) to the eleventh power (the next term is under
-// 1e-14).
+// 2^y for -1000 <= y <= 0: y = n + r, |r| <= 1/2, and the series of 2^r =
+// e^(r ln 2) to the eleventh power (the next term is under 1e-14). n is the low
+// word of y + 1.5 2^52, and goes into the exponent as it is.
 __device__ __forceinline__ double exp2_neg(double y) {
     constexpr double L = 0.693147180559945309417;
     constexpr double c2 = L * L / 2, c3 = c2 * L / 3, c4 = c3 * L / 4, c5 = c4 * L / 5, c6 = c5 * L / 6,
                      c7 = c6 * L / 7, c8 = c7 * L / 8, c9 = c8 * L / 9, c10 = c9 * L / 10, c11 = c10 * L / 11;
-    y = __builtin_fmax(y, -1000.0);
-    const double n = __builtin_rint(y), r = y - n;
+    constexpr double kRound = 6755399441055744.0;
+    const double m = y + kRound, r = y - (m - kRound);
     double s = c11;
     s = __builtin_fma(s, r, c10);
     s = __builtin_fma(s, r, c9);
@@ -55,19 +55,20 @@ __device__ __forceinline__ double exp2_neg(double y) {
     s = __builtin_fma(s, r, c2);
     s = __builtin_fma(s, r, L);
     s = __builtin_fma(s, r, 1.0);
-    return __builtin_ldexp(s, (int)n);
+    const u32x2 b = __builtin_bit_cast(u32x2, s);
+    return __builtin_bit_cast(double, u32x2{b[0], b[1] + (__builtin_bit_cast(u32x2, m)[0] << 20)});
 }
 
-// The weights of a request: w of a logit (-infinity and NaN: nothing that
-// counts), and w as a whole number of 2^-shift: w + 2^(52 - shift) has 2^-shift
-// as the last place of its mantissa.
+// The weights of a request: w of a logit (at least 2^-1000, also of -infinity
+// and NaN), and w as a whole number of 2^-shift, 0 for those: w + 2^(52 - shift)
+// has 2^-shift as the last place of its mantissa.
 struct Weights {
     float top;    // the largest logit
     double per;   // log2(e) / temperature
     double lift;  // 2^(52 - shift)
     __device__ __forceinline__ double of(float v) const {
         if (top == INFINITY) return v == top ? 1.0 : 0.0;  // among infinite logits all weigh the same
-        return exp2_neg(((double)v - (double)top) * per);
+        return exp2_neg(__builtin_fmax(((double)v - (double)top) * per, -1000.0));
     }
     __device__ __forceinline__ uint64_t whole(double w) const {
         return __builtin_bit_cast(uint64_t, w + lift) - __builtin_bit_cast(uint64_t, lift);
@@ -99,14 +100,53 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t v, int src) {
     return (uint64_t)(uint32_t)__shfl((int)(uint32_t)v, src) |
            (uint64_t)(uint32_t)__shfl((int)(uint32_t)(v >> 32), src) << 32;
 }
-__device__ __forceinline__ uint64_t shfl64_xor(uint64_t v, int o) {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(uint32_t)v, o) |
-           (uint64_t)(uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), o) << 32;
+// The value of lane ^ O, by moves among vector registers (through LDS a step of
+// a 1024-thread sort takes 220 ns).
+template <int O>
+__device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
+    static_assert(O == 1 || O == 2 || O == 4 || O == 8 || O == 16 || O == 32, "one bit of the lane");
+    const int x = (int)v;
+    if constexpr (O == 1) return __builtin_amdgcn_mov_dpp(x, 0xb1, 0xf, 0xf, true);  // quads 1 0 3 2
+    if constexpr (O == 2) return __builtin_amdgcn_mov_dpp(x, 0x4e, 0xf, 0xf, true);  // quads 2 3 0 1
+    if constexpr (O == 4)  // half rows mirrored (^ 7), then quads 3 2 1 0 (^ 3)
+        return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
+    if constexpr (O == 8) return __builtin_amdgcn_mov_dpp(x, 0x128, 0xf, 0xf, true);  // rows turned by 8
+    if constexpr (O == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? p[0] : p[1];
+    }
+    if constexpr (O == 32) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? p[0] : p[1];
+    }
+}
+template <int O, class T>
+__device__ __forceinline__ T lane_xor(T v) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, lane_xor32<O>(__builtin_bit_cast(uint32_t, v)));
+    } else {
+        const u32x2 x = __builtin_bit_cast(u32x2, v);
+        return __builtin_bit_cast(T, u32x2{lane_xor32<O>(x[0]), lane_xor32<O>(x[1])});
+    }
+}
+// f over all lanes of a wave (f of two values, in any order).
+template <class T, class F>
+__device__ __forceinline__ T wave_all(T v, F f) {
+    v = f(v, lane_xor<32>(v));
+    v = f(v, lane_xor<16>(v));
+    v = f(v, lane_xor<8>(v));
+    v = f(v, lane_xor<4>(v));
+    v = f(v, lane_xor<2>(v));
+    return f(v, lane_xor<1>(v));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_min(float v) {
+    return wave_all(v, [](float a, float b) { return fminf(a, b); });
 }
 __device__ __forceinline__ uint64_t wave_total(uint64_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += shfl64_xor(v, o);
-    return v;
+    return wave_all(v, [](uint64_t a, uint64_t b) { return a + b; });
 }
 __device__ __forceinline__ uint64_t wave_scan(uint64_t v, int lane) {  // inclusive
 #pragma unroll
@@ -229,12 +269,9 @@ __device__ __forceinline__ Ask find_way(const SampleSpace& s, int b, BlockLds<NT
             ++live;
         }
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        top = fmaxf(top, __shfl_xor(top, o));
-        under = fminf(under, __shfl_xor(under, o));
-        live += __shfl_xor(live, o);
-    }
+    top = wave_max(top);
+    under = wave_min(under);
+    live = (int)wave_all((uint32_t)live, [](uint32_t a, uint32_t b) { return a + b; });
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
         L.part_top[wave] = top;
@@ -282,8 +319,8 @@ __device__ __forceinline__ Scale scale_of_count(const Ask& r) {
 // which is at least 1, with the border's own; fewer than V of them, so that one
 // weighs at least (1 - p) / V.
 __device__ __forceinline__ Scale scale_of_mass(const Ask& r, const Weights& W, int V) {
-    const double reach = log2((double)V / (1.0 - (double)r.p)) + 1.0;
-    return Scale{r.top, r.top == INFINITY ? 0.f : (float)fmin(W.per * (kBins - 2) / reach, 1e30)};
+    const float reach = log2f((float)V / (1.f - r.p)) + 1.f;
+    return Scale{r.top, r.top == INFINITY ? 0.f : fminf((float)W.per * ((kBins - 2) / reach), 1e30f)};
 }
 
 // the sum of a value over the threads before this one; *all: over all of them
@@ -415,12 +452,13 @@ __device__ __forceinline__ void each_listed(const Row<BF16>& row, const int* til
 // The sums of 4 values over a wave: of value i in the lanes 16 i to 16 i + 15.
 __device__ __forceinline__ uint64_t wave_totals(const uint64_t (&x)[4], int lane) {
     const bool h = lane & 32, q = lane & 16;
-    const uint64_t a = (h ? x[2] : x[0]) + shfl64_xor(h ? x[0] : x[2], 32);
-    const uint64_t b = (h ? x[3] : x[1]) + shfl64_xor(h ? x[1] : x[3], 32);
-    uint64_t v = (q ? b : a) + shfl64_xor(q ? a : b, 16);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += shfl64_xor(v, o);
-    return v;
+    const uint64_t a = (h ? x[2] : x[0]) + lane_xor<32>(h ? x[0] : x[2]);
+    const uint64_t b = (h ? x[3] : x[1]) + lane_xor<32>(h ? x[1] : x[3]);
+    uint64_t v = (q ? b : a) + lane_xor<16>(q ? a : b);
+    v += lane_xor<8>(v);
+    v += lane_xor<4>(v);
+    v += lane_xor<2>(v);
+    return v + lane_xor<1>(v);
 }
 
 // ------------------------------------------------------------- row by tiles --
@@ -436,8 +474,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_tops_kernel(SampleSpace s) {
             float m = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j]);  // of a number and NaN the number
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+            m = wave_max(m);
             if (lane == 0) s.tops[(int64_t)b * s.nt + t] = m;
         });
     // what the others add to
@@ -459,9 +496,9 @@ __device__ __forceinline__ void tile_sums(const SampleSpace& s, const Row<BF16>&
     const double least = (double)r.least;
     for (int t = t0 + threadIdx.x; t < min(t1, s.nt); t += NT) sums[t] = 0;
     __syncthreads();
-    uint64_t x[4];
+    uint64_t x[4] = {0, 0, 0, 0};
     each_tile<NT>(
-        row, t0, t1, [&](int t) { return tops[t] >= kept.v && W.of(tops[t]) >= least; },
+        row, t0, t1, [&](int t) { return tops[t] >= kept.v && (least == 0.0 || W.of(tops[t]) >= least); },
         [&](int t, const float(&v)[8]) {
             uint64_t y = 0;
 #pragma unroll
@@ -648,12 +685,8 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
     for (;;) {
         const bool in = tid < n && mine >= low && mine <= high;
         // how many are left, and their range
-        uint64_t lo = in ? mine : ~0ull, hi = in ? mine : 0;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            lo = min(lo, shfl64_xor(lo, o));
-            hi = max(hi, shfl64_xor(hi, o));
-        }
+        const uint64_t lo = wave_all(in ? mine : ~(uint64_t)0, [](uint64_t a, uint64_t b) { return a < b ? a : b; });
+        const uint64_t hi = wave_all(in ? mine : (uint64_t)0, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
         const uint64_t m = __ballot(in);
         for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
         __syncthreads();
@@ -707,26 +740,42 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
     return p;
 }
 
+// One step of a bitonic sort within waves: the lower of two places takes the
+// larger number in a falling run of `size`.
+template <int STRIDE>
+__device__ __forceinline__ uint64_t sort_step(uint64_t x, int size) {
+    const uint64_t y = lane_xor<STRIDE>(x);
+    const bool larger = ((threadIdx.x & STRIDE) == 0) == ((threadIdx.x & size) == 0);
+    return (x > y) == larger ? x : y;
+}
+template <int STRIDE>
+__device__ __forceinline__ uint64_t sort_steps(uint64_t x, int size) {  // STRIDE, STRIDE / 2, ... 1
+    x = sort_step<STRIDE>(x, size);
+    if constexpr (STRIDE > 1) x = sort_steps<STRIDE / 2>(x, size);
+    return x;
+}
 // The numbers of the first n threads (a power of 2 from 64 on) in falling order.
 __device__ __forceinline__ uint64_t sort_falling(uint64_t x, int n, uint64_t* space) {
     const int tid = threadIdx.x;
-    for (int size = 2; size <= n; size *= 2)
-        for (int stride = size / 2; stride > 0; stride /= 2) {
-            uint64_t y;
-            if (stride >= 64) {
-                __syncthreads();
-                space[tid] = x;
-                __syncthreads();
-                if (tid >= n) continue;  // whole waves
-                y = space[tid ^ stride];
-            } else {
-                if (tid >= n) continue;
-                y = shfl64_xor(x, stride);
-            }
-            // the lower of the two places takes the larger number in a falling run
+    if (tid < n) {  // whole waves
+        x = sort_steps<1>(x, 2);
+        x = sort_steps<2>(x, 4);
+        x = sort_steps<4>(x, 8);
+        x = sort_steps<8>(x, 16);
+        x = sort_steps<16>(x, 32);
+        x = sort_steps<32>(x, 64);
+    }
+    for (int size = 128; size <= n; size *= 2) {
+        for (int stride = size / 2; stride >= 64; stride /= 2) {
+            __syncthreads();
+            space[tid] = x;
+            __syncthreads();
+            const uint64_t y = space[tid ^ stride];
             const bool larger = ((tid & stride) == 0) == ((tid & size) == 0);
-            x = larger ? max(x, y) : min(x, y);
+            x = (x > y) == larger ? x : y;
         }
+        if (tid < n) x = sort_steps<32>(x, size);
+    }
     __syncthreads();
     return x;
 }
@@ -817,11 +866,8 @@ __device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops
     __syncthreads();
     if (n <= kList) return rank_list(n, above, want, weight, L);
     // more tokens than the list holds: by the digits of their logits' order
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        low = fminf(low, __shfl_xor(low, o));
-        high = fmaxf(high, __shfl_xor(high, o));
-    }
+    low = wave_min(low);
+    high = wave_max(high);
     if (lane == 0) {
         L.block.part_top[tid >> 6] = high;
         L.block.part_under[tid >> 6] = low;
@@ -883,8 +929,7 @@ __device__ __forceinline__ void first_token(const SampleSpace& s, const Row<BF16
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (v[j] == r.top) first = min(first, row.index(t, j, lane));
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) first = min(first, __shfl_xor(first, o));
+    first = (int)wave_all((uint32_t)first, [](uint32_t a, uint32_t b) { return min(a, b); });
     if (lane == 0) {
         s.a.ids[b] = first;
         s.a.probs[b] = 1.f;
