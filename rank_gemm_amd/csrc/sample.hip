@@ -34,29 +34,41 @@
 namespace lora {
 
 // ------------------------------------------------------------------ weights --
-// 2^y for -1000 <= y <= 0: y = n + r, |r| <= 1/2, and the series of 2^r =
-// e^(r ln 2) to the eleventh power (the next term is under 1e-14). n is the low
-// word of y + 1.5 2^52, and goes into the exponent as it is.
-__device__ __forceinline__ double exp2_neg(double y) {
+// a b + c with c in scalar registers (the compiler would copy every c to vector
+// registers first).
+__device__ __forceinline__ double fma_s(double a, double b, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+    return d;
+}
+// 2^y of N numbers -1000 <= y <= 0: y = n + r, |r| <= 1/2, and the series of 2^r
+// = e^(r ln 2) to the eleventh power (the next term is under 1e-14). n is the
+// low word of y + 1.5 2^52, and goes into the exponent as it is.
+template <int N>
+__device__ __forceinline__ void exp2_neg(double (&y)[N]) {
     constexpr double L = 0.693147180559945309417;
     constexpr double c2 = L * L / 2, c3 = c2 * L / 3, c4 = c3 * L / 4, c5 = c4 * L / 5, c6 = c5 * L / 6,
                      c7 = c6 * L / 7, c8 = c7 * L / 8, c9 = c8 * L / 9, c10 = c9 * L / 10, c11 = c10 * L / 11;
+    constexpr double c[11] = {c10, c9, c8, c7, c6, c5, c4, c3, c2, L, 1.0};
     constexpr double kRound = 6755399441055744.0;
-    const double m = y + kRound, r = y - (m - kRound);
-    double s = c11;
-    s = __builtin_fma(s, r, c10);
-    s = __builtin_fma(s, r, c9);
-    s = __builtin_fma(s, r, c8);
-    s = __builtin_fma(s, r, c7);
-    s = __builtin_fma(s, r, c6);
-    s = __builtin_fma(s, r, c5);
-    s = __builtin_fma(s, r, c4);
-    s = __builtin_fma(s, r, c3);
-    s = __builtin_fma(s, r, c2);
-    s = __builtin_fma(s, r, L);
-    s = __builtin_fma(s, r, 1.0);
-    const u32x2 b = __builtin_bit_cast(u32x2, s);
-    return __builtin_bit_cast(double, u32x2{b[0], b[1] + (__builtin_bit_cast(u32x2, m)[0] << 20)});
+    double r[N];
+    uint32_t n[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const double m = y[i] + kRound;
+        n[i] = __builtin_bit_cast(u32x2, m)[0];
+        r[i] = y[i] - (m - kRound);
+        y[i] = c11;
+    }
+#pragma unroll
+    for (int k = 0; k < 11; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = fma_s(y[i], r[i], c[k]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const u32x2 b = __builtin_bit_cast(u32x2, y[i]);
+        y[i] = __builtin_bit_cast(double, u32x2{b[0], b[1] + (n[i] << 20)});
+    }
 }
 
 // The weights of a request: w of a logit (at least 2^-1000, also of -infinity
@@ -66,9 +78,22 @@ struct Weights {
     float top;    // the largest logit
     double per;   // log2(e) / temperature
     double lift;  // 2^(52 - shift)
+    template <int N>
+    __device__ __forceinline__ void of(double (&w)[N], const float (&v)[N]) const {
+        if (top == INFINITY) {  // uniform; among infinite logits all weigh the same
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = v[i] == top ? 1.0 : 0.0;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = __builtin_fmax(((double)v[i] - (double)top) * per, -1000.0);
+        exp2_neg<N>(w);
+    }
     __device__ __forceinline__ double of(float v) const {
-        if (top == INFINITY) return v == top ? 1.0 : 0.0;  // among infinite logits all weigh the same
-        return exp2_neg(__builtin_fmax(((double)v - (double)top) * per, -1000.0));
+        double w[1];
+        const float x[1] = {v};
+        of<1>(w, x);
+        return w[0];
     }
     __device__ __forceinline__ uint64_t whole(double w) const {
         return __builtin_bit_cast(uint64_t, w + lift) - __builtin_bit_cast(uint64_t, lift);
@@ -501,12 +526,15 @@ __device__ __forceinline__ void tile_sums(const SampleSpace& s, const Row<BF16>&
         row, t0, t1, [&](int t) { return tops[t] >= kept.v && (least == 0.0 || W.of(tops[t]) >= least); },
         [&](int t, const float(&v)[8]) {
             uint64_t y = 0;
+            bool is[8], any = false;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (kept.holds(v[j], row.index(t, j, lane))) {
-                    const double w = W.of(v[j]);
-                    y += w < least ? 0 : W.whole(w);
-                }
+            for (int j = 0; j < 8; ++j) any |= is[j] = kept.holds(v[j], row.index(t, j, lane));
+            if (__any(any)) {
+                double w[8];
+                W.of<8>(w, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y += is[j] && !(w[j] < least) ? W.whole(w[j]) : 0;
+            }
             x[t & 3] = y;  // t0 is a multiple of 4: a constant place
         },
         [&](int t, uint32_t is) {
@@ -541,10 +569,14 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
         each_tile<kTilesNT>(
             row, t0, t0 + s.per_wg, [](int) { return true; },
             [&](int, const float(&v)[8]) {
+                double w[8];
+                W.of<8>(w, v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint64_t q = W.whole(W.of(v[j]));
-                    if (q) add_bin(bins, S.bin(v[j]), q, rest);
+                    const uint64_t q = W.whole(w[j]);
+                    const int n = S.bin(v[j]);
+                    rest += n == kBins - 1 ? q : 0;
+                    if (n < kBins - 1 && q) add(&bins[n], q);
                 }
             });
     else
@@ -1121,7 +1153,8 @@ static hipError_t run(const SampleSpace& s, hipStream_t st, StageTimer* tm) {
     const dim3 tiles((s.nt + s.per_wg - 1) / s.per_wg, s.a.B), rows(s.a.B);
     const bool filters = s.a.top_k || s.a.top_p;
     hipError_t e = launch(tm, "sample_tops", sample_tops_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
-    if (e == hipSuccess) e = launch(tm, "sample_bins", sample_bins_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
+    if (e == hipSuccess)
+        e = launch(tm, "sample_bins", sample_bins_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
     if (e == hipSuccess && filters) {
         e = launch(tm, "sample_gather", sample_gather_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
         if (e == hipSuccess) e = launch_shm(tm, "sample_border", sample_border_kernel<BF16>, rows, dim3(kBorderNT), s.nt * 8, st, s);
@@ -1139,7 +1172,11 @@ hipError_t sample(const SampleArgs& a, bool bf16, hipStream_t st, StageTimer* tm
     while ((int64_t)1 << bits < a.V) ++bits;
     s.lift = (double)((int64_t)1 << (52 - std::min(46, 62 - bits)));
     s.nt = sample_tiles(a.V);
-    s.per_wg = 16;  // 4 a wave, whose loads are in flight at once
+    // 4 a wave, whose loads are in flight at once. More would bring fewer
+    // histograms to memory (64 tiles, 256 rows of 128k: 30 against 50 us where
+    // every row makes one), but rows of a batch mostly go different ways, and the
+    // few that pass over all tiles are then spread thinner (39 against 28 us)
+    s.per_wg = 16;
     const size_t tiles = (size_t)a.B * s.nt;
     char* ws = static_cast<char*>(a.workspace);
     s.bins = reinterpret_cast<uint64_t*>(ws);
