@@ -219,27 +219,47 @@ __device__ __forceinline__ int tile_page(const AttnPlan& p, const int32_t* table
 }
 
 // A tile's rows of keys or values into LDS; rows that are left out, and chunks
-// behind dim, as zeros.
+// behind dim, as zeros. Where every row is attended to, dim fills its chunks and
+// the rows of an instruction lie in one page, its address is a scalar and the
+// lane's constant offset.
 template <class C, bool V>
-__device__ __forceinline__ void load_stage(const AttnPlan& p, const void* base, const AttnTile<C>& t, u32x4* dst,
-                                           int lane) {
-    const int r0 = lane / C::CH, c0 = lane % C::CH, dim_chunks = p.a.c.dim * (C::F8 ? 1 : 2) / 16;
-    const int64_t step = p.a.c.row_stride * (C::F8 ? 1 : 2);
+__device__ __forceinline__ void load_stage(const AttnPlan& p, const void* base, const AttnTile<C>& t,
+                                           u32x4* dst, int lane) {
+    constexpr int ES = C::F8 ? 1 : 2;
+    // what follows from the lane is computed again for every stage: kept from
+    // one to the next it takes the registers of the products
+    asm volatile("" : "+v"(lane));
+    const int r0 = lane / C::CH, c0 = lane % C::CH;
+    const bool whole = C::TK == 64 ? t.mask == ~0ull : t.mask == 0xffffffffull;
+    if (p.hold && whole && p.a.c.dim == C::DP) {  // uniform
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) {
+            const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)t.off, j * C::RI);
+            const uint32_t hi32 = __builtin_amdgcn_readlane((int)(uint32_t)(t.off >> 32), j * C::RI);
+            const char* at = static_cast<const char*>(base) + (int64_t)((uint64_t)hi32 << 32 | lo32);
+            const int r = j * C::RI + r0;
+            const uint32_t off = r0 * (uint32_t)p.a.c.row_stride * ES + (c0 ^ (V ? swz_v<C>(r) : swz_k<C>(r))) * 16;
+            dma16(as_global<u32x4>(at + off), dst + j * 64);
+        }
+        return;
+    }
+    const int dim_chunks = p.a.c.dim * ES / 16;
+    const int64_t step = p.a.c.row_stride * ES;
 #pragma unroll
     for (int j = 0; j < C::NI; ++j) {
         const int r = j * C::RI + r0;
         const int chunk = c0 ^ (V ? swz_v<C>(r) : swz_k<C>(r));
-        int64_t off;
+        int64_t at;
         if (p.hold) {  // uniform
             const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)t.off, j * C::RI);
             const uint32_t hi32 = __builtin_amdgcn_readlane((int)(uint32_t)(t.off >> 32), j * C::RI);
-            off = (int64_t)((uint64_t)hi32 << 32 | lo32) + r0 * step;
+            at = (int64_t)((uint64_t)hi32 << 32 | lo32) + r0 * step;
         } else {
             const uint32_t lo32 = __shfl((int)(uint32_t)t.off, r), hi32 = __shfl((int)(uint32_t)(t.off >> 32), r);
-            off = (int64_t)((uint64_t)hi32 << 32 | lo32);
+            at = (int64_t)((uint64_t)hi32 << 32 | lo32);
         }
         const bool ok = ((t.mask >> r) & 1) && chunk < dim_chunks;
-        dma16(or_zero(ok, static_cast<const char*>(base) + off + chunk * 16), dst + j * 64);
+        dma16(or_zero(ok, static_cast<const char*>(base) + at + chunk * 16), dst + j * 64);
     }
 }
 
@@ -265,19 +285,8 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
 
     u32x4* kbuf = L.kv[wave];
     u32x4* vbuf = kbuf + C::STAGE / 16;
-    AttnTile<C> tile{};
-    int page = 0;
-    if (nt > 0) {
-        page = tile_page<C>(p, table, first + lane, hi);
-        tile = tile_rows<C>(p, first + lane, lo, hi, page, head);
-        load_stage<C, false>(p, a.c.k, tile, kbuf, lane);
-        issue_fence();
-        page = tile_page<C>(p, table, first + C::U + lane, hi);
-        load_stage<C, true>(p, a.c.v, tile, vbuf, lane);
-        issue_fence();
-    }
-
-    // q as the right operand: column fr = head, 8 k a lane
+    // q as the right operand: column fr = head, 8 k a lane; ahead of the tiles, so
+    // that the wait for it is not one for them
     u32x4 q[RT][NK];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -288,6 +297,22 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
             const int d = C::F8 ? (c >> 1) * 64 + fg * 16 + (c & 1) * 8 : c * 32 + fg * 8;
             q[rt][c] = *or_zero(h < nq && d < D, a.q + b * a.q_stride + (int64_t)(h0 + h) * D + d);
         }
+    AttnTile<C> tile{};
+    int page = 0;
+    if (nt > 0) {
+        page = tile_page<C>(p, table, first + lane, hi);
+        tile = tile_rows<C>(p, first + lane, lo, hi, page, head);
+        page = tile_page<C>(p, table, first + C::U + lane, hi);
+        load_stage<C, false>(p, a.c.k, tile, kbuf, lane);
+        issue_fence();
+        load_stage<C, true>(p, a.c.v, tile, vbuf, lane);
+        issue_fence();
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int c = 0; c < NK; ++c) asm volatile("" : "+v"(q[rt][c]));  // it has landed
     const float sc = a.scale_log2 * (C::F8 ? a.c.k_scale[hk] : 1.f);
 
     f32x4 o[RT][ND];
@@ -307,16 +332,13 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
                         (C::F8 ? (swz_v<C>(vr) << 4) + (fr & 1) * 8
                                : ((((fr & 3) >> 1) ^ swz_v<C>(vr)) << 4) + (fr & 1) * 8);
 
-    for (int i = 0; i < nt; ++i) {
-        const int pos = first + i * C::U;
-        const bool more = i + 1 < nt;
-        const uint64_t mask = tile.mask;
-        f32x4 s[RT][NB][2];
+    f32x4 s[RT][NB][2];
+    u32x4 ph[RT][NB], pl[RT][NB];
+    auto scores = [&]() {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int n = 0; n < NB; ++n) s[rt][n][0] = s[rt][n][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        vm_landed<C::NI>();  // the keys: the values were asked for after them
         constexpr int NR = C::F8 ? (DP / 64) : (NK < 4 ? NK : 4);  // 16-byte reads of a row at once
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -345,15 +367,9 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
                         }
                     }
             }
-        AttnTile<C> next = tile;
-        if (more) {
-            next = tile_rows<C>(p, pos + C::U + lane, lo, hi, page, head);
-            load_stage<C, false>(p, a.c.k, next, kbuf, lane);
-            issue_fence();
-            page = tile_page<C>(p, table, pos + 2 * C::U + lane, hi);
-        }
+    };
+    auto weights = [&](uint64_t mask) {
         // scores (base 2), the running maximum, P as two bf16 halves
-        u32x4 ph[RT][NB], pl[RT][NB];
         const bool all = C::TK == 64 ? mask == ~0ull : mask == 0xffffffffull;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -393,10 +409,8 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
                         pack_bf16x2(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xffff0000u));
                 }
         }
-        if (more)
-            vm_landed<C::NI>();  // the values: the next tile's keys were asked for after them
-        else
-            vm_landed<0>();
+    };
+    auto values = [&]() {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -425,8 +439,31 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
                         o[rt][d0 + d] = mfma16x16x32(v[d], pl[rt][n], o[rt][d0 + d]);
                     }
             }
-        if (more) load_stage<C, true>(p, a.c.v, next, vbuf, lane);
+    };
+    // Loads in their order: pages of tile i + 2, keys of i + 1, values of i + 1;
+    // they land in it too, so that a wait names how many of the later ones may
+    // still be out.
+    for (int i = 0; i + 1 < nt; ++i) {
+        vm_landed<C::NI>();  // the keys: the values were asked for after them
+        scores();
+        const int pos = first + (i + 1) * C::U;
+        const AttnTile<C> next = tile_rows<C>(p, pos + lane, lo, hi, page, head);
+        page = tile_page<C>(p, table, pos + C::U + lane, hi);
+        load_stage<C, false>(p, a.c.k, next, kbuf, lane);
+        issue_fence();
+        weights(tile.mask);
+        vm_landed<C::NI>();  // the values: the next keys were asked for after them
+        values();
+        load_stage<C, true>(p, a.c.v, next, vbuf, lane);
+        issue_fence();
         tile = next;
+    }
+    if (nt > 0) {
+        vm_landed<C::NI>();
+        scores();
+        weights(tile.mask);
+        vm_landed<0>();
+        values();
     }
 
     // the waves' m, l and o joined through LDS, 16 heads at a time
@@ -539,8 +576,10 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(AttnPlan p
 }
 
 // Rows of more than one piece joined, rows without a position written as
-// zeros. One workgroup a row: its threads take 4 dimensions of a head each, and
-// where there are few of those, several share a head's pieces.
+// zeros. A workgroup takes all heads of a row, or one where there are few rows
+// (8 rows of 64 pieces: 6.4 us with all, 3.0 with one): its threads 4
+// dimensions of a head each, and where there are few of those, several share a
+// head's pieces.
 constexpr int kJoinThreads = 512;
 template <bool F8>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
@@ -557,12 +596,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
     const int2 meta = hi > lo ? p.meta[r] : make_int2(0, 0);
     if (hi > lo && meta.y == 1) return;  // written by the first kernel
     const float vs = F8 ? a.c.v_scale[hk] : 1.f;
-    const int items = nq * (D / 4);
+    const int h0 = gridDim.y > 1 ? (int)blockIdx.y : 0, heads = gridDim.y > 1 ? 1 : nq;
+    if (h0 >= nq) return;
+    const int items = heads * (D / 4);
     int share = 1;
     while (2 * share * items <= kJoinThreads) share *= 2;
     const int at = threadIdx.x / share, sub = threadIdx.x % share;
     for (int i0 = 0; i0 < items; i0 += kJoinThreads / share) {
-        const int i = i0 + at, h = i / (D / 4), d4 = i % (D / 4);
+        const int i = i0 + at, h = h0 + i / (D / 4), d4 = i % (D / 4);
         float m = kLowest, l = 0.f;
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
         if (i < items) {
@@ -610,7 +651,8 @@ struct Shape {
 Shape attn_shape(int heads, int kv_heads, int dim, int width, int page_rows, bool f8) {
     Shape s;
     s.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-    const int group = heads / kv_heads, most = s.dp == 256 ? 32 : 64;
+    // heads a workgroup: as many as its registers hold
+    const int group = heads / kv_heads, most = s.dp == 256 ? 16 : s.dp == 128 ? 32 : 64;
     s.blocks = cdiv(group, most);
     s.block_heads = cdiv(group, s.blocks);
     s.rt = s.block_heads <= 16 ? 1 : s.block_heads <= 32 ? 2 : 4;
@@ -625,6 +667,8 @@ Shape attn_shape(int heads, int kv_heads, int dim, int width, int page_rows, boo
 template <int DP, bool F8>
 auto attn_kernel(int rt) {
     if constexpr (DP == 256)
+        return attn_decode_kernel<AttnCfg<DP, F8, 1>>;
+    else if constexpr (DP == 128)
         return rt == 1 ? attn_decode_kernel<AttnCfg<DP, F8, 1>> : attn_decode_kernel<AttnCfg<DP, F8, 2>>;
     else
         return rt == 1   ? attn_decode_kernel<AttnCfg<DP, F8, 1>>
@@ -661,7 +705,7 @@ hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* t
     p.shift = sh;
     p.magic = a.c.page_rows > 1 ? (uint32_t)((1ull << (32 + sh)) / a.c.page_rows + 1) : 0;
     const int chunks = s.dp * (f8 ? 1 : 2) / 16;
-    p.hold = a.c.page_rows % (64 / chunks) == 0;
+    p.hold = a.c.page_rows % (64 / chunks) == 0 && a.c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
     const size_t rows = (size_t)a.B * p.rows, slots = s.wgs + rows;
     char* ws = static_cast<char*>(a.workspace);
     p.part = reinterpret_cast<float*>(ws);
@@ -674,8 +718,8 @@ hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* t
     const uint32_t grid = s.wgs ? s.wgs : (uint32_t)rows;
     hipError_t e = launch(tm, "attn_decode", kernel, dim3(grid), dim3(64 * kAttnWaves), st, p);
     if (e != hipSuccess || s.wgs == 0) return e;
-    return launch(tm, "attn_join", f8 ? attn_join_kernel<true> : attn_join_kernel<false>, dim3((uint32_t)rows),
-                  dim3(kJoinThreads), st, p);
+    return launch(tm, "attn_join", f8 ? attn_join_kernel<true> : attn_join_kernel<false>,
+                  dim3((uint32_t)rows, rows < 256 ? s.block_heads : 1), dim3(kJoinThreads), st, p);
 }
 
 }  // namespace lora
