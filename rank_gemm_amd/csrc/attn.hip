@@ -44,7 +44,7 @@ struct AttnPlan {
     int block_heads;  // heads a block
     uint32_t magic;   // position / page_rows = umulhi(position, magic) >> shift (page_rows > 1)
     int shift;
-    int hold;         // the rows of one load instruction lie in one page
+    int whole;        // whole tiles by AttnTile::group
     float* part;      // [wgs + B rows][block_heads][dim] o of a piece
     float2* ml;       // [wgs + B rows][block_heads] m, l of a piece
     int2* meta;       // [B rows] first piece, pieces
@@ -171,6 +171,7 @@ __device__ __forceinline__ void attn_range(const AttnArgs& a, int b, int* lo, in
     *lo = a.window > 0 ? max(n - a.window, 0) : 0;
     *hi = n;
 }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 template <class C>
 __device__ __forceinline__ int attn_units(const AttnArgs& a, int b) {
     int lo, hi;
@@ -194,70 +195,90 @@ struct AttnLds {
     int request;
 };
 
-template <class C>
-struct AttnTile {  // where a tile's rows are
-    int64_t off;    // bytes to this lane's row (lane = row of the tile)
-    uint64_t mask;  // rows that are attended to
+// 64 entries of a request's page table, one a lane: a wait for them is one for
+// everything the wave has asked for, so they are fetched for many tiles at once
+// (page_rows 16: 8 tiles, 64: 32).
+struct AttnPages {
+    const int32_t* table;
+    int first, last;  // entries held, the request's last one
+    int page;
 };
-
-template <class C>
-__device__ __forceinline__ AttnTile<C> tile_rows(const AttnPlan& p, int pos, int lo, int hi, int page, int64_t head) {
-    const AttnArgs& a = p.a;
-    AttnTile<C> t;
-    const int idx = min(a.c.page_rows > 1 ? (int)(__umulhi((uint32_t)pos, p.magic) >> p.shift) : pos,
-                        a.width - 1);
-    const bool ok = pos >= lo && pos < hi && (threadIdx.x & 63) < C::TK && page >= 0 && page < a.c.n_pages;
-    t.off = (page * a.c.page_stride + (int64_t)(pos - idx * a.c.page_rows) * a.c.row_stride + head) * (C::F8 ? 1 : 2);
-    t.mask = __ballot(ok);
-    return t;
+__device__ __forceinline__ int page_of(const AttnPlan& p, int pos) {
+    return p.a.c.page_rows > 1 ? (int)(__umulhi((uint32_t)pos, p.magic) >> p.shift) : pos;
 }
-// The page that holds position pos; past the request's last position the page of that one.
+
+// Where a tile's rows are. Whole tiles over pages of a multiple of 16 rows, with
+// dim filling its chunks, are four numbers or two; of others every lane has its
+// row's, and the mask says which are attended to.
 template <class C>
-__device__ __forceinline__ int tile_page(const AttnPlan& p, const int32_t* table, int pos, int hi) {
-    const int at = min(pos, hi - 1);
-    return table[p.a.c.page_rows > 1 ? (int)(__umulhi((uint32_t)at, p.magic) >> p.shift) : at];
+struct AttnTile {
+    static constexpr int G = C::TK / 16;
+    bool whole;
+    int64_t group[G];  // bytes to each 16 rows
+    int64_t off;       // bytes to this lane's row (lane = row of the tile)
+    uint64_t mask;     // rows that are attended to
+};
+template <class C>
+__device__ __forceinline__ AttnTile<C> tile_rows(const AttnPlan& p, AttnPages& pages, int pos, int lo, int hi,
+                                                 int64_t head) {
+    constexpr int ES = C::F8 ? 1 : 2;
+    const KvCache& c = p.a.c;
+    const int lane = threadIdx.x & 63, e0 = page_of(p, pos), e1 = page_of(p, min(pos + C::TK, hi) - 1);
+    if (e1 - pages.first >= 64) {  // uniform
+        pages.first = e0;
+        pages.page = pages.table[min(e0 + lane, pages.last)];
+        asm volatile("" : "+v"(pages.page));  // waited for here
+    }
+    AttnTile<C> t;
+    t.whole = p.whole && pos >= lo && pos + C::TK <= hi;
+    if (t.whole) {
+#pragma unroll
+        for (int g = 0; g < AttnTile<C>::G; ++g) {
+            const int at = pos + 16 * g, e = page_of(p, at);
+            const int page = __builtin_amdgcn_readlane(pages.page, e - pages.first);
+            t.whole &= page >= 0 && page < c.n_pages;
+            t.group[g] = (page * c.page_stride + (int64_t)(at - e * c.page_rows) * c.row_stride + head) * ES;
+        }
+        t.mask = C::TK == 64 ? ~0ull : 0xffffffffull;
+    }
+    if (!t.whole) {
+        const int at = min(pos + lane, hi - 1), e = page_of(p, at);
+        const int page = __shfl(pages.page, min(e - pages.first, 63));
+        t.off = (page * c.page_stride + (int64_t)(at - e * c.page_rows) * c.row_stride + head) * ES;
+        t.mask = __ballot(lane < C::TK && pos + lane >= lo && pos + lane < hi && page >= 0 && page < c.n_pages);
+    }
+    return t;
 }
 
 // A tile's rows of keys or values into LDS; rows that are left out, and chunks
-// behind dim, as zeros. Where every row is attended to, dim fills its chunks and
-// the rows of an instruction lie in one page, its address is a scalar and the
-// lane's constant offset.
+// behind dim, as zeros. The swizzle is in the source address, since the LDS
+// address goes lane by lane.
 template <class C, bool V>
-__device__ __forceinline__ void load_stage(const AttnPlan& p, const void* base, const AttnTile<C>& t,
-                                           u32x4* dst, int lane) {
+__device__ __forceinline__ void load_stage(const AttnPlan& p, const void* base, const AttnTile<C>& t, u32x4* dst,
+                                           uint32_t lane) {
     constexpr int ES = C::F8 ? 1 : 2;
     // what follows from the lane is computed again for every stage: kept from
     // one to the next it takes the registers of the products
     asm volatile("" : "+v"(lane));
-    const int r0 = lane / C::CH, c0 = lane % C::CH;
-    const bool whole = C::TK == 64 ? t.mask == ~0ull : t.mask == 0xffffffffull;
-    if (p.hold && whole && p.a.c.dim == C::DP) {  // uniform
+    const uint32_t r0 = lane / C::CH, c0 = lane % C::CH;
+    if (t.whole) {  // uniform
 #pragma unroll
         for (int j = 0; j < C::NI; ++j) {
-            const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)t.off, j * C::RI);
-            const uint32_t hi32 = __builtin_amdgcn_readlane((int)(uint32_t)(t.off >> 32), j * C::RI);
-            const char* at = static_cast<const char*>(base) + (int64_t)((uint64_t)hi32 << 32 | lo32);
-            const int r = j * C::RI + r0;
-            const uint32_t off = r0 * (uint32_t)p.a.c.row_stride * ES + (c0 ^ (V ? swz_v<C>(r) : swz_k<C>(r))) * 16;
+            const uint32_t r = j * C::RI + r0;
+            const char* at = static_cast<const char*>(base) + t.group[j * C::RI / 16] +
+                             (int64_t)(j * C::RI % 16) * p.a.c.row_stride * ES;
+            const uint32_t off = r0 * ((uint32_t)p.a.c.row_stride * ES) + (c0 ^ (V ? swz_v<C>(r) : swz_k<C>(r))) * 16;
             dma16(as_global<u32x4>(at + off), dst + j * 64);
         }
         return;
     }
-    const int dim_chunks = p.a.c.dim * ES / 16;
-    const int64_t step = p.a.c.row_stride * ES;
+    const uint32_t dim_chunks = p.a.c.dim * ES / 16;
 #pragma unroll
     for (int j = 0; j < C::NI; ++j) {
-        const int r = j * C::RI + r0;
-        const int chunk = c0 ^ (V ? swz_v<C>(r) : swz_k<C>(r));
-        int64_t at;
-        if (p.hold) {  // uniform
-            const uint32_t lo32 = __builtin_amdgcn_readlane((int)(uint32_t)t.off, j * C::RI);
-            const uint32_t hi32 = __builtin_amdgcn_readlane((int)(uint32_t)(t.off >> 32), j * C::RI);
-            at = (int64_t)((uint64_t)hi32 << 32 | lo32) + r0 * step;
-        } else {
-            const uint32_t lo32 = __shfl((int)(uint32_t)t.off, r), hi32 = __shfl((int)(uint32_t)(t.off >> 32), r);
-            at = (int64_t)((uint64_t)hi32 << 32 | lo32);
-        }
+        const uint32_t r = j * C::RI + r0;
+        const uint32_t chunk = c0 ^ (V ? swz_v<C>(r) : swz_k<C>(r));
+        const uint32_t lo32 = __shfl((int)(uint32_t)t.off, r), hi32 = __shfl((int)(uint32_t)(t.off >> 32), r);
+        const int64_t at = (int64_t)((uint64_t)hi32 << 32 | lo32);
         const bool ok = ((t.mask >> r) & 1) && chunk < dim_chunks;
         dma16(or_zero(ok, static_cast<const char*>(base) + at + chunk * 16), dst + j * 64);
     }
@@ -275,13 +296,14 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
     const int h0 = hk * group + hb * p.block_heads, nq = min(p.block_heads, group - hb * p.block_heads);
     int lo, hi;
     attn_range(a, b, &lo, &hi);
+    lo = uniform(lo), hi = uniform(hi);
     const int start = lo & ~15;
     // this wave's tiles: position start + (4 unit + wave) TK
     const int first = start + (kAttnWaves * t0 + wave) * C::TK;
     const int end = min(hi, start + t1 * C::U);
     const int nt = first < end ? (end - first + C::U - 1) / C::U : 0;
-    const int32_t* table = a.table + b * a.table_stride;
     const int64_t head = hk * a.c.head_stride;
+    AttnPages pages{a.table + b * a.table_stride, -64, nt > 0 ? page_of(p, hi - 1) : 0, 0};
 
     u32x4* kbuf = L.kv[wave];
     u32x4* vbuf = kbuf + C::STAGE / 16;
@@ -298,11 +320,8 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
             q[rt][c] = *or_zero(h < nq && d < D, a.q + b * a.q_stride + (int64_t)(h0 + h) * D + d);
         }
     AttnTile<C> tile{};
-    int page = 0;
     if (nt > 0) {
-        page = tile_page<C>(p, table, first + lane, hi);
-        tile = tile_rows<C>(p, first + lane, lo, hi, page, head);
-        page = tile_page<C>(p, table, first + C::U + lane, hi);
+        tile = tile_rows<C>(p, pages, first, lo, hi, head);
         load_stage<C, false>(p, a.c.k, tile, kbuf, lane);
         issue_fence();
         load_stage<C, true>(p, a.c.v, tile, vbuf, lane);
@@ -440,15 +459,12 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
                     }
             }
     };
-    // Loads in their order: pages of tile i + 2, keys of i + 1, values of i + 1;
-    // they land in it too, so that a wait names how many of the later ones may
-    // still be out.
+    // Loads land in their order, keys of tile i + 1 behind the values of i, so
+    // that a wait names how many of the later ones may still be out.
     for (int i = 0; i + 1 < nt; ++i) {
         vm_landed<C::NI>();  // the keys: the values were asked for after them
         scores();
-        const int pos = first + (i + 1) * C::U;
-        const AttnTile<C> next = tile_rows<C>(p, pos + lane, lo, hi, page, head);
-        page = tile_page<C>(p, table, pos + C::U + lane, hi);
+        const AttnTile<C> next = tile_rows<C>(p, pages, first + (i + 1) * C::U, lo, hi, head);
         load_stage<C, false>(p, a.c.k, next, kbuf, lane);
         issue_fence();
         weights(tile.mask);
@@ -553,18 +569,19 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(AttnPlan p
         L.found[0] = before;
     }
     __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(L.request);
+    int b = uniform(L.request);
     int64_t at = L.found[0];  // where request b begins
     for (int64_t u = u0; u < u1 && b < a.B;) {
-        const int n = attn_units<C>(a, b);
+        const int n = uniform(attn_units<C>(a, b));
         const int64_t all = (int64_t)n * p.rows;
         if (u >= at + all) {
             at += all;
             ++b;
             continue;
         }
-        const int row = (int)((u - at) / n), t0 = (int)(u - at - (int64_t)row * n);
-        const int t1 = (int)min((int64_t)n, t0 + (u1 - u));
+        // a request's units are far under 2^31, its part of a workgroup's too
+        const int row = uniform((int)((u - at) / n)), t0 = uniform((int)(u - at - (int64_t)row * n));
+        const int t1 = uniform((int)min((int64_t)n, t0 + (u1 - u)));
         const int64_t r = (int64_t)b * p.rows + row, slot = blockIdx.x + r;
         if (t0 == 0 && tid == 0) {
             const int64_t s = at + (int64_t)row * n;
@@ -704,8 +721,7 @@ hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* t
     while ((2ll << sh) < a.c.page_rows) ++sh;
     p.shift = sh;
     p.magic = a.c.page_rows > 1 ? (uint32_t)((1ull << (32 + sh)) / a.c.page_rows + 1) : 0;
-    const int chunks = s.dp * (f8 ? 1 : 2) / 16;
-    p.hold = a.c.page_rows % (64 / chunks) == 0 && a.c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
+    p.whole = a.c.page_rows % 16 == 0 && a.c.dim == s.dp && a.c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
     const size_t rows = (size_t)a.B * p.rows, slots = s.wgs + rows;
     char* ws = static_cast<char*>(a.workspace);
     p.part = reinterpret_cast<float*>(ws);
