@@ -142,18 +142,60 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t* __restr
     topk_token(logits, E, k, renorm, ids + t * k, weights + t * k, sel);
 }
 
-// The same over two launches, one wave per (expert, token) and then one
-// workgroup per token: a router too large for one CU to read quickly (512 KB:
-// 11 us in one launch, 8 in two).
+// The same over two launches, logits and then one workgroup per token: a
+// router too large for one CU to read quickly (512 KB: 11 us in one launch, 8
+// in two). A wave takes TE experts and TT tokens, so that rows in registers meet
+// several others: 64 tokens and 256 experts of width 4096 take 6.4 us as 4 x 4,
+// 13.6 as 1 x 1. Each logit is summed as dot_rows does it, whatever the tile.
+template <int TE, int TT>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t* __restrict__ X,
-                                                         const uint16_t* __restrict__ R, int H, int E,
+                                                         const uint16_t* __restrict__ R, int T, int H, int E,
                                                          double* __restrict__ logits) {
-    const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6), t = blockIdx.y;
-    if (e >= E) return;
-    double s[1];
-    dot_rows<1, 4>(X + (int64_t)t * H, R + (int64_t)e * H, H, H, lane, s);
-    wave_sum(s);
-    if (lane == 0) logits[(int64_t)t * E + e] = s[0];
+    constexpr int CH = TE * TT == 1 ? 4 : 2;  // pieces of a row in flight
+    const int lane = threadIdx.x & 63, e0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * TE, t0 = blockIdx.y * TT;
+    if (e0 >= E) return;
+    double s[TE][TT];
+#pragma unroll
+    for (int e = 0; e < TE; ++e)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) s[e][t] = 0.0;
+    for (int k0 = lane * 8; k0 < H; k0 += 512 * CH) {
+        u32x4 a[TE][CH], b[TT][CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = k0 + 512 * c;
+#pragma unroll
+            for (int e = 0; e < TE; ++e) a[e][c] = *or_zero(k < H, R + (int64_t)min(e0 + e, E - 1) * H + k);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) b[t][c] = *or_zero(k < H, X + (int64_t)min(t0 + t, T - 1) * H + k);
+        }
+        issue_fence();
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    double x[TE], y[TT];
+#pragma unroll
+                    for (int e = 0; e < TE; ++e)
+                        x[e] = (double)__uint_as_float(h ? a[e][c][i] & 0xffff0000u : a[e][c][i] << 16);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t)
+                        y[t] = (double)__uint_as_float(h ? b[t][c][i] & 0xffff0000u : b[t][c][i] << 16);
+#pragma unroll
+                    for (int e = 0; e < TE; ++e)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) s[e][t] = __builtin_fma(y[t], x[e], s[e][t]);
+                }
+    }
+#pragma unroll
+    for (int e = 0; e < TE; ++e) wave_sum(s[e]);
+#pragma unroll
+    for (int e = 0; e < TE; ++e)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+            if (lane == 0 && e0 + e < E && t0 + t < T) logits[(int64_t)(t0 + t) * E + e0 + e] = s[e][t];
 }
 
 __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict__ logits, int E, int k, int renorm,
@@ -174,9 +216,12 @@ __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict
 // are their s, divided by its sum where renorm, times scale. Everything is
 // held in 64 bits, and every choice is by rank, as in topk_token: equal values
 // to the lower index, NaN below every number.
+// Above INT64_MIN, so that experts that are not left rank behind every NaN.
+__device__ __forceinline__ int64_t score_key(double c) { return max(rank_key(c), INT64_MIN + 1); }
+constexpr int64_t kNotLeft = INT64_MIN;
 struct ScoredLds {
     double logits[kMoeMaxExperts];  // then the scores
-    int64_t key[kMoeMaxExperts];    // of c
+    int64_t key[kMoeMaxExperts];    // of c; of experts that are not left kNotLeft
     double best[kMoeMaxExperts];    // [groups][group_best] largest c
     int left[kMoeMaxExperts];       // is this group left?
     double sel[kMoeMaxK];
@@ -199,7 +244,7 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
         const double l = L.logits[tid];
         s = r.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / den;
         c = r.bias ? s + (double)r.bias[tid] : s;
-        L.key[tid] = rank_key(c);
+        L.key[tid] = score_key(c);
     }
     __syncthreads();
     if (tid < E) L.logits[tid] = s;
@@ -209,12 +254,13 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
             const int g0 = tid / n * n;
             const int64_t mine = L.key[tid];
             int before = 0;
+#pragma unroll 4
             for (int j = g0; j < g0 + n; ++j) before += L.key[j] > mine || (L.key[j] == mine && j < tid);
             if (before < best) L.best[tid / n * best + before] = c;
         }
         __syncthreads();
         if (tid < r.groups) {
-            auto value = [&](int g) { return rank_key(best == 2 ? L.best[2 * g] + L.best[2 * g + 1] : L.best[g]); };
+            auto value = [&](int g) { return score_key(best == 2 ? L.best[2 * g] + L.best[2 * g + 1] : L.best[g]); };
             const int64_t mine = value(tid);
             int before = 0;
             for (int g = 0; g < r.groups; ++g) {
@@ -223,18 +269,18 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
             }
             L.left[tid] = before < r.top_groups;
         }
-    } else if (tid == 0) {
-        L.left[0] = 1;
+        __syncthreads();
+        if (tid < E && !L.left[tid / n]) L.key[tid] = kNotLeft;
     }
     __syncthreads();
     const int rt = E <= 64 ? 16 : E <= 128 ? 8 : E <= 256 ? 4 : 2;  // threads per expert, neighbours in a wave
     const int e = tid / rt, part = tid % rt;
-    const bool on = e < E && L.left[e / n];
+    const int64_t mine = e < E ? L.key[e] : kNotLeft;
+    const bool on = mine != kNotLeft;
     int before = 0;
     if (on) {
-        const int64_t mine = L.key[e];
-        for (int j = part; j < E; j += rt)
-            before += L.left[j / n] && (L.key[j] > mine || (L.key[j] == mine && j < e));
+#pragma unroll 4
+        for (int j = part; j < E; j += rt) before += L.key[j] > mine || (L.key[j] == mine && j < e);
     }
     for (int o = 1; o < rt; o <<= 1) before += __shfl_xor(before, o);
     if (on && part == 0 && before < k) {
@@ -700,14 +746,23 @@ size_t moe_route_workspace(int T, int H, int E) {
     return (int64_t)E * H <= kMoeRouteOne ? 0 : (size_t)T * E * sizeof(double);
 }
 
+static hipError_t moe_logits(const uint16_t* X, const uint16_t* router, int T, int H, int E, double* logits,
+                             hipStream_t st, StageTimer* tm) {
+    // tiles of 4 x 4 where they still are two waves a CU, of 1 x 1 otherwise
+    if ((int64_t)T * E >= 16 * 512)
+        return launch(tm, "moe_logits", moe_logits_kernel<4, 4>, dim3((E + 15) / 16, (T + 3) / 4), dim3(256), st, X,
+                      router, T, H, E, logits);
+    return launch(tm, "moe_logits", moe_logits_kernel<1, 1>, dim3((E + 3) / 4, T), dim3(256), st, X, router, T, H, E,
+                  logits);
+}
+
 hipError_t moe_route(const uint16_t* X, const uint16_t* router, int T, int H, int E, int k, int renorm, int32_t* ids,
                      float* weights, void* workspace, hipStream_t st, StageTimer* tm) {
     if ((int64_t)E * H <= kMoeRouteOne)
         return launch(tm, "moe_route", moe_route_kernel, dim3(T), dim3(1024), st, X, router, H, E, k, renorm, ids,
                       weights);
     double* logits = static_cast<double*>(workspace);
-    hipError_t e = launch(tm, "moe_logits", moe_logits_kernel, dim3((E + 3) / 4, T), dim3(256), st, X, router, H, E,
-                          logits);
+    hipError_t e = moe_logits(X, router, T, H, E, logits, st, tm);
     if (e != hipSuccess) return e;
     return launch(tm, "moe_topk", moe_topk_kernel, dim3(T), dim3(1024), st, (const double*)logits, E, k, renorm, ids,
                   weights);
@@ -720,8 +775,7 @@ hipError_t moe_route_scored(const uint16_t* X, const uint16_t* router, int T, in
         return launch(tm, "moe_scored", moe_scored_kernel, dim3(T), dim3(1024), st, X, router, H, E, k, r, ids,
                       weights);
     double* logits = static_cast<double*>(workspace);
-    hipError_t e = launch(tm, "moe_logits", moe_logits_kernel, dim3((E + 3) / 4, T), dim3(256), st, X, router, H, E,
-                          logits);
+    hipError_t e = moe_logits(X, router, T, H, E, logits, st, tm);
     if (e != hipSuccess) return e;
     return launch(tm, "moe_scored_topk", moe_scored_topk_kernel, dim3(T), dim3(1024), st, (const double*)logits, E, k,
                   r, ids, weights);

@@ -852,13 +852,16 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCacheDesc:
     pages, rows, heads, dim = shape
     if pages < 1 or rows < 1 or heads < 1 or dim < 1 or strides[3] != 1:
         raise ValueError("a cache needs a page, a row and a head, and a contiguous last dimension")
-    # a dimension of one element has any stride
-    s = [n if m > 1 else dim for n, m in zip(strides, shape)]
-    extent = 0
-    for st, m in sorted((n, m) for n, m in zip(s, shape[:3]) if m > 1):
-        if st < max(extent, dim):
-            raise ValueError(f"rows of the cache overlap (shape {tuple(shape)}, strides {tuple(strides)})")
-        extent = st * m
+    if strides[0] == rows * heads * dim and strides[1] == heads * dim and strides[2] == dim:
+        s = strides
+    else:
+        # a dimension of one element has any stride
+        s = [n if m > 1 else dim for n, m in zip(strides, shape)]
+        extent = 0
+        for st, m in sorted((n, m) for n, m in zip(s, shape[:3]) if m > 1):
+            if st < max(extent, dim):
+                raise ValueError(f"rows of the cache overlap (shape {tuple(shape)}, strides {tuple(strides)})")
+            extent = st * m
     if not f8:
         if k_scale is not None or v_scale is not None:
             raise ValueError("scales belong to an 8-bit cache")
