@@ -68,6 +68,35 @@ __device__ __forceinline__ float hi_half(float v) {
     return __builtin_amdgcn_fmed3f(v, -kMax, kMax);
 }
 
+// The value of lane ^ O, by moves among vector registers (a shuffle through LDS
+// holds it for 16 cycles; a step of a 1024-thread sort takes 220 ns so).
+template <int O>
+__device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
+    static_assert(O == 1 || O == 2 || O == 4 || O == 8 || O == 16 || O == 32, "one bit of the lane");
+    const int x = (int)v;
+    if constexpr (O == 1) return __builtin_amdgcn_mov_dpp(x, 0xb1, 0xf, 0xf, true);  // quads 1 0 3 2
+    if constexpr (O == 2) return __builtin_amdgcn_mov_dpp(x, 0x4e, 0xf, 0xf, true);  // quads 2 3 0 1
+    if constexpr (O == 4)  // half rows mirrored (^ 7), then quads 3 2 1 0 (^ 3)
+        return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
+    if constexpr (O == 8) return __builtin_amdgcn_mov_dpp(x, 0x128, 0xf, 0xf, true);  // rows turned by 8
+    if constexpr (O == 16) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? p[0] : p[1];
+    }
+    if constexpr (O == 32) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? p[0] : p[1];
+    }
+}
+template <int O, class T>
+__device__ __forceinline__ T lane_xor(T v) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, lane_xor32<O>(__builtin_bit_cast(uint32_t, v)));
+    } else {
+        const u32x2 x = __builtin_bit_cast(u32x2, v);
+        return __builtin_bit_cast(T, u32x2{lane_xor32<O>(x[0]), lane_xor32<O>(x[1])});
+    }
+}
 // 16x16x32 bf16 matrix-core product: lane l supplies row (l % 16) of the
 // left operand and column (l % 16) of the right one, 8 consecutive k each
 // (k = 8 * (l / 16) + e); lane l receives rows 4 * (l / 16) + i, column l % 16.

@@ -55,12 +55,31 @@ __device__ __forceinline__ void dot_rows(const uint16_t* __restrict__ xp, const 
                 }
     }
 }
+template <int O, int NE>
+__device__ __forceinline__ void sum_steps(double (&s)[NE]) {
+#pragma unroll
+    for (int e = 0; e < NE; ++e) s[e] += lane_xor<O>(s[e]);
+    if constexpr (O > 1) sum_steps<O / 2>(s);
+}
 template <int NE>
 __device__ __forceinline__ void wave_sum(double (&s)[NE]) {
+    sum_steps<32>(s);
+}
+// The same sums of 16 values, s[i] in the lanes 4 i to 4 i + 3: every step down
+// to lane ^ 4 halves how many values a lane goes on with.
+template <int O, int N>
+__device__ __forceinline__ double wave_sum16(double (&s)[N]) {
+    if constexpr (N > 1) {
+        double h[N / 2];
+        const bool up = threadIdx.x & O;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-#pragma unroll
-        for (int e = 0; e < NE; ++e) s[e] += __shfl_xor(s[e], o);
+        for (int i = 0; i < N / 2; ++i)
+            h[i] = (up ? s[i + N / 2] : s[i]) + lane_xor<O>(up ? s[i] : s[i + N / 2]);
+        return wave_sum16<O / 2>(h);
+    } else {
+        sum_steps<O>(s);
+        return s[0];
+    }
 }
 
 // The order of logits as signed integers: NaN below every number, -0 as 0.
@@ -145,7 +164,7 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const uint16_t* __restr
 // The same over two launches, logits and then one workgroup per token: a
 // router too large for one CU to read quickly (512 KB: 11 us in one launch, 8
 // in two). A wave takes TE experts and TT tokens, so that rows in registers meet
-// several others: 64 tokens and 256 experts of width 4096 take 6.4 us as 4 x 4,
+// several others: 64 tokens and 256 experts of width 4096 take 6.8 us as 4 x 4,
 // 13.6 as 1 x 1. Each logit is summed as dot_rows does it, whatever the tile.
 template <int TE, int TT>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t* __restrict__ X,
@@ -189,13 +208,18 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const uint16_t* __restr
                         for (int t = 0; t < TT; ++t) s[e][t] = __builtin_fma(y[t], x[e], s[e][t]);
                 }
     }
+    if constexpr (TE * TT == 16) {
+        double v[16];
 #pragma unroll
-    for (int e = 0; e < TE; ++e) wave_sum(s[e]);
-#pragma unroll
-    for (int e = 0; e < TE; ++e)
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-            if (lane == 0 && e0 + e < E && t0 + t < T) logits[(int64_t)(t0 + t) * E + e0 + e] = s[e][t];
+        for (int i = 0; i < 16; ++i) v[i] = s[i % TE][i / TE];
+        v[0] = wave_sum16<32>(v);
+        const int i = lane >> 2, e = e0 + i % TE, t = t0 + i / TE;
+        if ((lane & 3) == 0 && e < E && t < T) logits[(int64_t)t * E + e] = v[0];
+    } else {
+        static_assert(TE * TT == 1, "16 logits a wave, or one");
+        wave_sum(s[0]);
+        if (lane == 0) logits[(int64_t)t0 * E + e0] = s[0][0];
+    }
 }
 
 __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict__ logits, int E, int k, int renorm,
@@ -216,9 +240,21 @@ __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict
 // are their s, divided by its sum where renorm, times scale. Everything is
 // held in 64 bits, and every choice is by rank, as in topk_token: equal values
 // to the lower index, NaN below every number.
-// Above INT64_MIN, so that experts that are not left rank behind every NaN.
-__device__ __forceinline__ int64_t score_key(double c) { return max(rank_key(c), INT64_MIN + 1); }
+// Above INT64_MIN + 1, so that experts that are not left rank behind every NaN
+// (and a key less 1 is one).
+__device__ __forceinline__ int64_t score_key(double c) { return max(rank_key(c), INT64_MIN + 2); }
 constexpr int64_t kNotLeft = INT64_MIN;
+// How many of keys from, from + step, ... below `end` come before number e: larger,
+// or equal at a lower index. (One comparison a key: up to e with a number less.)
+__device__ __forceinline__ int ranked_before(const int64_t* key, int from, int end, int step, int e) {
+    const int64_t mine = key[e];
+    int before = 0, j = from;
+#pragma unroll 4
+    for (; j < min(e, end); j += step) before += key[j] > mine - 1;
+#pragma unroll 4
+    for (; j < end; j += step) before += key[j] > mine;
+    return before;
+}
 struct ScoredLds {
     double logits[kMoeMaxExperts];  // then the scores
     int64_t key[kMoeMaxExperts];    // of c; of experts that are not left kNotLeft
@@ -251,11 +287,7 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
     const int best = min(r.group_best, n);
     if (r.groups > 1) {
         if (tid < E) {
-            const int g0 = tid / n * n;
-            const int64_t mine = L.key[tid];
-            int before = 0;
-#pragma unroll 4
-            for (int j = g0; j < g0 + n; ++j) before += L.key[j] > mine || (L.key[j] == mine && j < tid);
+            const int g0 = tid / n * n, before = ranked_before(L.key, g0, g0 + n, 1, tid);
             if (before < best) L.best[tid / n * best + before] = c;
         }
         __syncthreads();
@@ -275,13 +307,8 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
     __syncthreads();
     const int rt = E <= 64 ? 16 : E <= 128 ? 8 : E <= 256 ? 4 : 2;  // threads per expert, neighbours in a wave
     const int e = tid / rt, part = tid % rt;
-    const int64_t mine = e < E ? L.key[e] : kNotLeft;
-    const bool on = mine != kNotLeft;
-    int before = 0;
-    if (on) {
-#pragma unroll 4
-        for (int j = part; j < E; j += rt) before += L.key[j] > mine || (L.key[j] == mine && j < e);
-    }
+    const bool on = e < E && L.key[e] != kNotLeft;
+    int before = on ? ranked_before(L.key, part, E, rt, e) : 0;
     for (int o = 1; o < rt; o <<= 1) before += __shfl_xor(before, o);
     if (on && part == 0 && before < k) {
         ids[before] = e;

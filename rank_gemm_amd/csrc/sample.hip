@@ -125,35 +125,6 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t v, int src) {
     return (uint64_t)(uint32_t)__shfl((int)(uint32_t)v, src) |
            (uint64_t)(uint32_t)__shfl((int)(uint32_t)(v >> 32), src) << 32;
 }
-// The value of lane ^ O, by moves among vector registers (through LDS a step of
-// a 1024-thread sort takes 220 ns).
-template <int O>
-__device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
-    static_assert(O == 1 || O == 2 || O == 4 || O == 8 || O == 16 || O == 32, "one bit of the lane");
-    const int x = (int)v;
-    if constexpr (O == 1) return __builtin_amdgcn_mov_dpp(x, 0xb1, 0xf, 0xf, true);  // quads 1 0 3 2
-    if constexpr (O == 2) return __builtin_amdgcn_mov_dpp(x, 0x4e, 0xf, 0xf, true);  // quads 2 3 0 1
-    if constexpr (O == 4)  // half rows mirrored (^ 7), then quads 3 2 1 0 (^ 3)
-        return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
-    if constexpr (O == 8) return __builtin_amdgcn_mov_dpp(x, 0x128, 0xf, 0xf, true);  // rows turned by 8
-    if constexpr (O == 16) {
-        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-        return threadIdx.x & 16 ? p[0] : p[1];
-    }
-    if constexpr (O == 32) {
-        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        return threadIdx.x & 32 ? p[0] : p[1];
-    }
-}
-template <int O, class T>
-__device__ __forceinline__ T lane_xor(T v) {
-    if constexpr (sizeof(T) == 4) {
-        return __builtin_bit_cast(T, lane_xor32<O>(__builtin_bit_cast(uint32_t, v)));
-    } else {
-        const u32x2 x = __builtin_bit_cast(u32x2, v);
-        return __builtin_bit_cast(T, u32x2{lane_xor32<O>(x[0]), lane_xor32<O>(x[1])});
-    }
-}
 // f over all lanes of a wave (f of two values, in any order).
 template <class T, class F>
 __device__ __forceinline__ T wave_all(T v, F f) {
