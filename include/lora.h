@@ -568,6 +568,7 @@ int lora_moe_route_scored(const void* x, const void* router, int T, int H, int E
 #define LORA_F8 3 /* a form of a cache, not of a pool */
 #define LORA_ATTN_MAX_DIM 256
 #define LORA_ATTN_MAX_BATCH 65535
+#define LORA_ATTN_MAX_ROWS 4194304 /* requests times heads */
 typedef struct lora_kv_cache {
     void *k, *v;
     const float *k_scale, *v_scale; /* LORA_F8 only */
@@ -585,9 +586,9 @@ typedef struct lora_kv_cache {
  *   rows   dev int64 [T]; a token whose row is outside the cache (-1, for a
  *          padded place of the batch) is not stored. Rows that are named twice
  *          hold pieces of either token.
- * Every other row of the cache is left as it was. Asynchronous on `stream`.
- * Errors: LORA_EINVAL (sizes, null, misaligned or equal pointers), LORA_EHIP.
- * T == 0 launches nothing.
+ * Every other row of the cache is left as it was; k, v and rows must not lie in
+ * it. Asynchronous on `stream`. Errors: LORA_EINVAL (sizes, null, misaligned or
+ * equal pointers), LORA_EHIP. T == 0 launches nothing.
  */
 int lora_kv_append(const lora_kv_cache* cache, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                    const int64_t* rows, int T, void* stream);
@@ -607,16 +608,19 @@ int lora_kv_append(const lora_kv_cache* cache, const void* k, const void* v, int
  *            boundaries
  *   lse      dev float [B][heads] out, or null: log sum_j exp(scale q . k_j)
  *   workspace dev, at least lora_attn_decode_workspace_bytes(...) bytes (0 for
- *            some sizes: it may then be null)
+ *            some sizes: it may then be null), on a 16-byte boundary; calls that
+ *            may overlap need separate ones
  * Positions whose page number is outside [0, n_pages) are left out. A request
  * without a position (length 0, or all left out) gets zeros and an lse of
  * -infinity. Scores, sums and outputs are held in fp32, out is rounded once;
- * a cache row that holds a NaN at an attended position gives NaN. The order of
- * sums depends on the lengths of the whole batch, not on time: equal inputs
- * give equal bits. No output may overlap an input, the workspace or another
+ * a cache row that holds a NaN or an infinity at an attended position gives NaN
+ * (in the dimensions where v does, in all where k does); what lies elsewhere in
+ * the cache is not read. The order of sums depends on the lengths of the whole
+ * batch, not on time: equal inputs give equal bits. No output may overlap an input, the workspace or another
  * output. Asynchronous on `stream`. Errors: LORA_EINVAL (sizes, a heads that
- * is no multiple of kv_heads, width * page_rows past 2^30, a scale that is not
- * finite, null, misaligned or equal pointers), LORA_ESPACE, LORA_EHIP. B == 0
+ * is no multiple of kv_heads, B over LORA_ATTN_MAX_BATCH, B * heads over
+ * LORA_ATTN_MAX_ROWS, width * page_rows past 2^30, a scale that is not finite or
+ * leaves fp32 times log2(e), null, misaligned or equal pointers), LORA_ESPACE, LORA_EHIP. B == 0
  * launches nothing.
  */
 size_t lora_attn_decode_workspace_bytes(int B, int heads, int kv_heads, int dim, int width, int page_rows);
@@ -642,7 +646,8 @@ int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride
  *            top_k < 1, top_p >= 1 and min_p <= 0 (or NaN) filter nothing;
  *            top_p <= 0 leaves the first token.
  *   ids      dev int32 [B] out;  probs  dev float [B] out
- *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes
+ *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes, on a 16-byte
+ *            boundary; calls that may overlap need separate ones
  * Tokens whose logit is NaN or -infinity are never drawn; where there is no
  * other, ids[b] = -1 and probs[b] = 0. Among logits of +infinity all weigh the
  * same, and nothing else does. Weights are 64-bit exponentials, rounded to

@@ -205,7 +205,7 @@ inline lora::KvCache kernel_cache(const lora_kv_cache& c) {
 }
 inline bool attn_sizes(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
     return B >= 0 && B <= LORA_ATTN_MAX_BATCH && kv_heads >= 1 && heads >= kv_heads && heads <= 65535 &&
-           (int64_t)B * heads <= INT32_MAX && heads % kv_heads == 0 && dim >= 1 && dim <= LORA_ATTN_MAX_DIM && width >= 1 && page_rows >= 1 &&
+           (int64_t)B * heads <= LORA_ATTN_MAX_ROWS && heads % kv_heads == 0 && dim >= 1 && dim <= LORA_ATTN_MAX_DIM && width >= 1 && page_rows >= 1 &&
            width <= (1 << 30) / page_rows;
 }
 
@@ -760,12 +760,13 @@ int lora_moe_route_scored(const void* x, const void* router, int T, int H, int E
         k > r->top_groups * (E / r->groups) || r->group_best < 1 || r->group_best > 2 || !std::isfinite(r->scale))
         return LORA_EINVAL;
     if (T == 0) return LORA_OK;
-    if (!x || !router || !ids || !weights || !aligned(x, 16) || !aligned(router, 16)) return LORA_EINVAL;
+    if (!x || !router || !ids || !weights || !aligned(x, 16) || !aligned(router, 16) || !aligned(r->bias, 4))
+        return LORA_EINVAL;
     const size_t need = lora_moe_route_workspace_bytes(T, H, E);
     if (need > 0 && (!workspace || !aligned(workspace, 8) || workspace_bytes < need)) return LORA_ESPACE;
     const void* out[2] = {ids, weights};
     for (const void* o : out)
-        if (o == x || o == router || o == r->bias) return LORA_EINVAL;
+        if (o == x || o == router || o == r->bias || (need > 0 && o == workspace)) return LORA_EINVAL;
     if (out[0] == out[1]) return LORA_EINVAL;
     hipStream_t st = as_stream(stream);
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
@@ -783,8 +784,8 @@ int lora_kv_append(const lora_kv_cache* c, const void* k, const void* v, int64_t
     int rc = check_cache(c);
     if (rc != LORA_OK) return rc;
     const int64_t row = (int64_t)c->kv_heads * c->dim;
-    // a workgroup per 256 pieces of 8 values
-    if (T < 0 || row / 8 > INT32_MAX || (int64_t)T * (row / 8) > (int64_t)INT32_MAX * 256) return LORA_EINVAL;
+    // a thread per piece of 8 values: a grid holds fewer than 2^32
+    if (T < 0 || row > INT32_MAX || (int64_t)T * (row / 8) > (int64_t)UINT32_MAX - 255) return LORA_EINVAL;
     for (int64_t s : {k_stride, v_stride})
         if (s < row || s % 8 != 0) return LORA_EINVAL;
     if (T == 0) return LORA_OK;
@@ -812,7 +813,8 @@ int lora_attn_decode(const lora_kv_cache* c, const void* q, int64_t q_stride, in
     int rc = check_cache(c);
     if (rc != LORA_OK) return rc;
     if (!attn_sizes(B, heads, c->kv_heads, c->dim, width, c->page_rows) || !std::isfinite(scale) || window < 0 ||
-        q_stride < (int64_t)heads * c->dim || q_stride % 8 != 0 || table_stride < width)
+        !std::isfinite((float)((double)scale * 1.4426950408889634)) || q_stride < (int64_t)heads * c->dim ||
+        q_stride % 8 != 0 || table_stride < width)
         return LORA_EINVAL;
     if (B == 0) return LORA_OK;
     if (!q || !table || !lengths || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) ||
@@ -845,7 +847,7 @@ int lora_sample(int dtype, const void* logits, int64_t stride, int B, int V, con
         return LORA_EINVAL;
     if (B == 0) return LORA_OK;
     if (!logits || !u || !ids || !probs || !aligned(logits, es_of(dtype)) || !aligned(u, 8) || !aligned(ids, 4) ||
-        !aligned(probs, 4))
+        !aligned(probs, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4))
         return LORA_EINVAL;
     const size_t need = lora_sample_workspace_bytes(B, V);
     if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LORA_ESPACE;

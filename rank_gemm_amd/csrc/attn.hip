@@ -25,6 +25,14 @@
 //
 // Positions whose page is outside the cache are left out, so no table makes a
 // kernel read past it; nothing past a request's length is read either.
+//
+// Bound by HBM: 64 requests of 4096 to 16384 positions, 32 heads over 8 of 128,
+// bf16 (2.7 GB) 471 us, 5.7 TB/s (a 1 GiB copy moves 5.1); without the second
+// halves of P it is no faster. Rows of 128 bytes of a head (8-bit, [page][row]
+// [head]) come at 5.0 TB/s; of 64 bytes at 3.3, as the other half of each
+// 128-byte line is another head's, which another workgroup reads at its own
+// time. 1 request of 131072 positions, 8-bit (268 MB): 57 us and 4 for the join;
+// some 8 us of every call are its beginning and end.
 #include <algorithm>
 
 #include "fuse.h"
@@ -66,6 +74,9 @@ struct AttnCfg {
     static constexpr int NI = STAGE / 1024;  // load instructions a stage
     static constexpr int RI = 64 / CH;       // rows a load instruction
     static constexpr int U = kAttnWaves * TK;
+    // waves a SIMD to compile for: 2 leaves 256 registers, where the products take
+    // vector registers alone and o is not copied to and fro
+    static constexpr int MinWaves = DP * RT <= 128 ? 2 : 1;
 };
 
 // Chunk c of row r lies at chunk c ^ swizzle(r) of its row, so that the reads
@@ -527,7 +538,7 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
 }
 
 template <class C>
-__global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(AttnPlan p) {
+__global__ __launch_bounds__(64 * kAttnWaves, C::MinWaves) void attn_decode_kernel(AttnPlan p) {
     __shared__ AttnLds<C> L;
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -594,7 +605,7 @@ __global__ __launch_bounds__(64 * kAttnWaves) void attn_decode_kernel(AttnPlan p
 
 // Rows of more than one piece joined, rows without a position written as
 // zeros. A workgroup takes all heads of a row, or one where there are few rows
-// (8 rows of 64 pieces: 6.4 us with all, 3.0 with one): its threads 4
+// (8 rows of 64 pieces: 6.4 us with all, 4.3 with one): its threads 4
 // dimensions of a head each, and where there are few of those, several share a
 // head's pieces.
 constexpr int kJoinThreads = 512;

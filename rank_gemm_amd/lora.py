@@ -46,7 +46,7 @@ LORA_DEVICE_PLAN_MAX_SLOTS = 4096
 LORA_NOALLOC_MAX_WORKSPACE = 32 << 20
 LORA_MAX_SLICES = 4
 LORA_MOE_MAX_EXPERTS, LORA_MOE_MAX_K, LORA_MOE_MAX_PAIRS = 512, 16, 512
-LORA_ATTN_MAX_DIM, LORA_ATTN_MAX_BATCH = 256, 65535
+LORA_ATTN_MAX_DIM, LORA_ATTN_MAX_BATCH, LORA_ATTN_MAX_ROWS = 256, 65535, 4194304
 LORA_SAMPLE_MAX_VOCAB, LORA_SAMPLE_MAX_BATCH = 4194304, 65535
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -633,14 +633,23 @@ def _same_device(*named):
     return dev
 
 
+def _on(dev, *tensors) -> bool:
+    """Whether every tensor given is on ``dev`` (None for one that is not there)."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            return False
+    return True
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(dev, fn, what: str, *args):
     """One call of the library on ``dev``'s current stream, with ``dev`` the
     current device (a decode step makes many such calls: the stream's handle
     is fetched without building a Stream object where torch offers it)."""
-    if torch.cuda.current_device() != dev.index:
+    if _get_device() != dev.index:
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(dev))
     else:
@@ -840,10 +849,10 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCacheDesc:
     """The descriptor of a cache given as tensors [pages, page_rows, kv_heads,
     dim] of any strides (the last dimension contiguous, alike for both)."""
     dt = getattr(k_cache, "dtype", None)
-    f8 = dt == torch.float8_e4m3fn
-    if not f8 and dt != torch.bfloat16:
+    f8 = dt is torch.float8_e4m3fn
+    if not f8 and dt is not torch.bfloat16:
         raise ValueError(f"k_cache must be bf16 or float8_e4m3fn, got {dt}")
-    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype != dt:
+    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype is not dt:
         raise ValueError("k_cache and v_cache must be device tensors of one type")
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides:
@@ -899,7 +908,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if v.shape[0] != T:
         raise ValueError(f"k has {T} tokens, v {v.shape[0]}")
     _dev_tensor(rows, torch.int64, "rows", (T,))
-    dev = _same_device(("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("rows", rows))
+    dev = k.device
+    if not _on(dev, v, k_cache, v_cache, rows):
+        _same_device(("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("rows", rows))
     _call(dev, lib().lora_kv_append, "lora_kv_append", ctypes.byref(d), k.data_ptr(), v.data_ptr(), sk, sv,
           rows.data_ptr(), T)
 
@@ -927,8 +938,10 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
         out = torch.empty((B, heads, dim), dtype=torch.bfloat16, device=q.device)
     _dev_tensor(out, torch.bfloat16, "out", (B, heads, dim))
     sums = torch.empty((B, heads), dtype=torch.float32, device=q.device) if lse else None
-    dev = _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("table", table), ("lengths", lengths),
-                       ("out", out))
+    dev = q.device
+    if not _on(dev, k_cache, v_cache, table, lengths, out):
+        _same_device(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("table", table), ("lengths", lengths),
+                     ("out", out))
     L = lib()
     n = L.lora_attn_decode_workspace_bytes(B, heads, d.kv_heads, d.dim, width, d.page_rows)
     keep, ws, nb = _space(workspace, n, dev) if n else (None, None, 0)

@@ -51,7 +51,7 @@ def test_cache_refuses(bad):
 
 @pytest.mark.parametrize("bad", [dict(T=-1), dict(k=None), dict(v=None), dict(rows=None), dict(k=P16 + 8200),
                                  dict(v=P16 + 8), dict(rows=P16 + 4), dict(ks=120), dict(vs=132), dict(k=P16),
-                                 dict(v=Q16), dict(rows=P16)])
+                                 dict(v=Q16), dict(rows=P16), dict(T=2 ** 31 - 1)])
 def test_append_refuses(bad):
     assert append(cache(), **bad) == lora.LORA_EINVAL
 
@@ -59,6 +59,7 @@ def test_append_refuses(bad):
 @pytest.mark.parametrize("bad", [
     dict(B=-1), dict(B=65536), dict(heads=3), dict(heads=0), dict(heads=65536), dict(width=0), dict(width=1 << 27),
     dict(ts=7), dict(qs=200), dict(qs=260), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1),
+    dict(B=40000, heads=128, qs=128 * 64), dict(scale=3e38),
     dict(q=None), dict(q=P16 + 8200), dict(table=None), dict(table=P16 + 2), dict(lengths=None), dict(out=None),
     dict(out=P16 + 8), dict(lse=P16 + 2), dict(out=P16), dict(out=Q16), dict(out=P16 + 8192), dict(lse=P16 + 16384),
     dict(lse=P16 + 20480), dict(lse=P16 + 32768)])
@@ -102,7 +103,8 @@ def route(scores=None, **kw):
     (dict(router=Q16 + 2), -1), (dict(ids=None), -1), (dict(weights=None), -1), (dict(score=2), -1),
     (dict(groups=0), -1), (dict(groups=3), -1), (dict(top_groups=0), -1), (dict(top_groups=3), -1), (dict(k=5), -1),
     (dict(group_best=0), -1), (dict(group_best=3), -1), (dict(scale=float("inf")), -1), (dict(ids=P16), -1),
-    (dict(ids=P16 + 12288), -1), (dict(bias=P16 + 12288), -1), (dict(H=8192, E=64), -6),
+    (dict(ids=P16 + 12288), -1), (dict(bias=P16 + 12288), -1), (dict(bias=P16 + 2), -1),
+    (dict(H=8192, E=64), -6), (dict(H=8192, E=64, ws=P16 + 8192, wsb=1 << 20), -1),
     (dict(H=8192, E=64, ws=P16, wsb=8), -6)])
 def test_route_refuses(bad, want):
     assert route(**bad) == want
@@ -124,6 +126,7 @@ def draw(**kw):
     dict(dtype=2), dict(B=-1), dict(B=65536), dict(V=0), dict(V=4194305, stride=4194305), dict(stride=99),
     dict(logits=None), dict(logits=P16 + 1), dict(u=None), dict(u=Q16 + 4), dict(ids=None), dict(ids=P16 + 8194),
     dict(probs=None), dict(probs=P16 + 8194), dict(ids=P16), dict(probs=Q16), dict(ids=P16 + 12288),
+    dict(temperature=P16 + 2), dict(top_k=P16 + 1),
     dict(temperature=P16 + 8192), dict(top_k=P16 + 8192), dict(top_p=P16 + 12288), dict(min_p=P16 + 12288)])
 def test_sample_refuses(bad):
     assert draw(**bad) == lora.LORA_EINVAL
