@@ -202,7 +202,7 @@ struct Row {
 __host__ __device__ inline int sample_tiles(int V) { return (V + 7 + kTile - 1) / kTile; }
 
 constexpr int kBins = 2048;
-constexpr int kList = 1024;  // tokens of a border's bin that are ranked
+constexpr int kList = 2048;  // tokens of a border's bin that are ranked, or of a list that is sorted
 
 // What the kernels leave for one another, in the workspace.
 struct RowState {
@@ -306,9 +306,12 @@ struct Scale {
     __device__ __forceinline__ int bin(float v) const { return (int)fminf((top - v) * per, (float)(kBins - 1)); }
 };
 // Of top_k: down to the lowest tile's largest logit, which the border is not
-// below where there are at least k tiles, otherwise twice as far.
+// below where there are at least k tiles; otherwise twice as far, or 24 (logits
+// of a vocabulary spread over some tens; a border past the last bin is found
+// too, by one workgroup: 5 rows of 3001, top_k 50, 66 us where reach falls short
+// of it, 25 us where not).
 __device__ __forceinline__ Scale scale_of_count(const Ask& r) {
-    const float reach = (r.top - r.under) * (r.k <= r.live ? 1.f : 2.f);
+    const float reach = r.k <= r.live ? r.top - r.under : fmaxf(2.f * (r.top - r.under), 24.f);
     return Scale{r.top, r.top == INFINITY ? 0.f : fminf((kBins - 2) / fmaxf(reach, 1e-30f), 1e30f)};
 }
 // Of top_p: the tokens behind the border weigh at least 1 - p of the whole,
@@ -622,6 +625,7 @@ constexpr int kBorderNT = 1024;
 struct BorderLds {
     uint64_t bins[kBins];
     uint64_t list[kList];
+    uint64_t space[kBorderNT];
     BlockLds<kBorderNT> block;
 };
 
@@ -681,16 +685,29 @@ __device__ __forceinline__ Prefix nth_equal(const Row<BF16>& row, const float* t
 // histograms until few are left, which are ranked.
 template <class Weight>
 __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want, Weight weight, BorderLds& L) {
+    constexpr int M = kList / kBorderNT;
     const int tid = threadIdx.x, lane = tid & 63;
-    const uint64_t mine = tid < n ? L.list[tid] : 0;
-    const uint64_t w = tid < n ? weight(token_logit(mine)) : 0;
-    uint64_t low = 0, high = ~0ull;  // the border is in [low, high]
+    uint64_t mine[M], w[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int i = tid + m * kBorderNT;
+        mine[m] = i < n ? L.list[i] : 0;  // no token is 0
+        w[m] = i < n ? weight(token_logit(mine[m])) : 0;
+    }
+    uint64_t low = 1, high = ~0ull;  // the border is in [low, high]
     for (;;) {
-        const bool in = tid < n && mine >= low && mine <= high;
         // how many are left, and their range
-        const uint64_t lo = wave_all(in ? mine : ~(uint64_t)0, [](uint64_t a, uint64_t b) { return a < b ? a : b; });
-        const uint64_t hi = wave_all(in ? mine : (uint64_t)0, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-        const uint64_t m = __ballot(in);
+        uint64_t lo = ~0ull, hi = 0;
+        uint32_t c = 0;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const bool in = mine[m] >= low && mine[m] <= high;
+            lo = in && mine[m] < lo ? mine[m] : lo;
+            hi = in && mine[m] > hi ? mine[m] : hi;
+            c += __popcll(__ballot(in));
+        }
+        lo = wave_all(lo, [](uint64_t a, uint64_t b) { return a < b ? a : b; });
+        hi = wave_all(hi, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
         for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
         __syncthreads();
         if (tid == 0) {
@@ -699,17 +716,19 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
             L.block.count = 0;
         }
         __syncthreads();
-        if (lane == 0 && m) {
+        if (lane == 0 && c) {
             atomicMin((unsigned long long*)&L.block.found[0], (unsigned long long)lo);
             atomicMax((unsigned long long*)&L.block.found[1], (unsigned long long)hi);
-            atomicAdd(&L.block.count, (uint32_t)__popcll(m));
+            atomicAdd(&L.block.count, c);
         }
         __syncthreads();
         low = L.block.found[0];
         high = L.block.found[1];
         if (L.block.count <= 64) break;
         const int sh = max(0, 64 - __builtin_clzll(high - low) - 11);  // (high - low) >> sh < 2048
-        if (in) add(&L.bins[(high - mine) >> sh], w);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            if (mine[m] >= low && mine[m] <= high) add(&L.bins[(high - mine[m]) >> sh], w[m]);
         __syncthreads();
         find_bin<kBorderNT>(L.bins, above, [&](uint64_t) { return want; }, L.block);
         const uint64_t at = L.block.found[0];
@@ -723,11 +742,13 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
     __syncthreads();
     if (tid == 0) L.block.count = 0;
     __syncthreads();
-    if (tid < n && mine >= low && mine <= high) {
-        const uint32_t at = atomicAdd(&L.block.count, 1u);
-        L.list[at] = mine;
-        L.bins[at] = w;
-    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (mine[m] >= low && mine[m] <= high) {
+            const uint32_t at = atomicAdd(&L.block.count, 1u);
+            L.list[at] = mine[m];
+            L.bins[at] = w[m];
+        }
     __syncthreads();
     const int c = (int)L.block.count;
     if (tid < c) {
@@ -743,79 +764,123 @@ __device__ __forceinline__ Prefix rank_list(int n, uint64_t above, uint64_t want
     return p;
 }
 
-// One step of a bitonic sort within waves: the lower of two places takes the
-// larger number in a falling run of `size`.
-template <int STRIDE>
-__device__ __forceinline__ uint64_t sort_step(uint64_t x, int size) {
-    const uint64_t y = lane_xor<STRIDE>(x);
-    const bool larger = ((threadIdx.x & STRIDE) == 0) == ((threadIdx.x & size) == 0);
+// A step of a bitonic sort: of two places the lower takes the larger number in a
+// falling run of `size`.
+__device__ __forceinline__ uint64_t sort_pick(uint64_t x, uint64_t y, int i, int stride, int size) {
+    const bool larger = ((i & stride) == 0) == ((i & size) == 0);
     return (x > y) == larger ? x : y;
 }
 template <int STRIDE>
-__device__ __forceinline__ uint64_t sort_steps(uint64_t x, int size) {  // STRIDE, STRIDE / 2, ... 1
-    x = sort_step<STRIDE>(x, size);
-    if constexpr (STRIDE > 1) x = sort_steps<STRIDE / 2>(x, size);
+__device__ __forceinline__ uint64_t sort_steps(uint64_t x, int i, int size) {  // STRIDE, STRIDE / 2, ... 1
+    x = sort_pick(x, lane_xor<STRIDE>(x), i, STRIDE, size);
+    if constexpr (STRIDE > 1) x = sort_steps<STRIDE / 2>(x, i, size);
     return x;
 }
-// The numbers of the first n threads (a power of 2 from 64 on) in falling order.
-__device__ __forceinline__ uint64_t sort_falling(uint64_t x, int n, uint64_t* space) {
+// M numbers a thread, number i = thread + 1024 m, of the first n (a power of 2
+// from 64 on), in falling order.
+template <int M>
+__device__ __forceinline__ void sort_falling(uint64_t (&x)[M], int n, uint64_t* space) {
     const int tid = threadIdx.x;
-    if (tid < n) {  // whole waves
-        x = sort_steps<1>(x, 2);
-        x = sort_steps<2>(x, 4);
-        x = sort_steps<4>(x, 8);
-        x = sort_steps<8>(x, 16);
-        x = sort_steps<16>(x, 32);
-        x = sort_steps<32>(x, 64);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int i = tid + m * kBorderNT;
+        if (i < n) {  // whole waves
+            x[m] = sort_steps<1>(x[m], i, 2);
+            x[m] = sort_steps<2>(x[m], i, 4);
+            x[m] = sort_steps<4>(x[m], i, 8);
+            x[m] = sort_steps<8>(x[m], i, 16);
+            x[m] = sort_steps<16>(x[m], i, 32);
+            x[m] = sort_steps<32>(x[m], i, 64);
+        }
     }
     for (int size = 128; size <= n; size *= 2) {
-        for (int stride = size / 2; stride >= 64; stride /= 2) {
-            __syncthreads();
-            space[tid] = x;
-            __syncthreads();
-            const uint64_t y = space[tid ^ stride];
-            const bool larger = ((tid & stride) == 0) == ((tid & size) == 0);
-            x = (x > y) == larger ? x : y;
-        }
-        if (tid < n) x = sort_steps<32>(x, size);
+        if constexpr (M == 2)
+            if (size > kBorderNT) {
+                const uint64_t y = x[0] > x[1] ? x[0] : x[1];
+                x[1] = x[0] > x[1] ? x[1] : x[0];
+                x[0] = y;
+            }
+        for (int stride = min(size, kBorderNT) / 2; stride >= 64; stride /= 2)
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                __syncthreads();
+                space[tid] = x[m];
+                __syncthreads();
+                x[m] = sort_pick(x[m], space[tid ^ stride], tid + m * kBorderNT, stride, size);
+            }
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            if (tid + m * kBorderNT < n) x[m] = sort_steps<32>(x[m], tid + m * kBorderNT, size);
     }
     __syncthreads();
-    return x;
 }
 
-// From the n <= kList tokens in L.list, which hold every one that can be kept,
+// From the n <= 1024 M tokens in L.list, which hold every one that can be kept,
 // to the draw: in their order, where the filters are prefixes, then by index.
 // want: what top_p asks for, where it is the first filter.
+template <int M>
 __device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const Ask& r, const Weights& W, int n,
                                             uint64_t want, BorderLds& L) {
     const int tid = threadIdx.x;
+    const double least = (double)r.least;
     int size = 64;
     while (size < n) size *= 2;
-    const uint64_t me = sort_falling(tid < n ? L.list[tid] : 0, size, L.bins);
-    const double w = W.of(token_logit(me)), least = (double)r.least;
-    bool kept = me != 0 && (r.k == 0 || tid < r.k);
-    uint64_t q = kept ? W.whole(w) : 0, all;
+    uint64_t x[M], q[M], all;
+    double w[M];
+    bool kept[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) x[m] = tid + m * kBorderNT < n ? L.list[tid + m * kBorderNT] : 0;
+    sort_falling<M>(x, size, L.space);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int i = tid + m * kBorderNT;
+        w[m] = W.of(token_logit(x[m]));
+        kept[m] = x[m] != 0 && (r.k == 0 || i < r.k);
+        q[m] = kept[m] ? W.whole(w[m]) : 0;
+        L.list[i] = x[m];
+    }
     if (r.p < 1.f) {
-        const uint64_t before = block_before<kBorderNT>(q, L.block, &all);
-        kept = kept && before < (r.k ? share(r.p, all) : want);
+        uint64_t before[M], sum = 0;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            before[m] = sum + block_before<kBorderNT>(q[m], L.block, &all);
+            sum += all;
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) kept[m] = kept[m] && before[m] < (r.k ? share(r.p, sum) : want);
     }
-    kept = kept && (!(w < least) || tid == 0);
-    q = kept ? W.whole(w) : 0;
-    __syncthreads();
-    L.list[tid] = me;
-    L.bins[kBorderNT + tid] = q;
-    // the index, inverted, and the place above: 0 where nothing is kept
-    const uint64_t by = sort_falling(kept ? me << 32 | (uint32_t)tid : 0, size, L.bins);
-    const int from = (int)(uint32_t)by;
-    q = by ? L.bins[kBorderNT + from] : 0;
-    const uint64_t before = block_before<kBorderNT>(q, L.block, &all);
-    const uint64_t pass = draw_at(s, b, all);
-    if (before <= pass && pass < before + q) {
-        const uint64_t t = L.list[from];
-        s.a.ids[b] = token_index(t);
-        s.a.probs[b] = probability(s, W, token_logit(t), all);
+    // the index, inverted, and the place in the order: 0 where nothing is kept
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        const int i = tid + m * kBorderNT;
+        kept[m] = kept[m] && (!(w[m] < least) || i == 0);
+        L.bins[i] = kept[m] ? W.whole(w[m]) : 0;
+        x[m] = kept[m] ? x[m] << 32 | (uint32_t)i : 0;
     }
+    sort_falling<M>(x, size, L.space);
+    uint64_t before[M], sum = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        q[m] = x[m] ? L.bins[(uint32_t)x[m]] : 0;
+        before[m] = sum + block_before<kBorderNT>(q[m], L.block, &all);
+        sum += all;
+    }
+    const uint64_t pass = draw_at(s, b, sum);
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (before[m] <= pass && pass < before[m] + q[m]) {
+            const uint64_t t = L.list[(uint32_t)x[m]];
+            s.a.ids[b] = token_index(t);
+            s.a.probs[b] = probability(s, W, token_logit(t), sum);
+        }
     if (tid == 0) s.state[b].drawn = 1;
+}
+__device__ __forceinline__ void finish(const SampleSpace& s, int b, const Ask& r, const Weights& W, int n,
+                                       uint64_t want, BorderLds& L) {
+    if (n <= kBorderNT)
+        finish_list<1>(s, b, r, W, n, want, L);
+    else
+        finish_list<kList / kBorderNT>(s, b, r, W, n, want, L);
 }
 
 // The shortest prefix of `in` with at least k of its tokens (MASS false) or p
@@ -1047,7 +1112,7 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
         __syncthreads();
         const int n = (int)L.block.count;
         if (n <= kList) {
-            finish_list(s, b, r, W, n, 0, L);
+            finish(s, b, r, W, n, 0, L);
             return;
         }
         kept = border<BF16, false>(row, tops, r, W, every, S, last, L);
@@ -1061,10 +1126,10 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
         const Scale S = mass ? scale_of_mass(r, W, s.a.V) : scale_of_count(r);
         __syncthreads();
         if (bin < kBins && n <= kList) {
-            if (tid < n) L.list[tid] = s.list[(int64_t)b * kList + tid];
+            for (int i = tid; i < n; i += kBorderNT) L.list[i] = s.list[(int64_t)b * kList + i];
             __syncthreads();
             if (short_list(s, b, mass, W, S, bin, above)) {
-                finish_list(s, b, r, W, n, want, L);
+                finish(s, b, r, W, n, want, L);
                 return;
             }
             kept = rank_list(n, above, want, [&](float v) -> uint64_t { return mass ? W.whole(W.of(v)) : 1; }, L);

@@ -64,6 +64,39 @@ def test_filters(B, V, dtype):
     check(x, u, t=t, k=k, p=p, least=least)
 
 
+def test_largest_vocabulary():
+    """Sums over 8192 tiles, and borders among millions of equal logits."""
+    V = 4194304
+    x = logits(4, V, torch.bfloat16, 30)
+    x[2] = 1.5
+    x[3, ::2] = -2.0
+    check(x, [0.3, 0.9, 0.5, 0.999], k=[0, 100, 3000001, 0], p=[0.7, 0.9, 0.5, 0.99], t=[1.0, 0.7, 1.0, 2.0])
+    check(x, [0.1, 0.6, 0.7, 0.2])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_rows_of_few_numbers(dtype):
+    """Infinite logits, the type's lowest value and many close ones, over more
+    tokens than one workgroup ranks."""
+    V = 20001
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(6, V, generator=g, device="cuda")
+    x[0, ::3] = float("inf")
+    x[1] = torch.finfo(dtype).min
+    x[1, 5::7] = x[2, 5::7]
+    x[2] = x[2] * 1e-4 + 3.0
+    x[3, 100:] = torch.finfo(dtype).min
+    x[4] = torch.where(x[4] > 0, 2.0, -float("inf"))
+    x[5] *= 1e30
+    x = x.to(dtype)
+    u = [0.1, 0.35, 0.6, 0.85, 0.999, 0.5]
+    check(x, u)
+    check(x, u, k=[5000, 1500, 9000, 150, 4000, 3])
+    check(x, u, p=[0.2, 0.9, 0.6, 0.95, 0.5, 0.9])
+    check(x, u, k=[5000, 1500, 9000, 150, 4000, 3], p=[0.2, 0.9, 0.6, 0.95, 0.5, 0.9], t=[1.0, 0.5, 1.0, 2.0, 1.0, 1e30])
+    check(x, u, least=[0.5, 0.1, 0.9, 0.3, 1.0, 0.5])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("V", [5, 700, 30000])
 def test_equal_logits(V, dtype):
