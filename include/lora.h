@@ -612,16 +612,18 @@ int lora_kv_append(const lora_kv_cache* cache, const void* k, const void* v, int
  *            may overlap need separate ones
  * Positions whose page number is outside [0, n_pages) are left out. A request
  * without a position (length 0, or all left out) gets zeros and an lse of
- * -infinity. Scores, sums and outputs are held in fp32, out is rounded once;
- * a cache row that holds a NaN or an infinity at an attended position gives NaN
- * (in the dimensions where v does, in all where k does); what lies elsewhere in
- * the cache is not read. The order of sums depends on the lengths of the whole
- * batch, not on time: equal inputs give equal bits. No output may overlap an input, the workspace or another
- * output. Asynchronous on `stream`. Errors: LORA_EINVAL (sizes, a heads that
- * is no multiple of kv_heads, B over LORA_ATTN_MAX_BATCH, B * heads over
+ * -infinity, and so does one all of whose scores are -infinity; a score of
+ * -infinity weighs nothing otherwise, one of NaN or +infinity gives NaN in all
+ * dimensions, and a NaN or an infinity in v, at whatever weight, one that is not
+ * finite in its own. What lies at other positions of the cache is not read.
+ * Scores, sums and outputs are held in fp32, out is rounded once. The order of
+ * sums depends on the lengths of the whole batch, not on time: equal inputs
+ * give equal bits. No output may overlap an input, the workspace or another
+ * output. Asynchronous on `stream`. Errors: LORA_EINVAL (sizes, a heads that is
+ * no multiple of kv_heads, B over LORA_ATTN_MAX_BATCH, B * heads over
  * LORA_ATTN_MAX_ROWS, width * page_rows past 2^30, a scale that is not finite or
- * leaves fp32 times log2(e), null, misaligned or equal pointers), LORA_ESPACE, LORA_EHIP. B == 0
- * launches nothing.
+ * leaves fp32 times log2(e), null, misaligned or equal pointers), LORA_ESPACE,
+ * LORA_EHIP. B == 0 launches nothing.
  */
 size_t lora_attn_decode_workspace_bytes(int B, int heads, int kv_heads, int dim, int width, int page_rows);
 int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride, int heads, const int32_t* table,
@@ -668,8 +670,8 @@ int lora_sample(int dtype, const void* logits, int64_t stride, int B, int V, con
  * Per-kernel timing, for diagnostics and the benchmark's roofline figures.
  * Between lora_profile_begin and lora_profile_end, lora_linear,
  * lora_linear_multi, lora_shrink, lora_mx4_quantize, lora_mx4_dequantize,
- * lora_linear_mx4, lora_moe_*, lora_kv_append, lora_attn_decode and lora_sample record a HIP event pair around every kernel
- * they launch, on the stream it is launched on (not while that stream is being
+ * lora_linear_mx4, lora_moe_*, lora_kv_append, lora_attn_decode and
+ * lora_sample record a HIP event pair around every kernel they launch, on the stream it is launched on (not while that stream is being
  * captured into a graph, and at most max_records kernels).
  * lora_profile_end waits for the recorded events and writes one entry per
  * kernel name, in first-launch order, into out[0..cap): count, mean, min,

@@ -205,8 +205,8 @@ inline lora::KvCache kernel_cache(const lora_kv_cache& c) {
 }
 inline bool attn_sizes(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
     return B >= 0 && B <= LORA_ATTN_MAX_BATCH && kv_heads >= 1 && heads >= kv_heads && heads <= 65535 &&
-           (int64_t)B * heads <= LORA_ATTN_MAX_ROWS && heads % kv_heads == 0 && dim >= 1 && dim <= LORA_ATTN_MAX_DIM && width >= 1 && page_rows >= 1 &&
-           width <= (1 << 30) / page_rows;
+           (int64_t)B * heads <= LORA_ATTN_MAX_ROWS && heads % kv_heads == 0 && dim >= 1 &&
+           dim <= LORA_ATTN_MAX_DIM && width >= 1 && page_rows >= 1 && width <= (1 << 30) / page_rows;
 }
 
 // The experts' kernels address one matrix, x and the inner values through

@@ -852,7 +852,7 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCacheDesc:
     f8 = dt is torch.float8_e4m3fn
     if not f8 and dt is not torch.bfloat16:
         raise ValueError(f"k_cache must be bf16 or float8_e4m3fn, got {dt}")
-    if not k_cache.is_cuda or not v_cache.is_cuda or v_cache.dtype is not dt:
+    if getattr(v_cache, "dtype", None) is not dt or not k_cache.is_cuda or not v_cache.is_cuda:
         raise ValueError("k_cache and v_cache must be device tensors of one type")
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != strides:
@@ -925,8 +925,8 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
     pages in order. ``scale`` defaults to dim ** -0.5. Returns out [B, heads,
     dim] bf16, with ``lse`` also the fp32 [B, heads] log of the sum of exp."""
     d = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected (B, heads, dim)")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a bf16 device tensor (B, heads, dim)")
     B, heads, dim = q.shape
     sq = _head_rows(q, "q", heads, d.dim)
     if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
@@ -947,7 +947,7 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
     keep, ws, nb = _space(workspace, n, dev) if n else (None, None, 0)
     _call(dev, L.lora_attn_decode, "lora_attn_decode", ctypes.byref(d), q.data_ptr(), sq, heads, table.data_ptr(),
           table.stride(0) if B > 1 else width, width, lengths.data_ptr(), B,
-          d.dim ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(),
+          d.dim ** -0.5 if scale is None else float(scale), min(int(window), 2 ** 31 - 1), out.data_ptr(),
           sums.data_ptr() if lse else None, ws, nb)
     return (out, sums) if lse else out
 

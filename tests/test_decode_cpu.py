@@ -151,6 +151,11 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         lora.kv_append(torch.zeros(1, 2, 64, dtype=b), torch.zeros(1, 2, 64, dtype=b), k, k,
                        torch.zeros(1, dtype=torch.int64))
+    for bad in (None, k.float()):
+        with pytest.raises(ValueError):
+            lora.kv_append(k[0], k[0], k, bad, torch.zeros(16, dtype=torch.int64))
+        with pytest.raises(ValueError):
+            lora.attn_decode(k[0], bad, k, torch.zeros(16, 4, dtype=torch.int32), torch.zeros(16, dtype=torch.int32))
     with pytest.raises(ValueError):
         lora.moe_route_scored(torch.zeros(4, 64, dtype=b), torch.zeros(8, 64, dtype=b), 2)
     with pytest.raises(ValueError):

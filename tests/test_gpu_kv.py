@@ -270,6 +270,49 @@ def test_rows_past_the_length_are_not_read():
     assert bool(got[hit].isnan().all()) and torch.equal(got[~hit], want[~hit])
 
 
+def test_infinite_keys():
+    """A score of -infinity weighs nothing (all of them: as a request without a
+    position), one of +infinity gives NaN, to the heads that meet it."""
+    c = Cache([300, 40], 2, 128, 16)
+    table, lengths = c.tensors()
+    q = torch.randn(2, 8, 128, device="cuda").to(torch.bfloat16)
+    q[..., 7] = 1.5
+    c.k[c.table[0, 100 // 16], 100 % 16, :, 7] = -float("inf")
+    for j in range(40):
+        c.k[c.table[1, j // 16], j % 16, 1, 7] = -float("inf")
+    out, lse = lora.attn_decode(q, c.k, c.v, table, lengths, lse=True)
+    k, v = c.rows(0, 0, 300)
+    keep = [j for j in range(300) if j != 100]
+    ref, rl, bound, lb = decode_ref.attention(as64(q[0]), k[keep], v[keep], 128 ** -0.5)
+    assert (np.abs(as64(out[0]) - ref) <= 2.0 ** -8 * np.abs(ref) + bound).all()
+    assert (np.abs(as64(lse[0]) - rl) <= lb + 2.0 ** -24 * np.abs(rl)).all()
+    assert not as64(out[1, 4:]).any() and np.isneginf(as64(lse[1, 4:])).all()
+    assert bool(out[1, :4].isfinite().all())
+    c.k[c.table[0, 17], 3, 0, 7] = float("inf")
+    got = lora.attn_decode(q, c.k, c.v, table, lengths)
+    assert bool(got[0, :4].isnan().all()) and torch.equal(got[0, 4:], out[0, 4:]) and torch.equal(got[1], out[1])
+
+
+def test_shared_pages():
+    """A page that several requests read, or one request several times."""
+    c = Cache([100, 200, 64], 2, 128, 16)
+    c.table[1, :3] = c.table[0, 2:5]
+    c.table[2, :4] = c.table[1, 5]
+    check(c, 8)
+
+
+def test_rows_far_apart():
+    """Rows 2^24 elements apart, heads and pages between them."""
+    x = torch.randn(2, 16, 1 << 24, device="cuda", dtype=torch.bfloat16)
+    c = Cache([40], 2, 128, 16, spare=0)
+    c.k, c.v = (y.as_strided((3, 16, 2, 128), (1024, 1 << 24, 256, 1), y.storage_offset()) for y in (x[0], x[1]))
+    check(c, 8)
+    new = torch.randn(2, 2, 128, device="cuda").to(torch.bfloat16)
+    lora.kv_append(new, -new, c.k, c.v, torch.tensor([47, 0], device="cuda"))
+    assert torch.equal(c.k[2, 15], new[0]) and torch.equal(c.v[0, 0], -new[1])
+    check(c, 8)
+
+
 def test_offsets_past_4_gib():
     """The first and the last page of a cache of over 4 GiB, and of its rows."""
     page, kv, dim = 16, 8, 128
