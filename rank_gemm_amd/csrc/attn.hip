@@ -17,11 +17,12 @@
 // are made, its values likewise); values are read from there transposed. No
 // wave waits on another until the end of a piece.
 //
-// Work is split by what there is, not by request: the positions of all
+// Long work is split by what there is, not by request: the positions of all
 // requests and kv heads, in units of 4 tiles, are one line, of which every
 // workgroup takes an equal part. It finds its part from the lengths itself. A
 // part that ends inside a request leaves m, l and o in the workspace, and a
-// second kernel joins the pieces of each request.
+// second kernel joins the pieces of each request. Short rows (a kv head of a
+// request each) go to a workgroup from end to end, in one launch.
 //
 // Positions whose page is outside the cache are left out, so no table makes a
 // kernel read past it; nothing past a request's length is read either.
@@ -41,7 +42,6 @@
 namespace lora {
 
 constexpr float kLowest = -3.402823466e38f;  // below every finite score, and finite
-constexpr int kAttnWaves = 4;
 
 // How the work is laid out, decided on the host.
 struct AttnPlan {
@@ -59,10 +59,11 @@ struct AttnPlan {
 };
 
 // DP: dimensions padded to 64, 128 or 256 (zeros behind dim). RT: 16-head
-// blocks of a kv head's heads.
-template <int DP_, bool F8_, int RT_>
+// blocks of a kv head's heads. W: waves a workgroup: 4, or 8 where a workgroup
+// takes a row from end to end and two waves a SIMD have the registers.
+template <int DP_, bool F8_, int RT_, int W_>
 struct AttnCfg {
-    static constexpr int DP = DP_, RT = RT_;
+    static constexpr int DP = DP_, RT = RT_, W = W_;
     static constexpr bool F8 = F8_;
     static constexpr int ROWB = DP * (F8 ? 1 : 2);  // bytes of a row in LDS
     static constexpr int CH = ROWB / 16;            // its 16-byte chunks
@@ -73,7 +74,7 @@ struct AttnCfg {
     static constexpr int STAGE = TK * ROWB;
     static constexpr int NI = STAGE / 1024;  // load instructions a stage
     static constexpr int RI = 64 / CH;       // rows a load instruction
-    static constexpr int U = kAttnWaves * TK;
+    static constexpr int U = W * TK;
     // waves a SIMD to compile for: 2 leaves 256 registers, where the products take
     // vector registers alone and o is not copied to and fro
     static constexpr int MinWaves = DP * RT <= 128 ? 2 : 1;
@@ -199,9 +200,9 @@ __device__ __forceinline__ int64_t units_per_wg(int64_t units, int wgs) {
 
 template <class C>
 struct AttnLds {
-    alignas(1024) u32x4 kv[kAttnWaves][2 * C::STAGE / 16];
-    float m[kAttnWaves][16], l[kAttnWaves][16];
-    int64_t scan[kAttnWaves];
+    alignas(1024) u32x4 kv[C::W][2 * C::STAGE / 16];
+    float m[C::W][16], l[C::W][16];
+    int64_t scan[C::W];
     int64_t found[2];
     int request;
 };
@@ -309,8 +310,8 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
     attn_range(a, b, &lo, &hi);
     lo = uniform(lo), hi = uniform(hi);
     const int start = lo & ~15;
-    // this wave's tiles: position start + (4 unit + wave) TK
-    const int first = start + (kAttnWaves * t0 + wave) * C::TK;
+    // this wave's tiles: position start + (W unit + wave) TK
+    const int first = start + (C::W * t0 + wave) * C::TK;
     const int end = min(hi, start + t1 * C::U);
     const int nt = first < end ? (end - first + C::U - 1) / C::U : 0;
     const int64_t head = hk * a.c.head_stride;
@@ -508,15 +509,15 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
 #pragma unroll
         for (int d = 0; d < ND; ++d) mine[fr * (DP / 4) + ((4 * d + fg) ^ fr)] = o[rt][d];
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * (D / 4); i += 64 * kAttnWaves) {
+        for (int i = threadIdx.x; i < 16 * (D / 4); i += 64 * C::W) {
             const int h = i / (D / 4), d4 = i % (D / 4);
             if (rt * 16 + h >= nq) break;
             float top = L.m[0][h], den = 0.f;
             f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, L.m[w][h]);
+            for (int w = 1; w < C::W; ++w) top = fmaxf(top, L.m[w][h]);
 #pragma unroll
-            for (int w = 0; w < kAttnWaves; ++w) {
+            for (int w = 0; w < C::W; ++w) {
                 const float f = __builtin_amdgcn_exp2f(L.m[w][h] - top);
                 den += f * L.l[w][h];
                 x += f * reinterpret_cast<const f32x4*>(L.kv[w])[h * (DP / 4) + (d4 ^ h)];
@@ -538,17 +539,17 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
 }
 
 template <class C>
-__global__ __launch_bounds__(64 * kAttnWaves, C::MinWaves) void attn_decode_kernel(AttnPlan p) {
+__global__ __launch_bounds__(64 * C::W, C::MinWaves) void attn_decode_kernel(AttnPlan p) {
     __shared__ AttnLds<C> L;
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (p.wgs == 0) {
+    if (C::W == 8 || p.wgs == 0) {
         const int b = blockIdx.x / p.rows, row = blockIdx.x % p.rows;
         attn_piece<C>(p, L, b, row, 0, attn_units<C>(a, b), true, 0);
         return;
     }
     // the line: where every request's units begin
-    const int per_thread = (a.B + 64 * kAttnWaves - 1) / (64 * kAttnWaves);
+    const int per_thread = (a.B + 64 * C::W - 1) / (64 * C::W);
     const int b0 = min(tid * per_thread, a.B), b1 = min(b0 + per_thread, a.B);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += attn_units<C>(a, b);
@@ -562,7 +563,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, C::MinWaves) void attn_decode_kern
     if (lane == 63) L.scan[wave] = in;
     __syncthreads();
     int64_t total = 0, before = in - mine;
-    for (int w = 0; w < kAttnWaves; ++w) {
+    for (int w = 0; w < C::W; ++w) {
         if (w < wave) before += L.scan[w];
         total += L.scan[w];
     }
@@ -604,10 +605,11 @@ __global__ __launch_bounds__(64 * kAttnWaves, C::MinWaves) void attn_decode_kern
 }
 
 // Rows of more than one piece joined, rows without a position written as
-// zeros. A workgroup takes all heads of a row, or one where there are few rows
-// (8 rows of 64 pieces: 6.4 us with all, 4.3 with one): its threads 4
-// dimensions of a head each, and where there are few of those, several share a
-// head's pieces.
+// zeros. A workgroup takes all heads of a row, or, where there are fewer than
+// 256 rows, as many as make 256 workgroups (8 rows of 4 heads and 64 pieces: 6.4
+// us with all, 4.3 with one; the attention of 128 rows of 64 heads, 600 positions
+// each, 92 us with one, 28 with 32): its threads 4 dimensions of a head each, and
+// where there are few of those, several share a head's pieces.
 constexpr int kJoinThreads = 512;
 template <bool F8>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
@@ -624,8 +626,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
     const int2 meta = hi > lo ? p.meta[r] : make_int2(0, 0);
     if (hi > lo && meta.y == 1) return;  // written by the first kernel
     const float vs = F8 ? a.c.v_scale[hk] : 1.f;
-    const int h0 = gridDim.y > 1 ? (int)blockIdx.y : 0, heads = gridDim.y > 1 ? 1 : nq;
-    if (h0 >= nq) return;
+    const int per = (p.block_heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * per, heads = min(per, nq - h0);
+    if (heads <= 0) return;
     const int items = heads * (D / 4);
     int share = 1;
     while (2 * share * items <= kJoinThreads) share *= 2;
@@ -674,9 +676,9 @@ namespace {
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Shape {
-    int dp, rt, blocks, block_heads, unit, wgs;
+    int dp, rt, blocks, block_heads, waves, wgs;
 };
-Shape attn_shape(int heads, int kv_heads, int dim, int longest, bool f8) {
+Shape attn_shape(int B, int heads, int kv_heads, int dim, int longest, bool f8) {
     Shape s;
     s.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
     // heads a workgroup: as many as its registers hold
@@ -684,27 +686,40 @@ Shape attn_shape(int heads, int kv_heads, int dim, int longest, bool f8) {
     s.blocks = cdiv(group, most);
     s.block_heads = cdiv(group, s.blocks);
     s.rt = s.block_heads <= 16 ? 1 : s.block_heads <= 32 ? 2 : 4;
-    const int rowb = s.dp * (f8 ? 1 : 2);
-    s.unit = kAttnWaves * (rowb <= 128 ? 64 : 32);
-    // two workgroups a CU, where their LDS allows it; none where a request has
-    // so few units that a workgroup takes its row from end to end, which saves
-    // finding the parts and the join: bf16, 32 heads over 8 of 128, 1024 positions
-    // (8 units) of 1 request 12.6 against 13.2 us, of 32 requests 22.8 against
-    // 28.8; 2048 (16 units) of 1 request 21.6 against 13.7
-    s.wgs = cdiv(longest, s.unit) <= 8 ? 0 : rowb > 256 ? 256 : 512;
+    const int64_t rows = (int64_t)B * kv_heads * s.blocks;
+    // 8 waves a workgroup where that is all there is to fill a CU, and two waves a
+    // SIMD have the registers: bf16, 32 heads over 8 of 128, 1024 positions of 1
+    // request (8 rows) 9.5 against 12.0 us with 4, 600 of 16 (128 rows) 10.6 against
+    // 11.5, 128 of 64 (512 rows) 9.7 against 6.7
+    const bool wide = rows <= 256 && s.dp * s.rt <= 128;
+    // Short rows go to a workgroup each from end to end, which saves finding the
+    // parts and the join (some 8 us): the same heads, 1000 positions of 1 request
+    // 10.4 against 14.1 us, 2048 15.2 against 12.5; of 64 requests of 1 to 2048
+    // 52 against 56 us, to 3300 93 against 92; 16 heads over 4 of 256, 600
+    // positions of 1 request 16.0 against 14.3
+    if (longest <= (rows >= 128 ? 2048 : wide ? 1536 : 512)) {
+        s.wgs = 0;
+        s.waves = wide ? 8 : 4;
+    } else {  // two workgroups a CU, where their LDS allows it
+        s.wgs = s.dp * (f8 ? 1 : 2) > 256 ? 256 : 512;
+        s.waves = 4;
+    }
     return s;
 }
 
-template <int DP, bool F8>
-auto attn_kernel(int rt) {
-    if constexpr (DP == 256)
-        return attn_decode_kernel<AttnCfg<DP, F8, 1>>;
-    else if constexpr (DP == 128)
-        return rt == 1 ? attn_decode_kernel<AttnCfg<DP, F8, 1>> : attn_decode_kernel<AttnCfg<DP, F8, 2>>;
-    else
-        return rt == 1   ? attn_decode_kernel<AttnCfg<DP, F8, 1>>
-               : rt == 2 ? attn_decode_kernel<AttnCfg<DP, F8, 2>>
-                         : attn_decode_kernel<AttnCfg<DP, F8, 4>>;
+template <int DP, bool F8, int RT>
+auto attn_kernel(int waves) {
+    if constexpr (DP * RT <= 128)
+        if (waves == 8) return attn_decode_kernel<AttnCfg<DP, F8, RT, 8>>;
+    return attn_decode_kernel<AttnCfg<DP, F8, RT, 4>>;
+}
+template <bool F8>
+auto attn_kernel(const Shape& s) {
+    if (s.dp == 256) return attn_kernel<256, F8, 1>(s.waves);
+    if (s.dp == 128) return s.rt == 1 ? attn_kernel<128, F8, 1>(s.waves) : attn_kernel<128, F8, 2>(s.waves);
+    return s.rt == 1   ? attn_kernel<64, F8, 1>(s.waves)
+           : s.rt == 2 ? attn_kernel<64, F8, 2>(s.waves)
+                       : attn_kernel<64, F8, 4>(s.waves);
 }
 
 }  // namespace
@@ -712,7 +727,7 @@ auto attn_kernel(int rt) {
 size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
     size_t most = 0;
     for (bool f8 : {false, true}) {
-        const Shape s = attn_shape(heads, kv_heads, dim, width * page_rows, f8);
+        const Shape s = attn_shape(B, heads, kv_heads, dim, width * page_rows, f8);
         if (s.wgs == 0) continue;
         const size_t rows = (size_t)B * kv_heads * s.blocks, slots = s.wgs + rows;
         most = std::max(most, align256(slots * s.block_heads * dim * sizeof(float)) +
@@ -724,7 +739,8 @@ size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width,
 hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* tm) {
     // positions a request can attend to, and the ones its first tile may begin ahead of them
     const int most = a.width * a.c.page_rows;
-    const Shape s = attn_shape(a.heads, a.c.kv_heads, a.c.dim, a.window > 0 && a.window < most ? a.window + 15 : most, f8);
+    const Shape s = attn_shape(a.B, a.heads, a.c.kv_heads, a.c.dim,
+                               a.window > 0 && a.window < most ? a.window + 15 : most, f8);
     AttnPlan p{};
     p.a = a;
     p.wgs = s.wgs;
@@ -743,15 +759,13 @@ hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* t
     p.part = reinterpret_cast<float*>(ws);
     p.ml = reinterpret_cast<float2*>(ws + align256(slots * s.block_heads * a.c.dim * sizeof(float)));
     p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.ml) + align256(slots * s.block_heads * sizeof(float2)));
-    auto kernel = f8 ? (s.dp == 64 ? attn_kernel<64, true>(s.rt) : s.dp == 128 ? attn_kernel<128, true>(s.rt)
-                                                                              : attn_kernel<256, true>(s.rt))
-                     : (s.dp == 64 ? attn_kernel<64, false>(s.rt) : s.dp == 128 ? attn_kernel<128, false>(s.rt)
-                                                                               : attn_kernel<256, false>(s.rt));
+    auto kernel = f8 ? attn_kernel<true>(s) : attn_kernel<false>(s);
     const uint32_t grid = s.wgs ? s.wgs : (uint32_t)rows;
-    hipError_t e = launch(tm, "attn_decode", kernel, dim3(grid), dim3(64 * kAttnWaves), st, p);
+    hipError_t e = launch(tm, "attn_decode", kernel, dim3(grid), dim3(64 * s.waves), st, p);
     if (e != hipSuccess || s.wgs == 0) return e;
+    const uint32_t splits = std::max(1u, std::min((uint32_t)s.block_heads, 256 / (uint32_t)rows));
     return launch(tm, "attn_join", f8 ? attn_join_kernel<true> : attn_join_kernel<false>,
-                  dim3((uint32_t)rows, rows < 256 ? s.block_heads : 1), dim3(kJoinThreads), st, p);
+                  dim3((uint32_t)rows, splits), dim3(kJoinThreads), st, p);
 }
 
 }  // namespace lora

@@ -159,7 +159,9 @@ SHAPES = [  # lengths, heads, kv heads, dim, page
     ([127, 128, 129, 255, 256, 257, 0, 1], 6, 3, 64, 32), ([700, 1, 1500], 12, 2, 80, 24), ([300, 4097], 5, 1, 96, 1),
     ([1000, 513], 16, 1, 128, 7), ([40, 2000], 64, 2, 64, 64), ([900], 3, 3, 256, 48), ([777, 10], 40, 1, 112, 16),
     ([257, 64], 130, 2, 128, 16), ([600, 50], 70, 1, 256, 32), ([90] * 33, 4, 4, 16, 16), ([33, 1025], 28, 4, 176, 128),
-    ([2049], 17, 17, 128, 3)]
+    ([2049], 17, 17, 128, 3), ([300, 70], 100, 2, 64, 16), ([900, 5, 1600], 96, 2, 48, 16), ([1300] + [9] * 63, 40, 2, 128, 16),
+    ([700] + [20] * 63, 4, 2, 256, 16), ([2000, 0] + [30] * 150, 2, 2, 64, 16), ([1536, 1000], 8, 2, 128, 16),
+    ([1537, 600], 8, 2, 128, 16), ([512], 32, 2, 256, 32), ([513, 100], 24, 1, 128, 16)]
 
 
 @pytest.mark.parametrize("form", ["bf16", "f8"])
