@@ -22,6 +22,11 @@
 //            read
 //   sums     the tiles' sums of the kept tokens
 //   draw     a workgroup a request
+// Bound by that chain: of one row of 131072 with top_k 50 and top_p 0.9 (20 us)
+// the border's workgroup takes 8 and each launch, busy or not, 2.4. Of 256 rows
+// of 128k fp32 (134 MB) tops reads at 6.5 TB/s (20 us); bins, by the 64-bit
+// exponentials of the rows that need all of theirs, 30 of 100 us with filters of
+// every kind and 46 of 68 with none.
 //
 // Weights are 64-bit exponentials held as whole numbers of 2^-shift, so that
 // sums do not depend on the order in which they are made: equal inputs give
@@ -144,13 +149,22 @@ __device__ __forceinline__ float wave_min(float v) {
 __device__ __forceinline__ uint64_t wave_total(uint64_t v) {
     return wave_all(v, [](uint64_t a, uint64_t b) { return a + b; });
 }
-__device__ __forceinline__ uint64_t wave_scan(uint64_t v, int lane) {  // inclusive
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t p = shfl64(v, lane - o < 0 ? lane : lane - o);
-        if (lane >= o) v += p;
-    }
-    return v;
+// v of the lane a DPP move names, 0 where it names none or the row is not in ROWS.
+template <int MOVE, int ROWS>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+    const u32x2 x = __builtin_bit_cast(u32x2, v);
+    return __builtin_bit_cast(uint64_t, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)x[0], MOVE, ROWS, 0xf, false),
+                                              (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x[1], MOVE, ROWS, 0xf, false)});
+}
+// The sum over the lanes up to this one: within rows of 16, then with the last
+// lane of the row before, then with lane 31.
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+    v += dpp64<0x111, 0xf>(v);
+    v += dpp64<0x112, 0xf>(v);
+    v += dpp64<0x114, 0xf>(v);
+    v += dpp64<0x118, 0xf>(v);
+    v += dpp64<0x142, 0xa>(v);
+    return v + dpp64<0x143, 0xc>(v);
 }
 
 // -------------------------------------------------------------------- rows --
@@ -326,7 +340,7 @@ __device__ __forceinline__ Scale scale_of_mass(const Ask& r, const Weights& W, i
 template <int NT>
 __device__ __forceinline__ uint64_t block_before(uint64_t v, BlockLds<NT>& L, uint64_t* all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint64_t in = wave_scan(v, lane);
+    const uint64_t in = wave_scan(v);
     __syncthreads();
     if (lane == 63) L.part[wave] = in;
     __syncthreads();
@@ -662,7 +676,7 @@ __device__ __forceinline__ Prefix nth_equal(const Row<BF16>& row, const float* t
                 uint32_t c = 0;
 #pragma unroll
                 for (int e = 0; e < Row<BF16>::E; ++e) c += v[i * Row<BF16>::E + e] == v0;
-                const uint64_t in = wave_scan(c, lane);
+                const uint64_t in = wave_scan(c);
                 uint64_t at = done + in - c;
 #pragma unroll
                 for (int e = 0; e < Row<BF16>::E; ++e) {
@@ -857,6 +871,9 @@ __device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const A
         L.bins[i] = kept[m] ? W.whole(w[m]) : 0;
         x[m] = kept[m] ? x[m] << 32 | (uint32_t)i : 0;
     }
+    // what is kept is the first of them, of top_k no more than k
+    if (r.k)
+        while (size > 64 && size / 2 >= r.k) size /= 2;
     sort_falling<M>(x, size, L.space);
     uint64_t before[M], sum = 0;
 #pragma unroll
@@ -1044,7 +1061,7 @@ __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row,
             w[e] = kept.holds(v[j], row.index(t, j, lane)) && !(wj < least) ? W.whole(wj) : 0;
             sum += w[e];
         }
-        const uint64_t in = run + wave_scan(sum, lane);
+        const uint64_t in = run + wave_scan(sum);
         const uint64_t m = __ballot(in > left);
         if (m) {
             if (lane == __builtin_ctzll(m)) {
