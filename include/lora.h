@@ -648,8 +648,9 @@ int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride
  *            top_k < 1, top_p >= 1 and min_p <= 0 (or NaN) filter nothing;
  *            top_p <= 0 leaves the first token.
  *   ids      dev int32 [B] out;  probs  dev float [B] out
- *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes, on a 16-byte
- *            boundary; calls that may overlap need separate ones
+ *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes (0 for some
+ *            sizes: it may then be null), on a 16-byte boundary; calls that may
+ *            overlap need separate ones
  * Tokens whose logit is NaN or -infinity are never drawn; where there is no
  * other, ids[b] = -1 and probs[b] = 0. Among logits of +infinity all weigh the
  * same, and nothing else does. Weights are 64-bit exponentials, rounded to

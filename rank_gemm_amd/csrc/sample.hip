@@ -5,11 +5,12 @@
 //   first token, by index, at which the running sum of the kept w passes u
 //   times their whole sum.
 //
-// No row is sorted. The border of a prefix is found by a histogram of the
+// No long row is sorted. The border of a prefix is found by a histogram of the
 // tokens over bins of equal width below the largest logit, and by ranking the
 // tokens of the one bin that holds it; the draw goes by sums over tiles of 512
-// tokens and then through one tile. Every pass over whole rows is spread over
-// the chip, tile by tile, whatever the batch:
+// tokens and then through one tile. Short rows, and rows of batches that fill
+// the chip, are a workgroup's each from end to end, in one launch. Every pass
+// over others is spread over the chip, tile by tile:
 //   tops     the largest logit of each tile
 //   bins     the histogram (top_p, or a top_k past the number of tiles); rows
 //            without those filters: the tiles' sums at once
@@ -23,10 +24,10 @@
 //   sums     the tiles' sums of the kept tokens
 //   draw     a workgroup a request
 // Bound by that chain: of one row of 131072 with top_k 50 and top_p 0.9 (20 us)
-// the border's workgroup takes 8 and each launch, busy or not, 2.4. Of 256 rows
-// of 128k fp32 (134 MB) tops reads at 6.5 TB/s (20 us); bins, by the 64-bit
-// exponentials of the rows that need all of theirs, 30 of 100 us with filters of
-// every kind and 46 of 68 with none.
+// the border's workgroup takes 8 and each launch, busy or not, 2.4; the one
+// launch over 32000 takes 14. Many rows by the passes of a CU over its own: 256
+// of 131072 bf16 with top_k 50 and top_p 0.9 22 us (3.1 TB/s), with no filter 57,
+// of which the 64-bit exponentials, some 20 operations a token, are 40.
 //
 // Weights are 64-bit exponentials held as whole numbers of 2^-shift, so that
 // sums do not depend on the order in which they are made: equal inputs give
@@ -267,12 +268,12 @@ __device__ __forceinline__ Ask asked(const SampleArgs& a, int b) {
 }
 // From the tiles' largest logits, by a workgroup.
 template <int NT>
-__device__ __forceinline__ Ask find_way(const SampleSpace& s, int b, BlockLds<NT>& L) {
+__device__ __forceinline__ Ask find_way(const SampleSpace& s, int b, const float* tops, BlockLds<NT>& L) {
     Ask r = asked(s.a, b);
     float top = -INFINITY, under = INFINITY;
     int live = 0;
     for (int i = threadIdx.x; i < s.nt; i += NT) {
-        const float v = s.tops[(int64_t)b * s.nt + i];
+        const float v = tops[i];
         if (v > -INFINITY) {
             top = fmaxf(top, v);
             under = fminf(under, v);
@@ -477,6 +478,14 @@ __device__ __forceinline__ uint64_t wave_totals(const uint64_t (&x)[4], int lane
 // ------------------------------------------------------------- row by tiles --
 constexpr int kTilesNT = 256;
 
+__device__ __forceinline__ void tile_top(float* tops, int t, const float (&v)[8], int lane) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j]);  // of a number and NaN the number
+    m = wave_max(m);
+    if (lane == 0) tops[t] = m;
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(kTilesNT) void sample_tops_kernel(SampleSpace s) {
     const int b = blockIdx.y, lane = threadIdx.x & 63, t0 = blockIdx.x * s.per_wg;
@@ -484,11 +493,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_tops_kernel(SampleSpace s) {
     each_tile<kTilesNT>(
         row, t0, t0 + s.per_wg, [](int) { return true; },
         [&](int t, const float(&v)[8]) {
-            float m = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j]);  // of a number and NaN the number
-            m = wave_max(m);
-            if (lane == 0) s.tops[(int64_t)b * s.nt + t] = m;
+            tile_top(s.tops + (int64_t)b * s.nt, t, v, lane);
         });
     // what the others add to
     for (int i = blockIdx.x * kTilesNT + threadIdx.x; i < kBins; i += gridDim.x * kTilesNT)
@@ -502,10 +507,9 @@ __global__ __launch_bounds__(kTilesNT) void sample_tops_kernel(SampleSpace s) {
 
 // The tiles' sums of the tokens that a prefix and min_p leave.
 template <int NT, bool BF16>
-__device__ __forceinline__ void tile_sums(const SampleSpace& s, const Row<BF16>& row, int b, int t0, int t1,
+__device__ __forceinline__ void tile_sums(const SampleSpace& s, const Row<BF16>& row, const float* tops, int t0, int t1,
                                           const Ask& r, const Weights& W, Prefix kept, uint64_t* sums) {
     const int lane = threadIdx.x & 63;
-    const float* tops = s.tops + (int64_t)b * s.nt;
     const double least = (double)r.least;
     for (int t = t0 + threadIdx.x; t < min(t1, s.nt); t += NT) sums[t] = 0;
     __syncthreads();
@@ -536,7 +540,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
     __shared__ uint64_t bins[kBins];
     __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.y, t0 = blockIdx.x * s.per_wg;
-    const Ask r = find_way<kTilesNT>(s, b, L);
+    const Ask r = find_way<kTilesNT>(s, b, s.tops + (int64_t)b * s.nt, L);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         RowState& st = s.state[b];
         st.way = r.way, st.live = r.live, st.top = r.top, st.under = r.under;
@@ -545,7 +549,8 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
     const Row<BF16> row(s.a, b);
     const Weights W = weights_of(s, r);
     if (r.way == kSums) {
-        tile_sums<kTilesNT>(s, row, b, t0, t0 + s.per_wg, r, W, Prefix{-INFINITY, -1}, s.sums + (int64_t)b * s.nt);
+        tile_sums<kTilesNT>(s, row, s.tops + (int64_t)b * s.nt, t0, t0 + s.per_wg, r, W, Prefix{-INFINITY, -1},
+                            s.sums + (int64_t)b * s.nt);
         return;
     }
     const bool mass = r.way == kMass;
@@ -581,12 +586,11 @@ __global__ __launch_bounds__(kTilesNT) void sample_bins_kernel(SampleSpace s) {
         if (bins[i]) add(&s.bins[(int64_t)b * kBins + i], bins[i]);
 }
 
-// Whether the tokens down to the border's bin are at most kList for sure: then
-// all of them are gathered, and the border kernel has what it needs to draw.
-// Of top_p: none of them weighs less than the bin's far edge.
-__device__ __forceinline__ bool short_list(const SampleSpace& s, int b, bool mass, const Weights& W, const Scale& S,
-                                           int bin, uint64_t above) {
-    const uint64_t through = above + s.bins[(int64_t)b * kBins + bin];
+// Whether the tokens down to the border's bin, `through` by count or weight, are
+// at most kList for sure: then all of them are gathered, and the border's
+// workgroup has what it needs to draw. Of top_p: none of them weighs less than
+// the bin's far edge.
+__device__ __forceinline__ bool short_list(bool mass, const Weights& W, const Scale& S, int bin, uint64_t through) {
     if (!mass) return through <= kList;
     if (bin == kBins - 1 || !(S.per > 0.f)) return false;
     const uint64_t edge = W.whole(W.of(S.top - (float)(bin + 2) / S.per));
@@ -608,7 +612,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_gather_kernel(SampleSpace s) 
         s.bins + (int64_t)b * kBins, 0, [&](uint64_t all) { return mass ? share(r.p, all) : (uint64_t)r.k; }, L);
     const int bin = (int)L.found[0];
     if (bin == kBins) return;
-    const bool all = short_list(s, b, mass, W, S, bin, L.found[1]);  // uniform
+    const bool all = short_list(mass, W, S, bin, L.found[1] + s.bins[(int64_t)b * kBins + bin]);  // uniform
     const float* tops = s.tops + (int64_t)b * s.nt;
     if (tid == 0) L.count = 0;
     __syncthreads();
@@ -890,7 +894,6 @@ __device__ __forceinline__ void finish_list(const SampleSpace& s, int b, const A
             s.a.ids[b] = token_index(t);
             s.a.probs[b] = probability(s, W, token_logit(t), sum);
         }
-    if (tid == 0) s.state[b].drawn = 1;
 }
 __device__ __forceinline__ void finish(const SampleSpace& s, int b, const Ask& r, const Weights& W, int n,
                                        uint64_t want, BorderLds& L) {
@@ -903,10 +906,12 @@ __device__ __forceinline__ void finish(const SampleSpace& s, int b, const Ask& r
 // The shortest prefix of `in` with at least k of its tokens (MASS false) or p
 // of its weights (MASS true), by this workgroup alone; `in` where it has less.
 // No border lies behind bin `last`; tokens behind it are not looked at (of MASS
-// it is the last there is).
+// it is the last there is). may, only where `in` is every token: where the list
+// down to the border is short the draw is made from it, and `drawn` says so.
 template <bool BF16, bool MASS>
-__device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops, const Ask& r, const Weights& W, Prefix in,
-                                         const Scale& S, int last, BorderLds& L) {
+__device__ __forceinline__ Prefix border(const SampleSpace& s, int b, const Row<BF16>& row, const float* tops,
+                                         const Ask& r, const Weights& W, Prefix in, const Scale& S, int last,
+                                         BorderLds& L, bool may, bool& drawn) {
     const int tid = threadIdx.x, lane = tid & 63;
     auto weight = [&](float v) -> uint64_t { return MASS ? W.whole(W.of(v)) : 1; };
     for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
@@ -930,7 +935,8 @@ __device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops
     uint64_t above = L.block.found[1];
     __syncthreads();
     if (bin == kBins) return in;
-    // the tokens of the border's bin
+    // the tokens of the border's bin, or down to there
+    const bool all = may && short_list(MASS, W, S, bin, above + L.bins[bin]);
     float low = INFINITY, high = -INFINITY;
     if (tid == 0) L.block.count = 0;
     __syncthreads();
@@ -939,7 +945,7 @@ __device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops
         [&](int t, const float(&v)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (in.holds(v[j], row.index(t, j, lane)) && S.bin(v[j]) == bin) {
+                if (in.holds(v[j], row.index(t, j, lane)) && (all ? S.bin(v[j]) <= bin : S.bin(v[j]) == bin)) {
                     const uint32_t at = atomicAdd(&L.block.count, 1u);
                     if (at < kList) L.list[at] = token(v[j], row.index(t, j, lane));
                     low = fminf(low, v[j]);
@@ -949,6 +955,11 @@ __device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops
     __syncthreads();
     const int n = (int)L.block.count;
     __syncthreads();
+    if (all) {
+        finish(s, b, r, W, n, want, L);
+        drawn = true;
+        return in;
+    }
     if (n <= kList) return rank_list(n, above, want, weight, L);
     // more tokens than the list holds: by the digits of their logits' order
     low = wave_min(low);
@@ -992,13 +1003,21 @@ __device__ __forceinline__ Prefix border(const Row<BF16>& row, const float* tops
     return nth_equal(row, tops, v0, (want - above + one - 1) / one, L);
 }
 
+// A row without a token that can be drawn.
+__device__ __forceinline__ bool no_token(const SampleSpace& s, int b, const Ask& r) {
+    if (r.top != -INFINITY) return false;
+    if (threadIdx.x == 0) {
+        s.a.ids[b] = -1;
+        s.a.probs[b] = 0.f;
+    }
+    return true;
+}
 // The first token in the order: of the largest logits the one at the lowest
 // index.
 template <int NT, bool BF16>
 __device__ __forceinline__ void first_token(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r,
-                                            BlockLds<NT>& L) {
+                                            const float* tops, BlockLds<NT>& L) {
     const int tid = threadIdx.x, lane = tid & 63;
-    const float* tops = s.tops + (int64_t)b * s.nt;
     if (tid == 0) L.found[0] = ~0ull;
     __syncthreads();
     for (int i = tid; i < s.nt; i += NT)
@@ -1024,7 +1043,7 @@ __device__ __forceinline__ void first_token(const SampleSpace& s, const Row<BF16
 // The draw, from the tiles' sums.
 template <int NT, bool BF16>
 __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r, const Weights& W,
-                                     Prefix kept, const uint64_t* sums, BlockLds<NT>& L) {
+                                     Prefix kept, const float* tops, const uint64_t* sums, BlockLds<NT>& L) {
     const int tid = threadIdx.x, lane = tid & 63;
     const double least = (double)r.least;
     const int per = (s.nt + NT - 1) / NT, t0 = min(tid * per, s.nt), t1 = min(t0 + per, s.nt);
@@ -1032,7 +1051,7 @@ __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row,
     for (int i = t0; i < t1; ++i) mine += sums[i];
     uint64_t before = block_before<NT>(mine, L, &all);
     if (all == 0) {  // min_p above every weight
-        first_token<NT>(s, row, b, r, L);
+        first_token<NT>(s, row, b, r, tops, L);
         return;
     }
     const uint64_t pass = draw_at(s, b, all);
@@ -1084,6 +1103,50 @@ __device__ __forceinline__ void draw(const SampleSpace& s, const Row<BF16>& row,
     }
 }
 
+// A top_k up to the number of tiles: whether that was all (drawn), or the border.
+// tiles: room for a list of them.
+template <bool BF16>
+__device__ __forceinline__ bool few(const SampleSpace& s, const Row<BF16>& row, int b, const Ask& r, const Weights& W,
+                                    const float* tops, int* tiles, Prefix& kept, BorderLds& L) {
+    // at least k tokens lie at or above the k-th largest of the tiles' tops
+    const int tid = threadIdx.x, lane = tid & 63;
+    const Scale S = scale_of_count(r);
+    for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < s.nt; i += kBorderNT)
+        if (tops[i] > -INFINITY) add(&L.bins[S.bin(tops[i])], 1);
+    __syncthreads();
+    find_bin<kBorderNT>(L.bins, 0, [&](uint64_t) { return (uint64_t)r.k; }, L.block);
+    const int last = min((int)L.block.found[0], kBins - 1);
+    if (tid == 0) L.block.count = 0;
+    __syncthreads();
+    for (int i = tid; i < row.tiles; i += kBorderNT)
+        if (tops[i] > -INFINITY && S.bin(tops[i]) <= last) tiles[atomicAdd(&L.block.count, 1u)] = i;
+    __syncthreads();
+    const int live = (int)L.block.count;
+    __syncthreads();
+    if (tid == 0) L.block.count = 0;
+    __syncthreads();
+    each_listed<kBorderNT>(
+        row, tiles, live, [&](int t, const float(&v)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (v[j] > -INFINITY && S.bin(v[j]) <= last) {
+                    const uint32_t at = atomicAdd(&L.block.count, 1u);
+                    if (at < kList) L.list[at] = token(v[j], row.index(t, j, lane));
+                }
+        });
+    __syncthreads();
+    const int n = (int)L.block.count;
+    bool drawn = n <= kList;
+    if (drawn) {
+        finish(s, b, r, W, n, 0, L);
+        return true;
+    }
+    kept = border<BF16, false>(s, b, row, tops, r, W, Prefix{-INFINITY, -1}, S, last, L, false, drawn);
+    return drawn;
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s) {
     extern __shared__ float lds_tops[];  // [nt], then a list of tiles
@@ -1094,45 +1157,12 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
     const Row<BF16> row(s.a, b);
     const Weights W = weights_of(s, r);
     const float* tops = lds_tops;
-    int* tiles = reinterpret_cast<int*>(lds_tops + s.nt);
     for (int i = tid; i < s.nt; i += kBorderNT) lds_tops[i] = s.tops[(int64_t)b * s.nt + i];
     const Prefix every{-INFINITY, -1};
     Prefix kept = every;
+    bool drawn = false;
     if (r.way == kFew) {
-        // at least k tokens lie at or above the k-th largest of the tiles' tops
-        const Scale S = scale_of_count(r);
-        for (int i = tid; i < kBins; i += kBorderNT) L.bins[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < s.nt; i += kBorderNT)
-            if (tops[i] > -INFINITY) add(&L.bins[S.bin(tops[i])], 1);
-        __syncthreads();
-        find_bin<kBorderNT>(L.bins, 0, [&](uint64_t) { return (uint64_t)r.k; }, L.block);
-        const int last = min((int)L.block.found[0], kBins - 1), lane = tid & 63;
-        if (tid == 0) L.block.count = 0;
-        __syncthreads();
-        for (int i = tid; i < row.tiles; i += kBorderNT)
-            if (tops[i] > -INFINITY && S.bin(tops[i]) <= last) tiles[atomicAdd(&L.block.count, 1u)] = i;
-        __syncthreads();
-        const int live = (int)L.block.count;
-        __syncthreads();
-        if (tid == 0) L.block.count = 0;
-        __syncthreads();
-        each_listed<kBorderNT>(
-            row, tiles, live, [&](int t, const float(&v)[8]) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (v[j] > -INFINITY && S.bin(v[j]) <= last) {
-                        const uint32_t at = atomicAdd(&L.block.count, 1u);
-                        if (at < kList) L.list[at] = token(v[j], row.index(t, j, lane));
-                    }
-            });
-        __syncthreads();
-        const int n = (int)L.block.count;
-        if (n <= kList) {
-            finish(s, b, r, W, n, 0, L);
-            return;
-        }
-        kept = border<BF16, false>(row, tops, r, W, every, S, last, L);
+        drawn = few(s, row, b, r, W, tops, reinterpret_cast<int*>(lds_tops + s.nt), kept, L);
     } else {
         const bool mass = r.way == kMass;
         const uint64_t want = find_bin<kBorderNT>(
@@ -1145,19 +1175,59 @@ __global__ __launch_bounds__(kBorderNT) void sample_border_kernel(SampleSpace s)
         if (bin < kBins && n <= kList) {
             for (int i = tid; i < n; i += kBorderNT) L.list[i] = s.list[(int64_t)b * kList + i];
             __syncthreads();
-            if (short_list(s, b, mass, W, S, bin, above)) {
+            drawn = short_list(mass, W, S, bin, above + s.bins[(int64_t)b * kBins + bin]);
+            if (drawn)
                 finish(s, b, r, W, n, want, L);
-                return;
-            }
-            kept = rank_list(n, above, want, [&](float v) -> uint64_t { return mass ? W.whole(W.of(v)) : 1; }, L);
+            else
+                kept = rank_list(n, above, want, [&](float v) -> uint64_t { return mass ? W.whole(W.of(v)) : 1; }, L);
         } else if (bin < kBins) {
-            kept = mass ? border<BF16, true>(row, tops, r, W, every, S, kBins - 1, L)
-                        : border<BF16, false>(row, tops, r, W, every, S, kBins - 1, L);
+            kept = mass ? border<BF16, true>(s, b, row, tops, r, W, every, S, kBins - 1, L, false, drawn)
+                        : border<BF16, false>(s, b, row, tops, r, W, every, S, kBins - 1, L, false, drawn);
         }
     }
-    if (r.k && r.p < 1.f)
-        kept = border<BF16, true>(row, tops, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L);
-    if (tid == 0) s.state[b].kept = kept;
+    if (!drawn && r.k && r.p < 1.f)
+        kept = border<BF16, true>(s, b, row, tops, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L, false, drawn);
+    if (tid == 0) {
+        s.state[b].drawn = drawn;
+        s.state[b].kept = kept;
+    }
+}
+
+// Everything of a row by one workgroup, in one launch.
+template <bool BF16>
+__global__ __launch_bounds__(kBorderNT) void sample_row_kernel(SampleSpace s) {
+    extern __shared__ uint64_t lds_sums[];  // [nt], then the tiles' largest logits, then a list of tiles
+    __shared__ BorderLds L;
+    const int tid = threadIdx.x, lane = tid & 63, b = blockIdx.x;
+    float* tops = reinterpret_cast<float*>(lds_sums + s.nt);
+    const Row<BF16> row(s.a, b);
+    each_tile<kBorderNT>(
+        row, 0, row.tiles, [](int) { return true; }, [&](int t, const float(&v)[8]) { tile_top(tops, t, v, lane); });
+    for (int t = row.tiles + tid; t < s.nt; t += kBorderNT) tops[t] = -INFINITY;
+    __syncthreads();
+    const Ask r = find_way(s, b, tops, L.block);
+    __syncthreads();
+    if (no_token(s, b, r)) return;
+    if (r.way == kDone) {
+        first_token(s, row, b, r, tops, L.block);
+        return;
+    }
+    const Weights W = weights_of(s, r);
+    const Prefix every{-INFINITY, -1};
+    Prefix kept = every;
+    bool drawn = false;
+    if (r.way == kFew)
+        drawn = few(s, row, b, r, W, tops, reinterpret_cast<int*>(tops + s.nt), kept, L);
+    else if (r.way == kCount)
+        kept = border<BF16, false>(s, b, row, tops, r, W, every, scale_of_count(r), kBins - 1, L, true, drawn);
+    if (!drawn && r.p < 1.f)
+        kept = border<BF16, true>(s, b, row, tops, r, W, kept, scale_of_mass(r, W, s.a.V), kBins - 1, L,
+                                  r.way == kMass, drawn);
+    if (drawn) return;
+    tile_sums<kBorderNT>(s, row, tops, 0, row.tiles, r, W, kept, lds_sums);
+    for (int t = row.tiles + tid; t < s.nt; t += kBorderNT) lds_sums[t] = 0;
+    __syncthreads();
+    draw(s, row, b, r, W, kept, tops, lds_sums, L.block);
 }
 
 template <bool BF16>
@@ -1166,7 +1236,7 @@ __global__ __launch_bounds__(kTilesNT) void sample_sums_kernel(SampleSpace s) {
     const Ask r = known_way(s, b);
     if (s.state[b].drawn || r.way == kDone || r.way == kSums) return;
     const Row<BF16> row(s.a, b);
-    tile_sums<kTilesNT>(s, row, b, t0, t0 + s.per_wg, r, weights_of(s, r), s.state[b].kept,
+    tile_sums<kTilesNT>(s, row, s.tops + (int64_t)b * s.nt, t0, t0 + s.per_wg, r, weights_of(s, r), s.state[b].kept,
                         s.sums + (int64_t)b * s.nt);
 }
 
@@ -1175,27 +1245,30 @@ __global__ __launch_bounds__(kTilesNT) void sample_draw_kernel(SampleSpace s) {
     __shared__ BlockLds<kTilesNT> L;
     const int b = blockIdx.x;
     const Ask r = known_way(s, b);
-    if (s.state[b].drawn) return;
-    if (r.top == -INFINITY) {
-        if (threadIdx.x == 0) {
-            s.a.ids[b] = -1;
-            s.a.probs[b] = 0.f;
-        }
-        return;
-    }
+    if (s.state[b].drawn || no_token(s, b, r)) return;
     const Row<BF16> row(s.a, b);
+    const float* tops = s.tops + (int64_t)b * s.nt;
     if (r.way == kDone) {
-        first_token<kTilesNT>(s, row, b, r, L);
+        first_token<kTilesNT>(s, row, b, r, tops, L);
         return;
     }
     const Prefix kept = r.way == kSums ? Prefix{-INFINITY, -1} : s.state[b].kept;
-    draw<kTilesNT>(s, row, b, r, weights_of(s, r), kept, s.sums + (int64_t)b * s.nt, L);
+    draw<kTilesNT>(s, row, b, r, weights_of(s, r), kept, tops, s.sums + (int64_t)b * s.nt, L);
 }
 
 // -------------------------------------------------------------------- host --
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Whether a row is one workgroup's from end to end: where it is short, or where
+// rows fill the chip. 16000 bf16 logits of 1 row with top_k 50 and top_p 0.9 18
+// against 25 us over the chip, with top_p alone 21 against 27, of 48 rows with
+// filters of every kind 23 against 34; 65536 of 1 row 15, 67 and 27 against 20,
+// 36 and 19; of 48 rows with every kind 38 both ways; 131072 of 256 rows 67
+// against 72, of 512 149 against 118.
+static bool one_a_row(int B, int V) { return V <= (B >= 128 ? 131072 : B >= 32 ? 65536 : 32768); }
+
 size_t sample_workspace(int B, int V) {
+    if (one_a_row(B, V)) return 0;
     const size_t tiles = (size_t)B * sample_tiles(V);
     return align256((size_t)B * kBins * 8) + align256(tiles * 8) + align256((size_t)B * kList * 8) +
            align256(tiles * 4) + align256((size_t)B * sizeof(RowState));
@@ -1204,6 +1277,8 @@ size_t sample_workspace(int B, int V) {
 template <bool BF16>
 static hipError_t run(const SampleSpace& s, hipStream_t st, StageTimer* tm) {
     const dim3 tiles((s.nt + s.per_wg - 1) / s.per_wg, s.a.B), rows(s.a.B);
+    if (one_a_row(s.a.B, s.a.V))
+        return launch_shm(tm, "sample_row", sample_row_kernel<BF16>, rows, dim3(kBorderNT), s.nt * 16, st, s);
     const bool filters = s.a.top_k || s.a.top_p;
     hipError_t e = launch(tm, "sample_tops", sample_tops_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
     if (e == hipSuccess)

@@ -140,6 +140,10 @@ def test_sample_workspace():
     if n:
         assert draw(ws=None) == lora.LORA_ESPACE and draw(wsb=n - 1) == lora.LORA_ESPACE
         assert draw(ws=P16 + 16392) == lora.LORA_ESPACE and draw(ws=P16 + 8192) == lora.LORA_EINVAL
+    big = dict(V=200000, stride=200000)
+    n = L.lora_sample_workspace_bytes(2, 200000)
+    assert n > 0 and draw(ws=None, **big) == lora.LORA_ESPACE and draw(wsb=n - 1, **big) == lora.LORA_ESPACE
+    assert draw(ws=P16 + 16392, **big) == lora.LORA_ESPACE and draw(ws=P16 + 8192, **big) == lora.LORA_EINVAL
 
 
 def test_binding_refuses_host_tensors():

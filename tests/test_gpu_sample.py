@@ -264,3 +264,34 @@ def test_binding_refuses():
         lora.sample(torch.zeros(2, 0, device="cuda"), u)
     ids, probs = lora.sample(torch.zeros(0, 9, device="cuda"), u[:0])
     assert ids.shape == (0,) and probs.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_few_rows_and_many(dtype):
+    """Rows of a small batch, whose passes are spread over the chip, and of one that
+    takes a workgroup a row give the same bits: rows of every kind, filters of
+    every kind."""
+    V, kinds = 40000, 8
+    x = logits(kinds, V, dtype, seed=2)
+    x[1] = 1.5  # all equal
+    x[2] = torch.randint(0, 3, (V,), device="cuda").to(dtype)  # many of few values
+    x[3, 5:] = -float("inf")
+    x[4] = float("nan")
+    x[5, ::7] = float("inf")
+    x[6, 1::2] = float("nan")
+    x[7] = torch.linspace(-300.0, 300.0, V, device="cuda").to(dtype)
+    g = np.random.default_rng(11)
+    for n in range(12):
+        u = torch.from_numpy(g.random(kinds)).cuda()
+        t = torch.from_numpy(g.choice([0.0, 0.3, 1.0, 40.0], kinds).astype(np.float32)).cuda()
+        k = torch.from_numpy(g.choice([0, 1, 30, 3000, V - 1], kinds).astype(np.int32)).cuda()
+        p = torch.from_numpy(g.choice([0.0, 0.1, 0.9, 0.9999, 1.0], kinds).astype(np.float32)).cuda()
+        least = torch.from_numpy(g.choice([0.0, 0.01, 2.0], kinds).astype(np.float32)).cuda()
+        for use in (dict(), dict(temperature=t), dict(temperature=t, top_k=k), dict(top_p=p),
+                    dict(temperature=t, top_k=k, top_p=p, min_p=least)):
+            ids, probs = lora.sample(x, u, **use)
+            many = {name: v.repeat(4) for name, v in use.items()}
+            ids4, probs4 = lora.sample(x.repeat(4, 1), u.repeat(4), **many)
+            assert torch.equal(ids.repeat(4), ids4) and torch.equal(probs.repeat(4), probs4), (n, sorted(use))
+    L = lora.lib()  # the two ways: with a workspace and without
+    assert L.lora_sample_workspace_bytes(kinds, V) > 0 and L.lora_sample_workspace_bytes(4 * kinds, V) == 0
