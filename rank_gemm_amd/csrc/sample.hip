@@ -8,9 +8,9 @@
 // No long row is sorted. The border of a prefix is found by a histogram of the
 // tokens over bins of equal width below the largest logit, and by ranking the
 // tokens of the one bin that holds it; the draw goes by sums over tiles of 512
-// tokens and then through one tile. Short rows, and rows of batches that fill
-// the chip, are a workgroup's each from end to end, in one launch. Every pass
-// over others is spread over the chip, tile by tile:
+// tokens and then through one tile. Short rows are a workgroup's each from end
+// to end, in one launch. Every pass over others is spread over the chip, tile by
+// tile:
 //   tops     the largest logit of each tile
 //   bins     the histogram (top_p, or a top_k past the number of tiles); rows
 //            without those filters: the tiles' sums at once
@@ -25,9 +25,9 @@
 //   draw     a workgroup a request
 // Bound by that chain: of one row of 131072 with top_k 50 and top_p 0.9 (20 us)
 // the border's workgroup takes 8 and each launch, busy or not, 2.4; the one
-// launch over 32000 takes 14. Many rows by the passes of a CU over its own: 256
-// of 131072 bf16 with top_k 50 and top_p 0.9 22 us (3.1 TB/s), with no filter 57,
-// of which the 64-bit exponentials, some 20 operations a token, are 40.
+// launch over 32000 takes 14. Of 256 rows of 131072 fp32 (134 MB) with filters of
+// every kind (100 us) tops reads at 6.5 TB/s (20 us), and bins takes 30: the 64-bit
+// exponentials are some 20 operations a token. With no filter they are 46 of 68.
 //
 // Weights are 64-bit exponentials held as whole numbers of 2^-shift, so that
 // sums do not depend on the order in which they are made: equal inputs give
@@ -1259,13 +1259,14 @@ __global__ __launch_bounds__(kTilesNT) void sample_draw_kernel(SampleSpace s) {
 // -------------------------------------------------------------------- host --
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Whether a row is one workgroup's from end to end: where it is short, or where
-// rows fill the chip. 16000 bf16 logits of 1 row with top_k 50 and top_p 0.9 18
-// against 25 us over the chip, with top_p alone 21 against 27, of 48 rows with
-// filters of every kind 23 against 34; 65536 of 1 row 15, 67 and 27 against 20,
-// 36 and 19; of 48 rows with every kind 38 both ways; 131072 of 256 rows 67
-// against 72, of 512 149 against 118.
-static bool one_a_row(int B, int V) { return V <= (B >= 128 ? 131072 : B >= 32 ? 65536 : 32768); }
+// Whether a row is one workgroup's from end to end: where it is short, or less
+// short and rows are many. 16000 bf16 logits of 1 row with top_k 50 and top_p 0.9
+// 18 against 25 us over the chip, with top_p alone 21 against 27, of 48 rows with
+// filters of every kind 23 against 34. 65536 of 1 row 15, 67 and 27 against 20, 36
+// and 19; of 48 rows with every kind 38 both ways, of 256 40 against 57. Past that
+// the row that takes longest holds up the rest: 256 of 131072 fp32, every kind,
+// 139 against 103.
+static bool one_a_row(int B, int V) { return V <= (B >= 32 ? 65536 : 32768); }
 
 size_t sample_workspace(int B, int V) {
     if (one_a_row(B, V)) return 0;
