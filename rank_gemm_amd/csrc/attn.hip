@@ -30,10 +30,9 @@
 // Bound by HBM: 64 requests of 4096 to 16384 positions, 32 heads over 8 of 128,
 // bf16 (2.7 GB) 471 us, 5.7 TB/s (a 1 GiB copy moves 5.1); without the second
 // halves of P it is no faster. Rows of 128 bytes of a head (8-bit, [page][row]
-// [head]) come at 5.0 TB/s; of 64 bytes at 3.3, as the other half of each
-// 128-byte line is another head's, which another workgroup reads at its own
-// time. 1 request of 131072 positions, 8-bit (268 MB): 57 us and 4 for the join;
-// some 8 us of every call are its beginning and end.
+// [head]) come at 5.0 TB/s, of 64 bytes, two heads of them together, at 5.1. 1
+// request of 131072 positions, 8-bit (268 MB): 49 us and 4 to 7 for the join; some
+// 8 us of every call are its beginning and end.
 #include <algorithm>
 
 #include "fuse.h"
@@ -50,6 +49,8 @@ struct AttnPlan {
     int rows;         // rows a request: kv heads x head blocks
     int blocks;       // head blocks a kv head
     int block_heads;  // heads a block
+    int hd;           // dimensions of a head: a.c.dim, or half of it where kv heads go in pairs
+    int pair;         // heads of the first kv head of a pair; 0: no pairs
     uint32_t magic;   // position / page_rows = umulhi(position, magic) >> shift (page_rows > 1)
     int shift;
     int whole;        // whole tiles by AttnTile::group
@@ -60,11 +61,13 @@ struct AttnPlan {
 
 // DP: dimensions padded to 64, 128 or 256 (zeros behind dim). RT: 16-head
 // blocks of a kv head's heads. W: waves a workgroup: 4, or 8 where a workgroup
-// takes a row from end to end and two waves a SIMD have the registers.
-template <int DP_, bool F8_, int RT_, int W_>
+// takes a row from end to end and two waves a SIMD have the registers. PAIR: two
+// kv heads as one, each of half the dimensions, which is one 64-byte chunk of the
+// reads of keys.
+template <int DP_, bool F8_, int RT_, int W_, bool PAIR_ = false>
 struct AttnCfg {
     static constexpr int DP = DP_, RT = RT_, W = W_;
-    static constexpr bool F8 = F8_;
+    static constexpr bool F8 = F8_, PAIR = PAIR_;
     static constexpr int ROWB = DP * (F8 ? 1 : 2);  // bytes of a row in LDS
     static constexpr int CH = ROWB / 16;            // its 16-byte chunks
     static constexpr int RW = CH < 16 ? 16 / CH : 1;  // rows of a 256-byte window (all banks)
@@ -156,6 +159,11 @@ __device__ __forceinline__ u32x4 widen8(uint32_t a, uint32_t b) {
     r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false));
     r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true));
     return r;
+}
+
+// The kv head that head h of a row reads.
+__device__ __forceinline__ int kv_head(const AttnPlan& p, int hk, int h) {
+    return p.pair ? 2 * hk + (h >= p.pair) : hk;
 }
 
 // Over the four lanes that hold a head (lane, lane ^ 16, ^ 32, ^ 48).
@@ -303,7 +311,7 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
     constexpr int DP = C::DP, RT = C::RT, NB = C::NB, NK = DP / 32, ND = DP / 16;
     const AttnArgs& a = p.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int fr = lane & 15, fg = lane >> 4, D = a.c.dim;
+    const int fr = lane & 15, fg = lane >> 4, D = p.hd;
     const int hk = row / p.blocks, hb = row % p.blocks, group = a.heads / a.c.kv_heads;
     const int h0 = hk * group + hb * p.block_heads, nq = min(p.block_heads, group - hb * p.block_heads);
     int lo, hi;
@@ -329,7 +337,8 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
             const int h = rt * 16 + fr;
             // 8-bit keys: a lane's 16-byte read holds the k of two products
             const int d = C::F8 ? (c >> 1) * 64 + fg * 16 + (c & 1) * 8 : c * 32 + fg * 8;
-            q[rt][c] = *or_zero(h < nq && d < D, a.q + b * a.q_stride + (int64_t)(h0 + h) * D + d);
+            const int at = C::PAIR ? d % (DP / 2) : d;
+            q[rt][c] = *or_zero(h < nq && at < D, a.q + b * a.q_stride + (int64_t)(h0 + h) * D + at);
         }
     AttnTile<C> tile{};
     if (nt > 0) {
@@ -344,7 +353,10 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int c = 0; c < NK; ++c) asm volatile("" : "+v"(q[rt][c]));  // it has landed
-    const float sc = a.scale_log2 * (C::F8 ? a.c.k_scale[hk] : 1.f);
+    float sc[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+        sc[rt] = a.scale_log2 * (C::F8 ? a.c.k_scale[C::PAIR ? kv_head(p, hk, min(rt * 16 + fr, nq - 1)) : hk] : 1.f);
 
     f32x4 o[RT][ND];
     float m[RT], l[RT];
@@ -380,6 +392,28 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
 #pragma unroll
                 for (int c = 0; c < NR; ++c) addr[c] = (k0 ^ ((c0 + c) << 6)) + n * 32 * C::ROWB;
                 lds_rows<4 * C::ROWB>(k[0], k[1], addr);
+                if constexpr (C::PAIR) {
+                    // each kv head's products by themselves (with zeros in q a NaN of
+                    // one would reach the other's), of which a column takes its own
+                    static_assert(RT == 1 && NR == 2 && C::CH == 2 * 4, "a chunk a kv head");
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f32x4 r[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            r[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+                            if constexpr (C::F8) {
+                                r[c] = mfma16x16x32(widen8(k[h][c][0], k[h][c][1]), q[0][2 * c], r[c]);
+                                r[c] = mfma16x16x32(widen8(k[h][c][2], k[h][c][3]), q[0][2 * c + 1], r[c]);
+                            } else {
+                                r[c] = mfma16x16x32(k[h][c], q[0][c], r[c]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[0][n][h][i] = fr < p.pair ? r[0][i] : r[1][i];
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int c = 0; c < NR; ++c)
 #pragma unroll
@@ -408,7 +442,7 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) e[n][j] = s[rt][n][j >> 2][j & 3] * sc;
+                for (int j = 0; j < 8; ++j) e[n][j] = s[rt][n][j >> 2][j & 3] * sc[rt];
             if (!all)
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
@@ -495,7 +529,6 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
     }
 
     // the waves' m, l and o joined through LDS, 16 heads at a time
-    const float vs = C::F8 ? a.c.v_scale[hk] : 1.f;
     const int64_t out_row = (int64_t)b * a.heads + h0;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -512,6 +545,7 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
         for (int i = threadIdx.x; i < 16 * (D / 4); i += 64 * C::W) {
             const int h = i / (D / 4), d4 = i % (D / 4);
             if (rt * 16 + h >= nq) break;
+            const int hq = rt * 16 + h, from = C::PAIR && hq >= p.pair ? d4 + D / 4 : d4;
             float top = L.m[0][h], den = 0.f;
             f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -520,10 +554,10 @@ __device__ __forceinline__ void attn_piece(const AttnPlan& p, AttnLds<C>& L, int
             for (int w = 0; w < C::W; ++w) {
                 const float f = __builtin_amdgcn_exp2f(L.m[w][h] - top);
                 den += f * L.l[w][h];
-                x += f * reinterpret_cast<const f32x4*>(L.kv[w])[h * (DP / 4) + (d4 ^ h)];
+                x += f * reinterpret_cast<const f32x4*>(L.kv[w])[h * (DP / 4) + (from ^ h)];
             }
-            const int hq = rt * 16 + h;
             if (whole) {
+                const float vs = C::F8 ? a.c.v_scale[C::PAIR ? kv_head(p, hk, hq) : hk] : 1.f;
                 const float r = den == 0.f ? 0.f : vs / den;
                 const u32x2 y = {pack_bf16x2(x[0] * r, x[1] * r), pack_bf16x2(x[2] * r, x[3] * r)};
                 *reinterpret_cast<u32x2*>(a.out + (out_row + hq) * D + 4 * d4) = y;
@@ -617,7 +651,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
     __shared__ float2 sml[kJoinThreads];
     const AttnArgs& a = p.a;
     const int64_t r = blockIdx.x;
-    const int b = (int)(r / p.rows), row = (int)(r - (int64_t)b * p.rows), D = a.c.dim;
+    const int b = (int)(r / p.rows), row = (int)(r - (int64_t)b * p.rows), D = p.hd;
     const int hk = row / p.blocks, hb = row % p.blocks, group = a.heads / a.c.kv_heads;
     const int nq = min(p.block_heads, group - hb * p.block_heads);
     const int64_t out_row = (int64_t)b * a.heads + hk * group + hb * p.block_heads;
@@ -625,7 +659,6 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
     attn_range(a, b, &lo, &hi);
     const int2 meta = hi > lo ? p.meta[r] : make_int2(0, 0);
     if (hi > lo && meta.y == 1) return;  // written by the first kernel
-    const float vs = F8 ? a.c.v_scale[hk] : 1.f;
     const int per = (p.block_heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * per, heads = min(per, nq - h0);
     if (heads <= 0) return;
     const int items = heads * (D / 4);
@@ -661,6 +694,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
                 x = x * f + so[threadIdx.x + n] * g;
                 m = top;
             }
+            const float vs = F8 ? a.c.v_scale[kv_head(p, hk, hb * p.block_heads + h)] : 1.f;
             const float k = l == 0.f ? 0.f : vs / l;
             const u32x2 y = {pack_bf16x2(x[0] * k, x[1] * k), pack_bf16x2(x[2] * k, x[3] * k)};
             *reinterpret_cast<u32x2*>(a.out + (out_row + h) * D + 4 * d4) = y;
@@ -714,7 +748,12 @@ auto attn_kernel(int waves) {
     return attn_decode_kernel<AttnCfg<DP, F8, RT, 4>>;
 }
 template <bool F8>
-auto attn_kernel(const Shape& s) {
+auto attn_kernel(const Shape& s, bool pair) {
+    if (pair) {
+        constexpr int DP = F8 ? 128 : 64;
+        return s.waves == 8 ? attn_decode_kernel<AttnCfg<DP, F8, 1, 8, true>>
+                            : attn_decode_kernel<AttnCfg<DP, F8, 1, 4, true>>;
+    }
     if (s.dp == 256) return attn_kernel<256, F8, 1>(s.waves);
     if (s.dp == 128) return s.rt == 1 ? attn_kernel<128, F8, 1>(s.waves) : attn_kernel<128, F8, 2>(s.waves);
     return s.rt == 1   ? attn_kernel<64, F8, 1>(s.waves)
@@ -724,14 +763,27 @@ auto attn_kernel(const Shape& s) {
 
 }  // namespace
 
+// Two neighbouring kv heads as one of twice the dimensions, where rows of one are
+// half a 128-byte line, whose rest another workgroup would read at its own time
+// (8-bit, 32 heads over 8 of 64, 16384 positions of 64 requests 208 against 337
+// us), and where they are many, if whole rows: 600 positions of 32 requests (256
+// rows) 8.4 against 10.7, of 16 8.2 against 6.5.
+static bool attn_pairs(int heads, int kv_heads, int dim, bool f8) {
+    return dim * (f8 ? 1 : 2) == 64 && kv_heads % 2 == 0 && 2 * (heads / kv_heads) <= 16;
+}
+
 size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
     size_t most = 0;
-    for (bool f8 : {false, true}) {
-        const Shape s = attn_shape(B, heads, kv_heads, dim, width * page_rows, f8);
-        if (s.wgs == 0) continue;
-        const size_t rows = (size_t)B * kv_heads * s.blocks, slots = s.wgs + rows;
+    auto add = [&](int kv, const Shape& s) {
+        if (s.wgs == 0) return;
+        const size_t rows = (size_t)B * kv * s.blocks, slots = s.wgs + rows;
         most = std::max(most, align256(slots * s.block_heads * dim * sizeof(float)) +
                                   align256(slots * s.block_heads * sizeof(float2)) + align256(rows * sizeof(int2)));
+    };
+    for (bool f8 : {false, true}) {
+        add(kv_heads, attn_shape(B, heads, kv_heads, dim, width * page_rows, f8));
+        if (attn_pairs(heads, kv_heads, dim, f8))
+            add(kv_heads / 2, attn_shape(B, heads, kv_heads / 2, 2 * dim, width * page_rows, f8));
     }
     return most;
 }
@@ -739,27 +791,40 @@ size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width,
 hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* tm) {
     // positions a request can attend to, and the ones its first tile may begin ahead of them
     const int most = a.width * a.c.page_rows;
-    const Shape s = attn_shape(a.B, a.heads, a.c.kv_heads, a.c.dim,
-                               a.window > 0 && a.window < most ? a.window + 15 : most, f8);
+    const int longest = a.window > 0 && a.window < most ? a.window + 15 : most;
+    Shape s = attn_shape(a.B, a.heads, a.c.kv_heads, a.c.dim, longest, f8);
     AttnPlan p{};
     p.a = a;
+    p.hd = a.c.dim;
     p.wgs = s.wgs;
     p.blocks = s.blocks;
     p.block_heads = s.block_heads;
     p.rows = a.c.kv_heads * s.blocks;
+    if (a.c.head_stride == a.c.dim && attn_pairs(a.heads, a.c.kv_heads, a.c.dim, f8) &&
+        (s.wgs || (int64_t)a.B * p.rows >= 256)) {
+        s = attn_shape(a.B, a.heads, a.c.kv_heads / 2, 2 * a.c.dim, longest, f8);
+        p.wgs = s.wgs;
+        p.pair = a.heads / a.c.kv_heads;
+        p.a.c.kv_heads /= 2;
+        p.a.c.dim *= 2;
+        p.a.c.head_stride *= 2;
+        p.blocks = s.blocks;
+        p.block_heads = s.block_heads;
+        p.rows = p.a.c.kv_heads;
+    }
     // t / P for t < 2^31: with 2^(sh) < P <= 2^(sh + 1) and magic =
     // floor(2^(32 + sh) / P) + 1, t magic / 2^(32 + sh) is over t / P by less than 1 / P
     int sh = 0;
     while ((2ll << sh) < a.c.page_rows) ++sh;
     p.shift = sh;
     p.magic = a.c.page_rows > 1 ? (uint32_t)((1ull << (32 + sh)) / a.c.page_rows + 1) : 0;
-    p.whole = a.c.page_rows % 16 == 0 && a.c.dim == s.dp && a.c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
+    p.whole = a.c.page_rows % 16 == 0 && p.a.c.dim == s.dp && a.c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
     const size_t rows = (size_t)a.B * p.rows, slots = s.wgs + rows;
     char* ws = static_cast<char*>(a.workspace);
     p.part = reinterpret_cast<float*>(ws);
-    p.ml = reinterpret_cast<float2*>(ws + align256(slots * s.block_heads * a.c.dim * sizeof(float)));
+    p.ml = reinterpret_cast<float2*>(ws + align256(slots * s.block_heads * p.hd * sizeof(float)));
     p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.ml) + align256(slots * s.block_heads * sizeof(float2)));
-    auto kernel = f8 ? attn_kernel<true>(s) : attn_kernel<false>(s);
+    auto kernel = f8 ? attn_kernel<true>(s, p.pair) : attn_kernel<false>(s, p.pair);
     const uint32_t grid = s.wgs ? s.wgs : (uint32_t)rows;
     hipError_t e = launch(tm, "attn_decode", kernel, dim3(grid), dim3(64 * s.waves), st, p);
     if (e != hipSuccess || s.wgs == 0) return e;

@@ -161,7 +161,9 @@ SHAPES = [  # lengths, heads, kv heads, dim, page
     ([257, 64], 130, 2, 128, 16), ([600, 50], 70, 1, 256, 32), ([90] * 33, 4, 4, 16, 16), ([33, 1025], 28, 4, 176, 128),
     ([2049], 17, 17, 128, 3), ([300, 70], 100, 2, 64, 16), ([900, 5, 1600], 96, 2, 48, 16), ([1300] + [9] * 63, 40, 2, 128, 16),
     ([700] + [20] * 63, 4, 2, 256, 16), ([2000, 0] + [30] * 150, 2, 2, 64, 16), ([1536, 1000], 8, 2, 128, 16),
-    ([1537, 600], 8, 2, 128, 16), ([512], 32, 2, 256, 32), ([513, 100], 24, 1, 128, 16)]
+    ([1537, 600], 8, 2, 128, 16), ([512], 32, 2, 256, 32), ([513, 100], 24, 1, 128, 16), ([3000, 77, 1], 8, 4, 64, 16),
+    ([2500, 2501], 16, 2, 64, 24), ([2100, 0, 5], 6, 6, 32, 16), ([1999], 4, 2, 48, 5), ([2222, 1700], 12, 2, 16, 64),
+    ([300, 0, 1] + [7] * 150, 8, 4, 64, 16), ([1900] + [20] * 255, 4, 2, 32, 10)]
 
 
 @pytest.mark.parametrize("form", ["bf16", "f8"])
@@ -293,6 +295,31 @@ def test_infinite_keys():
     c.k[c.table[0, 17], 3, 0, 7] = float("inf")
     got = lora.attn_decode(q, c.k, c.v, table, lengths)
     assert bool(got[0, :4].isnan().all()) and torch.equal(got[0, 4:], out[0, 4:]) and torch.equal(got[1], out[1])
+
+
+@pytest.mark.parametrize("lengths", [[2500], [300] * 130])
+@pytest.mark.parametrize("dim,form", [(64, "f8"), (32, "bf16")])
+def test_neighbouring_kv_heads_are_apart(dim, form, lengths):
+    """A NaN (and an infinity) in the rows of one kv head reaches its heads alone,
+    also where two kv heads share a line of memory."""
+    c = Cache(lengths, 4, dim, 16, form)
+    table, n = c.tensors()
+    B = len(lengths)
+    q = torch.randn(B, 8, dim, device="cuda").to(torch.bfloat16)
+    call = lambda: lora.attn_decode(q, c.k, c.v, table, n, k_scale=c.ks, v_scale=c.vs)
+    want = call()
+    for bad in (float("nan"),) if form == "f8" else (float("nan"), float("inf")):
+        for head in range(4):
+            for x in (c.k, c.v):
+                at = (int(c.table[0, 7]), 5, head)
+                raw = x[at].clone()
+                x[at] = torch.full((dim,), bad, device="cuda").to(x.dtype)
+                got = call()
+                hit = torch.zeros_like(got, dtype=torch.bool)
+                hit[0, 2 * head:2 * head + 2] = True
+                assert not bool(got[hit].isfinite().any()) and torch.equal(got[~hit], want[~hit])
+                x[at] = raw
+    assert torch.equal(want, call())
 
 
 def test_shared_pages():
