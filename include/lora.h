@@ -672,8 +672,9 @@ int lora_sample(int dtype, const void* logits, int64_t stride, int B, int V, con
  * Between lora_profile_begin and lora_profile_end, lora_linear,
  * lora_linear_multi, lora_shrink, lora_mx4_quantize, lora_mx4_dequantize,
  * lora_linear_mx4, lora_moe_*, lora_kv_append, lora_attn_decode and
- * lora_sample record a HIP event pair around every kernel they launch, on the stream it is launched on (not while that stream is being
- * captured into a graph, and at most max_records kernels).
+ * lora_sample record a HIP event pair around every kernel they launch, on the
+ * stream it is launched on (not while that stream is being captured into a
+ * graph, and at most max_records kernels).
  * lora_profile_end waits for the recorded events and writes one entry per
  * kernel name, in first-launch order, into out[0..cap): count, mean, min,
  * max and median duration; *n_out receives the number of names. Profiling

@@ -824,7 +824,8 @@ int lora_attn_decode(const lora_kv_cache* c, const void* q, int64_t q_stride, in
     if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return LORA_ESPACE;
     for (const void* o : {(const void*)out, (const void*)lse})
         for (const void* in : {q, (const void*)table, (const void*)lengths, (const void*)c->k, (const void*)c->v,
-                               (const void*)c->k_scale, (const void*)c->v_scale, (const void*)(need > 0 ? workspace : nullptr)})
+                               (const void*)c->k_scale, (const void*)c->v_scale,
+                               (const void*)(need > 0 ? workspace : nullptr)})
             if (o && o == in) return LORA_EINVAL;
     if (out == lse) return LORA_EINVAL;
     hipStream_t st = as_stream(stream);

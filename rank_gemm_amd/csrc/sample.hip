@@ -1286,7 +1286,8 @@ static hipError_t run(const SampleSpace& s, hipStream_t st, StageTimer* tm) {
         e = launch(tm, "sample_bins", sample_bins_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
     if (e == hipSuccess && filters) {
         e = launch(tm, "sample_gather", sample_gather_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
-        if (e == hipSuccess) e = launch_shm(tm, "sample_border", sample_border_kernel<BF16>, rows, dim3(kBorderNT), s.nt * 8, st, s);
+        if (e == hipSuccess)
+            e = launch_shm(tm, "sample_border", sample_border_kernel<BF16>, rows, dim3(kBorderNT), s.nt * 8, st, s);
         if (e == hipSuccess) e = launch(tm, "sample_sums", sample_sums_kernel<BF16>, tiles, dim3(kTilesNT), st, s);
     }
     if (e == hipSuccess) e = launch(tm, "sample_draw", sample_draw_kernel<BF16>, rows, dim3(kTilesNT), st, s);

@@ -185,6 +185,14 @@ def test_window(window):
     check(Cache([40, 257, 1999], 2, 80, 24, "f8"), 6, window=window)
 
 
+@pytest.mark.parametrize("window", [17, 1700, 2300])
+@pytest.mark.parametrize("dim,form,page", [(64, "f8", 16), (64, "f8", 24), (32, "bf16", 16)])
+def test_window_over_pairs(dim, form, page, window):
+    """Kv heads that share a line of memory, in long rows and in many."""
+    check(Cache([40, 2600, 0, 1999], 4, dim, page, form), 12, window=window)
+    check(Cache([2100] + [30] * 64, 4, dim, page, form), 8, window=window)
+
+
 @pytest.mark.parametrize("n,heads,kv,dim,page,form", [(40000, 8, 2, 128, 64, "bf16"), (70001, 4, 1, 64, 16, "f8"),
                                                       (33333, 32, 8, 128, 16, "f8"), (20011, 2, 1, 256, 11, "bf16")])
 def test_long(n, heads, kv, dim, page, form):
