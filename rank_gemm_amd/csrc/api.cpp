@@ -832,7 +832,8 @@ int lora_attn_decode(const lora_kv_cache* c, const void* q, int64_t q_stride, in
     std::unique_lock<std::mutex> lk(profiler().mu, std::defer_lock);
     if (profiler().on) lk.lock();
     const lora::AttnArgs a{kernel_cache(*c), (const uint16_t*)q, q_stride, heads, B, table, table_stride, width, lengths,
-                           (float)((double)scale * 1.4426950408889634), window, (uint16_t*)out, lse, workspace};
+                           (float)((double)scale * 1.4426950408889634), window, (uint16_t*)out, lse, workspace,
+                           workspace ? workspace_bytes : 0};
     return lora::attn_decode(a, c->form == LORA_F8, st, timer_for(st)) == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 

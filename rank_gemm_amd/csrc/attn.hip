@@ -35,6 +35,7 @@
 // 8 us of every call are its beginning and end.
 #include <algorithm>
 
+#include "attn_plan.h"
 #include "fuse.h"
 #include "kernels.h"
 
@@ -707,40 +708,6 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnPlan p) {
 // ------------------------------------------------------------------- host --
 namespace {
 
-size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
-
-struct Shape {
-    int dp, rt, blocks, block_heads, waves, wgs;
-};
-Shape attn_shape(int B, int heads, int kv_heads, int dim, int longest, bool f8) {
-    Shape s;
-    s.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-    // heads a workgroup: as many as its registers hold
-    const int group = heads / kv_heads, most = s.dp == 256 ? 16 : s.dp == 128 ? 32 : 64;
-    s.blocks = cdiv(group, most);
-    s.block_heads = cdiv(group, s.blocks);
-    s.rt = s.block_heads <= 16 ? 1 : s.block_heads <= 32 ? 2 : 4;
-    const int64_t rows = (int64_t)B * kv_heads * s.blocks;
-    // 8 waves a workgroup where that is all there is to fill a CU, and two waves a
-    // SIMD have the registers: bf16, 32 heads over 8 of 128, 1024 positions of 1
-    // request (8 rows) 9.5 against 12.0 us with 4, 600 of 16 (128 rows) 10.6 against
-    // 11.5, 128 of 64 (512 rows) 9.7 against 6.7
-    const bool wide = rows <= 256 && s.dp * s.rt <= 128;
-    // Short rows go to a workgroup each from end to end, which saves finding the
-    // parts and the join (some 8 us): the same heads, 1000 positions of 1 request
-    // 10.4 against 14.1 us, 2048 15.2 against 12.5; of 64 requests of 1 to 2048
-    // 52 against 56 us, to 3300 93 against 92; 16 heads over 4 of 256, 600
-    // positions of 1 request 16.0 against 14.3
-    if (longest <= (rows >= 128 ? 2048 : wide ? 1536 : 512)) {
-        s.wgs = 0;
-        s.waves = wide ? 8 : 4;
-    } else {  // two workgroups a CU, where their LDS allows it
-        s.wgs = s.dp * (f8 ? 1 : 2) > 256 ? 256 : 512;
-        s.waves = 4;
-    }
-    return s;
-}
-
 template <int DP, bool F8, int RT>
 auto attn_kernel(int waves) {
     if constexpr (DP * RT <= 128)
@@ -748,7 +715,7 @@ auto attn_kernel(int waves) {
     return attn_decode_kernel<AttnCfg<DP, F8, RT, 4>>;
 }
 template <bool F8>
-auto attn_kernel(const Shape& s, bool pair) {
+auto attn_kernel(const AttnShape& s, bool pair) {
     if (pair) {
         constexpr int DP = F8 ? 128 : 64;
         return s.waves == 8 ? attn_decode_kernel<AttnCfg<DP, F8, 1, 8, true>>
@@ -763,74 +730,47 @@ auto attn_kernel(const Shape& s, bool pair) {
 
 }  // namespace
 
-// Two neighbouring kv heads as one of twice the dimensions, where rows of one are
-// half a 128-byte line, whose rest another workgroup would read at its own time
-// (8-bit, 32 heads over 8 of 64, 16384 positions of 64 requests 208 against 337
-// us), and where they are many, if whole rows: 600 positions of 32 requests (256
-// rows) 8.4 against 10.7, of 16 8.2 against 6.5.
-static bool attn_pairs(int heads, int kv_heads, int dim, bool f8) {
-    return dim * (f8 ? 1 : 2) == 64 && kv_heads % 2 == 0 && 2 * (heads / kv_heads) <= 16;
-}
-
 size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width, int page_rows) {
-    size_t most = 0;
-    auto add = [&](int kv, const Shape& s) {
-        if (s.wgs == 0) return;
-        const size_t rows = (size_t)B * kv * s.blocks, slots = s.wgs + rows;
-        most = std::max(most, align256(slots * s.block_heads * dim * sizeof(float)) +
-                                  align256(slots * s.block_heads * sizeof(float2)) + align256(rows * sizeof(int2)));
-    };
-    for (bool f8 : {false, true}) {
-        add(kv_heads, attn_shape(B, heads, kv_heads, dim, width * page_rows, f8));
-        if (attn_pairs(heads, kv_heads, dim, f8))
-            add(kv_heads / 2, attn_shape(B, heads, kv_heads / 2, 2 * dim, width * page_rows, f8));
-    }
-    return most;
+    return attn_workspace_bytes(B, heads, kv_heads, dim, width, page_rows);
 }
 
 hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* tm) {
-    // positions a request can attend to, and the ones its first tile may begin ahead of them
-    const int most = a.width * a.c.page_rows;
-    const int longest = a.window > 0 && a.window < most ? a.window + 15 : most;
-    Shape s = attn_shape(a.B, a.heads, a.c.kv_heads, a.c.dim, longest, f8);
+    const KvCache& c = a.c;
+    const AttnLayout l = attn_layout(a.B, a.heads, c.kv_heads, c.dim, a.width, c.page_rows, a.window, f8,
+                                     c.head_stride == c.dim);
+    if (l.bytes > a.workspace_bytes) return hipErrorInvalidValue;
+    const AttnShape& s = l.s;
     AttnPlan p{};
     p.a = a;
-    p.hd = a.c.dim;
-    p.wgs = s.wgs;
-    p.blocks = s.blocks;
-    p.block_heads = s.block_heads;
-    p.rows = a.c.kv_heads * s.blocks;
-    if (a.c.head_stride == a.c.dim && attn_pairs(a.heads, a.c.kv_heads, a.c.dim, f8) &&
-        (s.wgs || (int64_t)a.B * p.rows >= 256)) {
-        s = attn_shape(a.B, a.heads, a.c.kv_heads / 2, 2 * a.c.dim, longest, f8);
-        p.wgs = s.wgs;
-        p.pair = a.heads / a.c.kv_heads;
+    p.hd = c.dim;
+    if (l.pair) {
+        p.pair = a.heads / c.kv_heads;
         p.a.c.kv_heads /= 2;
         p.a.c.dim *= 2;
         p.a.c.head_stride *= 2;
-        p.blocks = s.blocks;
-        p.block_heads = s.block_heads;
-        p.rows = p.a.c.kv_heads;
     }
+    p.wgs = s.wgs;
+    p.blocks = s.blocks;
+    p.block_heads = s.block_heads;
+    p.rows = p.a.c.kv_heads * s.blocks;
     // t / P for t < 2^31: with 2^(sh) < P <= 2^(sh + 1) and magic =
     // floor(2^(32 + sh) / P) + 1, t magic / 2^(32 + sh) is over t / P by less than 1 / P
     int sh = 0;
-    while ((2ll << sh) < a.c.page_rows) ++sh;
+    while ((2ll << sh) < c.page_rows) ++sh;
     p.shift = sh;
-    p.magic = a.c.page_rows > 1 ? (uint32_t)((1ull << (32 + sh)) / a.c.page_rows + 1) : 0;
-    p.whole = a.c.page_rows % 16 == 0 && p.a.c.dim == s.dp && a.c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
-    const size_t rows = (size_t)a.B * p.rows, slots = s.wgs + rows;
+    p.magic = c.page_rows > 1 ? (uint32_t)((1ull << (32 + sh)) / c.page_rows + 1) : 0;
+    p.whole = c.page_rows % 16 == 0 && p.a.c.dim == s.dp && c.row_stride < (1 << 24);  // 16 rows' bytes in 31 bits
     char* ws = static_cast<char*>(a.workspace);
     p.part = reinterpret_cast<float*>(ws);
-    p.ml = reinterpret_cast<float2*>(ws + align256(slots * s.block_heads * p.hd * sizeof(float)));
-    p.meta = reinterpret_cast<int2*>(reinterpret_cast<char*>(p.ml) + align256(slots * s.block_heads * sizeof(float2)));
+    p.ml = reinterpret_cast<float2*>(ws + l.ml_at);
+    p.meta = reinterpret_cast<int2*>(ws + l.meta_at);
     auto kernel = f8 ? attn_kernel<true>(s, p.pair) : attn_kernel<false>(s, p.pair);
-    const uint32_t grid = s.wgs ? s.wgs : (uint32_t)rows;
+    const uint32_t rows = (uint32_t)l.rows, grid = s.wgs ? s.wgs : rows;
     hipError_t e = launch(tm, "attn_decode", kernel, dim3(grid), dim3(64 * s.waves), st, p);
     if (e != hipSuccess || s.wgs == 0) return e;
-    const uint32_t splits = std::max(1u, std::min((uint32_t)s.block_heads, 256 / (uint32_t)rows));
+    const uint32_t splits = std::max(1u, std::min((uint32_t)s.block_heads, 256 / rows));
     return launch(tm, "attn_join", f8 ? attn_join_kernel<true> : attn_join_kernel<false>,
-                  dim3((uint32_t)rows, splits), dim3(kJoinThreads), st, p);
+                  dim3(rows, splits), dim3(kJoinThreads), st, p);
 }
 
 }  // namespace lora

@@ -218,6 +218,7 @@ struct AttnArgs {
     uint16_t* out;           // [B][heads][dim]
     float* lse;              // [B][heads] or null
     void* workspace;
+    size_t workspace_bytes;  // 0: none
 };
 size_t attn_decode_workspace(int B, int heads, int kv_heads, int dim, int width, int page_rows);
 hipError_t attn_decode(const AttnArgs& a, bool f8, hipStream_t st, StageTimer* tm);
