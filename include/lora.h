@@ -534,8 +534,10 @@ int lora_moe_experts(int form, const void* x, const int32_t* ids, const float* w
  *   bias     dev float [E], or null: it moves the choice, not the weights
  * Equal values (c, or a group's) go to the lower index; a NaN ranks below every
  * number, ids stay valid and distinct. Logits, scores and sums are held in 64
- * bits, weights rounded to fp32 once. The softmax's scores are NaN if a logit
- * is, or if the largest is infinite. Sizes, buffers, workspace and errors are
+ * bits, weights rounded to fp32 once; renormalised ones are the formula's also
+ * where the chosen scores are too small for 64 bits, and NaN where every chosen
+ * logit is -infinity. The softmax's scores are NaN if a logit is, or if the
+ * largest is infinite. Sizes, buffers, workspace and errors are
  * lora_moe_route's; LORA_EINVAL also for an unknown score, groups < 1 or E not
  * a multiple of it, top_groups outside [1, groups], k > top_groups * E /
  * groups, group_best other than 1 and 2, a scale that is not finite, and an

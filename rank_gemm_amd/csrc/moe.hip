@@ -257,12 +257,16 @@ __device__ __forceinline__ int ranked_before(const int64_t* key, int from, int e
     for (; j < end; j += step) before += key[j] > mine;
     return before;
 }
+// Chosen scores (by a bias, or by groups) whose sum is below this are near the end
+// of 64 bits, or past it, at 0. Both kinds of score are there in proportion to
+// e^l, a sigmoid to 2^-960 of itself, so that they are taken against the largest.
+constexpr double kSmallScores = 0x1p-960;
 struct ScoredLds {
-    double logits[kMoeMaxExperts];  // then the scores
+    double logits[kMoeMaxExperts], scores[kMoeMaxExperts];
     int64_t key[kMoeMaxExperts];    // of c; of experts that are not left kNotLeft
     double best[kMoeMaxExperts];    // [groups][group_best] largest c
     int left[kMoeMaxExperts];       // is this group left?
-    double sel[kMoeMaxK];
+    double sel[kMoeMaxK], sel_logit[kMoeMaxK];
 };
 __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const RouteScored& r, int32_t* ids,
                                              float* weights) {
@@ -283,9 +287,9 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
         s = r.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / den;
         c = r.bias ? s + (double)r.bias[tid] : s;
         L.key[tid] = score_key(c);
+        L.scores[tid] = s;
     }
     __syncthreads();
-    if (tid < E) L.logits[tid] = s;
     const int best = min(r.group_best, n);
     if (r.groups > 1) {
         if (tid < E) {
@@ -314,16 +318,24 @@ __device__ __forceinline__ void scored_token(ScoredLds& L, int E, int k, const R
     for (int o = 1; o < rt; o <<= 1) before += __shfl_xor(before, o);
     if (on && part == 0 && before < k) {
         ids[before] = e;
-        L.sel[before] = L.logits[e];
+        L.sel[before] = L.scores[e];
+        L.sel_logit[before] = L.logits[e];
     }
     __syncthreads();
     if (tid < k) {
-        double sum = 1.0;
+        double mine = L.sel[tid], sum = 1.0;
         if (r.renorm) {
             sum = 0.0;
             for (int j = 0; j < k; ++j) sum += L.sel[j];
+            if (sum < kSmallScores) {  // uniform
+                double most = -INFINITY;
+                for (int j = 0; j < k; ++j) most = fmax(most, L.sel_logit[j]);
+                mine = exp(L.sel_logit[tid] - most);
+                sum = 0.0;
+                for (int j = 0; j < k; ++j) sum += exp(L.sel_logit[j] - most);
+            }
         }
-        weights[tid] = (float)(L.sel[tid] / sum * (double)r.scale);
+        weights[tid] = (float)(mine / sum * (double)r.scale);
     }
 }
 
