@@ -1259,14 +1259,22 @@ __global__ __launch_bounds__(kTilesNT) void sample_draw_kernel(SampleSpace s) {
 // -------------------------------------------------------------------- host --
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Whether a row is one workgroup's from end to end: where it is short, or less
-// short and rows are many. 16000 bf16 logits of 1 row with top_k 50 and top_p 0.9
-// 18 against 25 us over the chip, with top_p alone 21 against 27, of 48 rows with
-// filters of every kind 23 against 34. 65536 of 1 row 15, 67 and 27 against 20, 36
-// and 19; of 48 rows with every kind 38 both ways, of 256 40 against 57. Past that
-// the row that takes longest holds up the rest: 256 of 131072 fp32, every kind,
-// 139 against 103.
-static bool one_a_row(int B, int V) { return V <= (B >= 32 ? 65536 : 32768); }
+// Whether a row is one workgroup's from end to end: where it is short, or longer
+// and rows fill the chip. us of a workgroup a row against over the chip, bf16, of
+// rows without a filter, with top_k 50 and top_p 0.9, with top_p 0.9 alone, of the
+// likeliest token, and of a batch with filters of every kind:
+//     1 row   of 16000    14 15   18 26   21 27    5  7   20 27
+//    16 rows  of 32768    18 15   14 21   41 38    6  8   43 48
+//     8       of 40000    19 15   14 21   46 37    6  8   37 39
+//    64       of 40960    20 18   15 21   47 45    6  9   50 50
+//    96       of 45056    22 20   15 22   52 49    6  9   55 52
+//    48       of 50021    22 18   15 22   55 45    6  9   58 50
+//    96       of 65536    28 22   15 22   71 56    7  9   72 54
+//   192       of 65536    29 31   16 27   71 76    7 12   72 65
+//   256       of 65536    30 37   16 31   72 83    7 14   72 70
+// Past that the row that takes longest holds up the rest: 256 of 131072 fp32, every
+// kind, 139 against 103.
+static bool one_a_row(int B, int V) { return V <= (B >= 192 ? 65536 : B >= 32 ? 40960 : 32768); }
 
 size_t sample_workspace(int B, int V) {
     if (one_a_row(B, V)) return 0;
