@@ -618,8 +618,9 @@ int lora_kv_append(const lora_kv_cache* cache, const void* k, const void* v, int
  * -infinity weighs nothing otherwise, one of NaN or +infinity gives NaN in all
  * dimensions, and a NaN or an infinity in v, at whatever weight, one that is not
  * finite in its own. What lies at other positions of the cache is not read.
- * Scores, sums and outputs are held in fp32, out is rounded once. The order of
- * sums depends on the lengths of the whole batch, not on time: equal inputs
+ * Scores, weights and sums are held in fp32; a weight meets v as two bf16 halves
+ * (16 bits of mantissa, off by at most 2^-17 of itself), and out is rounded
+ * once. The order of sums depends on the lengths of the whole batch, not on time: equal inputs
  * give equal bits. No output may overlap an input, the workspace or another
  * output. Asynchronous on `stream`. Errors: LORA_EINVAL (sizes, a heads that is
  * no multiple of kv_heads, B over LORA_ATTN_MAX_BATCH, B * heads over
@@ -657,7 +658,7 @@ int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride
  * other, ids[b] = -1 and probs[b] = 0. Among logits of +infinity all weigh the
  * same, and nothing else does. Weights are 64-bit exponentials, rounded to
  * whole numbers of 2^-shift (shift = 46 up to 65536 tokens, then 62 less the
- * bits of V - 1); their sums are exact, so equal inputs give equal bits.
+ * bits of V - 1; a token that weighs under half of one is not drawn); their sums are exact, so equal inputs give equal bits.
  * 1 <= V <= LORA_SAMPLE_MAX_VOCAB, B <= LORA_SAMPLE_MAX_BATCH. Asynchronous on
  * `stream`. Errors: LORA_EINVAL (sizes, unknown dtype, null, misaligned or
  * equal pointers), LORA_ESPACE, LORA_EHIP. B == 0 launches nothing.

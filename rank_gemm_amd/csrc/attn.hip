@@ -9,7 +9,8 @@
 // output o of its own (base 2):
 //   S = K q   (rows: positions, columns: heads; a lane holds 8 neighbouring
 //              positions of one head per 32)
-//   o = o f + V^T P   (rows: dimensions, columns: heads), P as two bf16 halves
+//   o = o f + V^T P   (rows: dimensions, columns: heads), P as two bf16 halves:
+//              16 bits of mantissa against the 8 of the output; l has P whole
 // The lane that holds a head's scores holds its column of P and of o too, so
 // the running maximum is shared by two lane swaps a tile and nothing else
 // moves. Keys and values go straight to LDS (kTile rows each, one buffer a
