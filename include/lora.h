@@ -609,9 +609,10 @@ int lora_kv_append(const lora_kv_cache* cache, const void* k, const void* v, int
  *   out      dev bf16 [B][heads][dim] out, overwritten completely, on 16-byte
  *            boundaries
  *   lse      dev float [B][heads] out, or null: log sum_j exp(scale q . k_j)
- *   workspace dev, at least lora_attn_decode_workspace_bytes(...) bytes (0 for
- *            some sizes: it may then be null), on a 16-byte boundary; calls that
- *            may overlap need separate ones
+ *   workspace dev, at least lora_attn_decode_workspace_bytes(...) bytes of the
+ *            call's own sizes (0 for some, also for larger batches than need one:
+ *            it may then be null), whatever the window, on a 16-byte boundary;
+ *            calls that may overlap need separate ones
  * Positions whose page number is outside [0, n_pages) are left out. A request
  * without a position (length 0, or all left out) gets zeros and an lse of
  * -infinity, and so does one all of whose scores are -infinity; a score of
@@ -651,14 +652,16 @@ int lora_attn_decode(const lora_kv_cache* cache, const void* q, int64_t q_stride
  *            top_k < 1, top_p >= 1 and min_p <= 0 (or NaN) filter nothing;
  *            top_p <= 0 leaves the first token.
  *   ids      dev int32 [B] out;  probs  dev float [B] out
- *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes (0 for some
- *            sizes: it may then be null), on a 16-byte boundary; calls that may
- *            overlap need separate ones
+ *   workspace dev, at least lora_sample_workspace_bytes(B, V) bytes of the call's
+ *            own sizes (0 for some, also for larger batches than need one: it may
+ *            then be null), on a 16-byte boundary; calls that may overlap need
+ *            separate ones
  * Tokens whose logit is NaN or -infinity are never drawn; where there is no
  * other, ids[b] = -1 and probs[b] = 0. Among logits of +infinity all weigh the
  * same, and nothing else does. Weights are 64-bit exponentials, rounded to
  * whole numbers of 2^-shift (shift = 46 up to 65536 tokens, then 62 less the
- * bits of V - 1; a token that weighs under half of one is not drawn); their sums are exact, so equal inputs give equal bits.
+ * bits of V - 1; a token that weighs at most half of one is not drawn). Their
+ * sums are exact, so equal inputs give equal bits.
  * 1 <= V <= LORA_SAMPLE_MAX_VOCAB, B <= LORA_SAMPLE_MAX_BATCH. Asynchronous on
  * `stream`. Errors: LORA_EINVAL (sizes, unknown dtype, null, misaligned or
  * equal pointers), LORA_ESPACE, LORA_EHIP. B == 0 launches nothing.
